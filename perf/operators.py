@@ -3,7 +3,8 @@ mixture-of-experts router, the whole mixture-of-experts layer on packed uint4
 experts, and the low-rank adapters of many requests beside a shared projection.
 
 `run` computes a case either in plain torch operations in fp32 (`own` false) or
-through the library's entry points (`own` true), on the same prepared inputs.
+through the library's entry points (`own` true), on the same prepared inputs; the
+library's result buffers and workspace are kept from step to step, as a serving loop does.
 `exact` is the definition in fp64.
 """
 import math
@@ -104,6 +105,12 @@ def _rank_of(case, l):
     return (R, R // 2, R - 3)[l % 3] if case["ranks"] else R
 
 
+def _slots(case):
+    """The ids and weights that a serving loop keeps from step to step."""
+    shape = (case["tokens"], case["k"])
+    return (torch.empty(shape, dtype=torch.int32, device=DEV), torch.empty(shape, dtype=torch.float32, device=DEV))
+
+
 def prepare(case, seed):
     g = _gen(seed)
     st = dict(case=case)
@@ -113,6 +120,7 @@ def prepare(case, seed):
         if own:
             import packed_int4_convrot_amd as ck
             st["ck"] = ck
+            st["slots"] = _slots(case)
     elif case["op"] == "moe":
         T, H, I, E = case["tokens"], case["hidden"], case["inter"], case["experts"]
         st["x"] = torch.randn((T, H), device=DEV, generator=g).to(torch.bfloat16)
@@ -124,6 +132,9 @@ def prepare(case, seed):
             import packed_int4_convrot_amd as ck
             st["ck"] = ck
             st["experts"] = ck.MoeExperts(*st["w1"], *st["w2"])
+            st["slots"] = _slots(case)
+            st["out"] = torch.empty_like(st["x"])
+            st["space"] = torch.empty(ck.moe_workspace_bytes(T, I, E, case["k"]), dtype=torch.uint8, device=DEV)
     else:
         M, K, N, R, L = case["rows"], case["K"], case["N"], case["rank"], case["adapters"]
         st["x"] = torch.randn((M, K), device=DEV, generator=g).to(torch.bfloat16)
@@ -147,6 +158,8 @@ def prepare(case, seed):
             st["ck"] = ck
             st["adapters"] = ck.LoraAdapters(st["a"], st["b"], scaling=st["scaling"],
                                              ranks=st["ranks"] if case["ranks"] else None)
+            st["out"] = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+            st["space"] = torch.empty(ck.lora_workspace_bytes(M, K, R, L), dtype=torch.uint8, device=DEV)
     return st
 
 
@@ -223,10 +236,12 @@ def run(state):
     if own:
         ck = state["ck"]
         if case["op"] == "route":
-            return ck.moe_route(state["logits"], state["k"], renormalize=case["renormalize"])
+            return ck.moe_route(state["logits"], state["k"], case["renormalize"], *state["slots"])
         if case["op"] == "moe":
-            return ck.moe(state["x"], state["logits"], state["experts"], state["k"], renormalize=case["renormalize"])
-        return ck.lora_add(state["x"], state["adapters"], state["index"], base=state["base"])
+            return ck.moe(state["x"], state["logits"], state["experts"], state["k"], case["renormalize"],
+                          state["out"], *state["slots"], workspace=state["space"])
+        return ck.lora_add(state["x"], state["adapters"], state["index"], base=state["base"], out=state["out"],
+                           workspace=state["space"])
     if case["op"] == "route":
         return _plain_route(state["logits"], state["k"], case["renormalize"])
     return _plain_moe(state) if case["op"] == "moe" else _plain_lora(state)
