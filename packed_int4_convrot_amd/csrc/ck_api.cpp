@@ -5,82 +5,20 @@
 #include "../../include/ck.h"
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <cstring>
-#include <string>
 
+#include "api_check.h"
 #include "launch.h"
 
 namespace {
 
-thread_local std::string g_last_error;
+using namespace ck::api;
 
-int fail(int status, const char *fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return status;
-}
-
-int ok()
-{
-    g_last_error.clear();
-    return CK_OK;
-}
-
-int hip_status(int e, const char *what)
-{
-    if (e != 0)
-        return fail(CK_ERR_HIP, "%s: HIP launch failed (hipError_t %d)", what, e);
-    return ok();
-}
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Byte range [lo, hi) spanned by `rows` rows of `cols` elements of `esize`
-// bytes with row stride `ld` elements.
-struct Range {
-    uintptr_t lo = 0, hi = 0;
-};
-Range span(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t esize)
-{
-    Range r;
-    if (!p || rows <= 0 || cols <= 0)
-        return r;
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    r.hi = r.lo + (uintptr_t)(((rows - 1) * ld + cols) * esize);
-    return r;
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
-
-constexpr int64_t kMaxK = 32768;
 // Row strides of codes and packed weights, in bytes: the tiled GEMM addresses
 // a block's 256 rows with 32-bit buffer offsets.
 constexpr int64_t kMaxLd = int64_t(1) << 23;
-// A launch covers at most 2^32 - 1 work-items per grid dimension.  Rotate-quant
-// and the weight producer launch one workgroup of up to 1024 threads per row,
-// so the rows stay below 2^22: (2^22 - 1) * 1024 = 2^32 - 1024 work-items.
-constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;
 // The tiled GEMM launches one 512-thread workgroup per 256 x 256 (or
 // 128 x 256) output tile.
 constexpr int64_t kMaxGemmTiles = (int64_t(1) << 32) / 512 - 1;
-
-int check_k(const char *fn, int64_t K)
-{
-    if (K <= 0)
-        return fail(CK_ERR_INVALID_ARG, "%s: K must be positive (got %lld)", fn, (long long)K);
-    if (K % 64 != 0)
-        return fail(CK_ERR_INVALID_ARG, "%s: K must be a multiple of 64 (got %lld)", fn, (long long)K);
-    if (K > kMaxK)
-        return fail(CK_ERR_UNSUPPORTED, "%s: K must be at most %lld (got %lld)", fn, (long long)kMaxK,
-                    (long long)K);
-    return CK_OK;
-}
 
 int check_g(const char *fn, int32_t G, int64_t K)
 {
@@ -88,27 +26,6 @@ int check_g(const char *fn, int32_t G, int64_t K)
         return fail(CK_ERR_UNSUPPORTED, "%s: rotation group G must be 16, 64 or 256 (got %d)", fn, G);
     if (K % G != 0)
         return fail(CK_ERR_INVALID_ARG, "%s: K (%lld) is not a multiple of G (%d)", fn, (long long)K, G);
-    return CK_OK;
-}
-
-int check_m(const char *fn, int64_t M)
-{
-    if (M < 0)
-        return fail(CK_ERR_INVALID_ARG, "%s: M must be >= 0 (got %lld)", fn, (long long)M);
-    if (M > kMaxRows)
-        return fail(CK_ERR_UNSUPPORTED, "%s: M above %lld", fn, (long long)kMaxRows);
-    return CK_OK;
-}
-
-int check_x(const char *fn, const uint16_t *x, int64_t K, int64_t ldx)
-{
-    if (!x)
-        return fail(CK_ERR_INVALID_ARG, "%s: x is NULL", fn);
-    if (ldx < K || ldx % 8 != 0)
-        return fail(CK_ERR_INVALID_ARG, "%s: ldx (%lld) must be >= K and a multiple of 8", fn,
-                    (long long)ldx);
-    if (!aligned(x, 16))
-        return fail(CK_ERR_INVALID_ARG, "%s: x must be 16-byte aligned", fn);
     return CK_OK;
 }
 
@@ -172,30 +89,6 @@ Range scales_span(const Weights &w, int64_t K)
         return span(w.scales, K / 64, w.N, w.N, 2);
     return span(w.scales, 1, w.N, w.N, 2);
 }
-
-// Outputs are written with 16-byte stores: 16-byte aligned rows.
-int check_out(const char *fn, const void *out, int64_t N, int64_t ldo, size_t esize)
-{
-    if (!out)
-        return fail(CK_ERR_INVALID_ARG, "%s: output is NULL", fn);
-    const int64_t per16 = 16 / (int64_t)esize;
-    if (ldo < N || ldo % per16 != 0)
-        return fail(CK_ERR_INVALID_ARG, "%s: output stride (%lld) must be >= N and a multiple of %lld",
-                    fn, (long long)ldo, (long long)per16);
-    if (!aligned(out, 16))
-        return fail(CK_ERR_INVALID_ARG, "%s: output must be 16-byte aligned", fn);
-    return CK_OK;
-}
-
-#define CK_TRY(expr)            \
-    do {                        \
-        int _st = (expr);       \
-        if (_st != CK_OK)       \
-            return _st;         \
-    } while (0)
-
-constexpr size_t kWsAlign = 256;
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Whole-linear workspace: the int8 codes of M rows padded to a multiple of 16
 // (the tiled layout of the few-row kernel fills whole 16-row tiles), then the
@@ -714,7 +607,7 @@ extern "C" {
 
 const char *ck_status_str(ck_status status) { return status_str_impl(status); }
 
-const char *ck_last_error_msg(void) { return g_last_error.c_str(); }
+const char *ck_last_error_msg(void) { return g_last_error; }
 
 const char *ck_version(void) { return "ck 0.2 gfx950"; }
 
