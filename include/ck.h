@@ -317,6 +317,107 @@ ck_status ck_quantize_weights(const uint16_t *w, int64_t N, int64_t K, int64_t l
                         int32_t scale_kind, uint8_t *packed, int64_t ldp, uint16_t *scales,
                         void *stream);
 
+/*
+ * ------------------------------------------------- weights chosen row by row
+ * Two operators for serving next to the linears above: a mixture-of-experts
+ * layer on packed uint4 experts for few tokens, and low-rank adapters of many
+ * requests beside a shared projection.  Forward only, like the linears.
+ */
+
+/* Router logit kinds. */
+typedef enum { CK_LOGITS_F32 = 0, CK_LOGITS_BF16 = 1 } ck_logit_kind;
+
+/*
+ * ck_moe_route
+ * Top-k routing of T tokens over E experts:
+ *   ids[t, :]     the experts of the k largest logits, descending, ties to the
+ *                 lowest expert (-0 ties with +0; NaN counts as -inf);
+ *   weights[t, j] e_j / sum e, e_j = exp(l_j - max l), the sum over the chosen
+ *                 experts (renormalize != 0) or over all E (0).
+ * A logit of -inf is never chosen: a token with fewer than k other logits has
+ * id -1 and weight 0 in its last slots, and a token without any in all of them.
+ * Where the maximum is +inf, the +inf logits share the weight.
+ *   logits   fp32 or bf16 [T, ldl] (ck_logit_kind), ldl >= E
+ *   ids      int32 [T, k], weights fp32 [T, k]
+ * 1 <= E <= 1024, 1 <= k <= 32 (CK_ERR_UNSUPPORTED above); k may exceed E.
+ */
+ck_status ck_moe_route(const void *logits, int32_t logit_kind, int64_t T, int64_t E, int64_t ldl, int32_t k,
+                       int32_t renormalize, int32_t *ids, float *weights, void *stream);
+
+/* Bytes of workspace ck_moe_w4a16 / ck_moe_experts_w4a16 need for T tokens, inner
+ * width I, E experts and k slots a token: the routing plan and the hidden
+ * activations of one pass (1024 (token, slot) pairs; more tokens run as several
+ * passes over the same workspace).  0 for sizes the entry points refuse. */
+size_t ck_moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int32_t k);
+
+/*
+ * ck_moe_w4a16  [AWQ]
+ * Whole mixture-of-experts layer for few tokens: ck_moe_route, then
+ *   h      = silu(W1[e][0:I] x_t) * (W1[e][I:2I] x_t)
+ *   out[t] = sum_j weights[t, j] * W2[ids[t, j]] h
+ * with W[n, c] = (q - 8) * s[c/Gw, n] + z[c/Gw, n] as in ck_w4a16_gemv (kept
+ * exact), fp32 sums throughout (h is held to 16 significant bits between the
+ * two products) and one rounding to bf16.  A token without experts gets zeros.
+ *   x       bf16 [T, ldx], H columns
+ *   logits  as in ck_moe_route; ids, weights: its results (written)
+ *   w1      uint8 [E, 2I, H/2] packed as in ck_w4_gemm_q: I gate rows, then I up
+ *           rows; s1, z1 bf16 [E, H/Gw, 2I]
+ *   w2      uint8 [E, H, I/2]; s2, z2 bf16 [E, I/Gw, H]
+ *           dense, each 16-byte aligned; z1 and z2 may be NULL (zeros)
+ *   out     bf16 [T, ldo], H columns
+ *   ws      device workspace of at least ck_moe_workspace_bytes(T, I, E, k)
+ *           bytes, 256-byte aligned (CK_ERR_WORKSPACE otherwise); scratch
+ * H % 64 == 0, I % 64 == 0 (CK_ERR_INVALID_ARG); H, I <= 32768, E <= 1024,
+ * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0; every pass of 1024 / k
+ * tokens reads its experts' weights anew.  A non-finite x or h reaches only its own token's
+ * row (as NaN where the weights' offsets cancel).
+ */
+ck_status ck_moe_w4a16(const uint16_t *x, int64_t T, int64_t H, int64_t ldx, const void *logits, int32_t logit_kind,
+                       int64_t ldl, int32_t k, int32_t renormalize, int64_t E, int64_t I, int32_t Gw,
+                       const uint8_t *w1, const uint16_t *s1, const uint16_t *z1, const uint8_t *w2,
+                       const uint16_t *s2, const uint16_t *z2, uint16_t *out, int64_t ldo, int32_t *ids,
+                       float *weights, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ck_moe_experts_w4a16
+ * ck_moe_w4a16 from given ids and weights (any routing rule): int32 [T, k] and
+ * fp32 [T, k], read only.  An id outside [0, E) is an empty slot; a token may
+ * name an expert more than once.
+ */
+ck_status ck_moe_experts_w4a16(const uint16_t *x, int64_t T, int64_t H, int64_t ldx, const int32_t *ids,
+                               const float *weights, int32_t k, int64_t E, int64_t I, int32_t Gw, const uint8_t *w1,
+                               const uint16_t *s1, const uint16_t *z1, const uint8_t *w2, const uint16_t *s2,
+                               const uint16_t *z2, uint16_t *out, int64_t ldo, void *ws, size_t ws_bytes,
+                               void *stream);
+
+/* Bytes of workspace ck_lora_add needs (fp32 [parts, M, R], the number of parts
+ * chosen by the sizes).  0 for sizes it refuses. */
+size_t ck_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
+
+/*
+ * ck_lora_add  [SD]
+ * Low-rank adapters of many requests beside a shared projection (packed
+ * weights cannot hold a merged adapter, so it runs at run time): with l = index[m],
+ *   out[m] = base[m] + scaling[l] * B_l[:, :r] (A_l[:r] x[m]),  r = ranks[l],
+ * and out[m] = base[m] where l is outside [0, L).  fp32 sums (A x is held to 16
+ * significant bits between the products), one rounding to bf16.
+ *   x       bf16 [M, ldx], K columns; index int32 [M]
+ *   a, b    bf16 [L, R, K] and [L, N, R], dense, 16-byte aligned: slots of L
+ *           adapters of up to R ranks
+ *   scaling fp32 [L] or NULL (1); ranks int32 [L] or NULL (R), clamped to [0, R];
+ *           what a slot holds beyond its rank is not used
+ *   base    bf16 [M, ldb], N columns: the projection's result; NULL for zeros;
+ *           may be out itself (same stride), which adds in place
+ *   out     bf16 [M, ldo], N columns
+ *   ws      at least ck_lora_workspace_bytes(M, K, R, L) bytes, 256-byte aligned
+ * K % 64 == 0, R % 8 == 0 (CK_ERR_INVALID_ARG); K <= 32768, R <= 256, N % 16
+ * == 0, ceil(M / 64) * ceil(N / 128) < 2^22 (CK_ERR_UNSUPPORTED).
+ */
+ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const int32_t *index, int64_t L,
+                      int64_t R, const uint16_t *a, const uint16_t *b, const float *scaling, const int32_t *ranks,
+                      int64_t N, const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo, void *ws,
+                      size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- test hooks
  * Same device code paths as above with a debug epilogue, so that each stage
  * can be compared exactly with the oracle. */

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libck.so")
 
 CK_OK, CK_ERR_INVALID_ARG, CK_ERR_UNSUPPORTED, CK_ERR_WORKSPACE, CK_ERR_HIP = range(5)
 CK_WS_PER_CHANNEL, CK_WS_PER_GROUP = 0, 1
+CK_LOGITS_F32, CK_LOGITS_BF16 = 0, 1
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -56,6 +57,15 @@ SIGNATURES = {
     "ck_test_gemm_i32_a4": ([_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _i64, _p], ctypes.c_int),
     "ck_test_linear_mfma_one_launch": ([_i32, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _i32, _i32, _i64, _p,
                                         _f32, _p, _i64, _p], ctypes.c_int),
+    "ck_moe_route": ([_p, _i32, _i64, _i64, _i64, _i32, _i32, _p, _p, _p], ctypes.c_int),
+    "ck_moe_workspace_bytes": ([_i64, _i64, _i64, _i32], _sz),
+    "ck_moe_w4a16": ([_p, _i64, _i64, _i64, _p, _i32, _i64, _i32, _i32, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p,
+                      _p, _i64, _p, _p, _p, _sz, _p], ctypes.c_int),
+    "ck_moe_experts_w4a16": ([_p, _i64, _i64, _i64, _p, _p, _i32, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p, _p, _i64,
+                              _p, _sz, _p], ctypes.c_int),
+    "ck_lora_workspace_bytes": ([_i64, _i64, _i64, _i64], _sz),
+    "ck_lora_add": ([_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _sz, _p],
+                    ctypes.c_int),
 }
 
 
@@ -419,3 +429,188 @@ def accumulators_i32(codes, packed):
     _check(lib.ck_test_gemm_i32(_ptr(codes), _ld(codes), M, K, _ptr(packed), _ld(packed), N,
                                 _ptr(acc), _ld(acc), _stream(codes)))
     return acc
+
+
+# ----------------------------------------------- weights chosen row by row
+# These run many times a decode step, where the call itself costs as much as the
+# kernels: the weights are checked once, when their handle is made.
+
+_LOGIT_KIND = {torch.float32: CK_LOGITS_F32, torch.bfloat16: CK_LOGITS_BF16}
+
+
+def _rows(t, name, dtype, device, shape):
+    """Row stride of a matrix of exactly this shape, dtype and device with unit column stride."""
+    if t.dtype is not dtype or t.device != device or tuple(t.shape) != shape:
+        raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)"
+                         % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+    ld, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if shape[0] <= 1:
+        return max(ld, shape[1])
+    if ld < shape[1]:
+        raise ValueError("%s has row stride %d below its row length %d (expanded or overlapping rows)"
+                         % (name, ld, shape[1]))
+    return ld
+
+
+def _flat(t, name, dtype, device, shape):
+    """Pointer of a contiguous tensor of exactly this shape, dtype and device."""
+    if t.dtype is not dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
+    return t.data_ptr()
+
+
+def _logits(logits):
+    """(kind, row stride) of a [T, E] GPU matrix of router logits."""
+    kind = _LOGIT_KIND.get(logits.dtype)
+    if kind is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D fp32 or bf16 GPU tensor")
+    return kind, _rows(logits, "logits", logits.dtype, logits.device, tuple(logits.shape))
+
+
+def _space(workspace, need, device):
+    """A workspace tensor of at least `need` bytes."""
+    if workspace is None:
+        return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+    if workspace.dtype is not torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
+            or workspace.device != device:
+        raise ValueError("workspace must be a contiguous 1-D uint8 tensor on %s" % device)
+    return workspace
+
+
+def _slots(ids, weights, T, k, device):
+    ids = torch.empty((T, k), dtype=torch.int32, device=device) if ids is None else ids
+    weights = torch.empty((T, k), dtype=torch.float32, device=device) if weights is None else weights
+    return ids, weights
+
+
+def moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None):
+    """Top-k routing of fp32 or bf16 logits [T, E]: int32 ids and fp32 softmax weights [T, k],
+    descending, ties to the lowest expert; -inf (and NaN) logits are never chosen (id -1,
+    weight 0).  renormalize: weights over the chosen experts sum to 1."""
+    kind, ldl = _logits(logits)
+    T, E = logits.shape
+    dev = logits.device
+    ids, weights = _slots(ids, weights, T, k, dev)
+    _check(lib.ck_moe_route(logits.data_ptr(), kind, T, E, ldl, k, 1 if renormalize else 0,
+                            _flat(ids, "ids", torch.int32, dev, (T, k)),
+                            _flat(weights, "weights", torch.float32, dev, (T, k)), _stream(logits)))
+    return ids, weights
+
+
+def moe_workspace_bytes(T: int, I: int, E: int, k: int) -> int:
+    """Workspace bytes of moe and moe_experts for T tokens, inner width I, E experts, k slots."""
+    return int(lib.ck_moe_workspace_bytes(T, I, E, k))
+
+
+class MoeExperts:
+    """The packed uint4 weights of a mixture-of-experts layer (AWQ W4A16, group 64):
+    w1 uint8 [E, 2I, H/2] (I gate rows, then I up rows), s1 and z1 bf16 [E, H/64, 2I],
+    w2 uint8 [E, H, I/2], s2 and z2 bf16 [E, I/64, H]; the zero points may be None.
+    The tensors are kept, not copied."""
+
+    def __init__(self, w1, s1, z1, w2, s2, z2):
+        if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or not isinstance(w2, torch.Tensor) or w2.dim() != 3:
+            raise ValueError("w1 and w2 must be 3-D tensors")
+        E, H, I = w1.shape[0], 2 * w1.shape[2], w1.shape[1] // 2
+        if w1.shape[1] % 2 or H <= 0 or I <= 0 or H % 64 or I % 64:
+            raise ValueError("w1 has shape %s: expected [E, 2I, H/2] with H and I multiples of 64" % (tuple(w1.shape),))
+        for name, t, shape in (("w1", w1, (E, 2 * I, H // 2)), ("w2", w2, (E, H, I // 2))):
+            if t.dtype not in (torch.uint8, torch.int8):
+                raise ValueError("%s must be uint8 or int8" % name)
+            _dense(t, name, t.dtype, shape)
+        for name, t, shape in (("s1", s1, (E, H // 64, 2 * I)), ("z1", z1, (E, H // 64, 2 * I)),
+                               ("s2", s2, (E, I // 64, H)), ("z2", z2, (E, I // 64, H))):
+            if t is None and name[0] == "z":
+                continue
+            _dense(t, name, torch.bfloat16, shape)
+        _same_device(w1, ("s1", s1), ("z1", z1), ("w2", w2), ("s2", s2), ("z2", z2))
+        self.tensors = (w1, s1, z1, w2, s2, z2)
+        self.E, self.H, self.I, self.device = E, H, I, w1.device
+        self._args = (E, I, 64) + tuple(None if t is None else t.data_ptr() for t in self.tensors)
+
+
+def _moe_buffers(x, experts, k, out, workspace):
+    T = x.shape[0]
+    ldx = _rows(x, "x", torch.bfloat16, experts.device, (T, experts.H))
+    out = torch.empty((T, experts.H), dtype=torch.bfloat16, device=experts.device) if out is None else out
+    ldo = _rows(out, "out", torch.bfloat16, experts.device, (T, experts.H))
+    workspace = _space(workspace, lib.ck_moe_workspace_bytes(T, experts.I, experts.E, k) if workspace is None else 0,
+                       experts.device)
+    return T, ldx, out, ldo, workspace
+
+
+def moe(x, logits, experts: MoeExperts, k: int, renormalize: bool = True, out=None, ids=None, weights=None,
+        workspace=None):
+    """Whole mixture-of-experts layer on packed experts, for few tokens: routes bf16 x [T, H]
+    by logits [T, E] as moe_route and returns (out bf16 [T, H], ids, weights) with
+    out[t] = sum_j weights[t, j] W2[e] (silu(W1[e][:I] x) * (W1[e][I:] x)), e = ids[t, j]."""
+    kind, ldl = _logits(logits)
+    T, ldx, out, ldo, workspace = _moe_buffers(x, experts, k, out, workspace)
+    dev = experts.device
+    if logits.shape != (T, experts.E) or logits.device != dev:
+        raise ValueError("logits must have shape (%d, %d) on %s" % (T, experts.E, dev))
+    ids, weights = _slots(ids, weights, T, k, dev)
+    _check(lib.ck_moe_w4a16(x.data_ptr(), T, experts.H, ldx, logits.data_ptr(), kind, ldl, k, 1 if renormalize else 0,
+                            *experts._args, out.data_ptr(), ldo, _flat(ids, "ids", torch.int32, dev, (T, k)),
+                            _flat(weights, "weights", torch.float32, dev, (T, k)), workspace.data_ptr(),
+                            workspace.numel(), _stream(x)))
+    return out, ids, weights
+
+
+def moe_experts(x, ids, weights, experts: MoeExperts, out=None, workspace=None):
+    """The experts' part of moe from given int32 ids and fp32 weights [T, k] (an id outside
+    [0, E) is an empty slot): out bf16 [T, H]."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be a 2-D tensor")
+    k = ids.shape[1]
+    T, ldx, out, ldo, workspace = _moe_buffers(x, experts, k, out, workspace)
+    dev = experts.device
+    _check(lib.ck_moe_experts_w4a16(x.data_ptr(), T, experts.H, ldx, _flat(ids, "ids", torch.int32, dev, (T, k)),
+                                    _flat(weights, "weights", torch.float32, dev, (T, k)), k, *experts._args,
+                                    out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _stream(x)))
+    return out
+
+
+class LoraAdapters:
+    """L slots of low-rank adapters of up to R ranks: a bf16 [L, R, K], b bf16 [L, N, R],
+    scaling fp32 [L] or None (1), ranks int32 [L] or None (R); what a slot holds beyond its
+    rank is not used.  The tensors are kept, not copied."""
+
+    def __init__(self, a, b, scaling=None, ranks=None):
+        if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
+            raise ValueError("a and b must be 3-D tensors")
+        (L, R, K), N = a.shape, b.shape[1]
+        _dense(a, "a", torch.bfloat16, (L, R, K))
+        _dense(b, "b", torch.bfloat16, (L, N, R))
+        if scaling is not None:
+            _dense(scaling, "scaling", torch.float32, (L,))
+        if ranks is not None:
+            _dense(ranks, "ranks", torch.int32, (L,))
+        _same_device(a, ("b", b), ("scaling", scaling), ("ranks", ranks))
+        self.tensors = (a, b, scaling, ranks)
+        self.L, self.R, self.K, self.N, self.device = L, R, K, N, a.device
+        self._args = (L, R) + tuple(None if t is None else t.data_ptr() for t in self.tensors) + (N,)
+
+
+def lora_workspace_bytes(M: int, K: int, R: int, L: int) -> int:
+    """Workspace bytes of lora_add for M rows of K columns and L adapters of up to R ranks."""
+    return int(lib.ck_lora_workspace_bytes(M, K, R, L))
+
+
+def lora_add(x, adapters: LoraAdapters, index, base=None, out=None, workspace=None):
+    """bf16 [M, N]: base[m] + scaling[l] B_l (A_l x[m]) with l = index[m] (int32 [M]), and base[m]
+    where l is outside [0, L).  base None: zeros; out may be base (in place)."""
+    M, dev = x.shape[0], adapters.device
+    ldx = _rows(x, "x", torch.bfloat16, dev, (M, adapters.K))
+    shape = (M, adapters.N)
+    out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    ldo = _rows(out, "out", torch.bfloat16, dev, shape)
+    ldb = ldo if base is None else _rows(base, "base", torch.bfloat16, dev, shape)
+    workspace = _space(workspace, lib.ck_lora_workspace_bytes(M, adapters.K, adapters.R, adapters.L)
+                       if workspace is None else 0, dev)
+    _check(lib.ck_lora_add(x.data_ptr(), M, adapters.K, ldx, _flat(index, "index", torch.int32, dev, (M,)),
+                           *adapters._args, None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
+                           workspace.data_ptr(), workspace.numel(), _stream(x)))
+    return out

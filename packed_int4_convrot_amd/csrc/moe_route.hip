@@ -1,0 +1,67 @@
+// Mixture-of-experts router: top-k of each token's logits, one wave a token.
+// ids descending by logit, ties to the lowest expert; weights exp(l - max) over
+// their sum (of the chosen, or of all experts), fp32.  Bound by launch latency
+// for few tokens and by reading the logits once for many.
+#include "moe_route.h"
+#include "rows_launch.h"
+
+namespace ck {
+namespace {
+
+constexpr int kTokensPerBlock = 4;
+
+template <int kNe, bool kBf16>
+__global__ __launch_bounds__(kTokensPerBlock * kWave) void moe_route_kernel(
+    const void *__restrict__ logits, int64_t T, int E, int64_t ldl, int k, bool renormalize,
+    int32_t *__restrict__ ids, float *__restrict__ weights)
+{
+    const int lane = threadIdx.x % kWave;
+    const int64_t t = (int64_t)blockIdx.x * kTokensPerBlock + threadIdx.x / kWave;
+    if (t >= T)
+        return;
+    const void *row = static_cast<const uint8_t *>(logits) + t * ldl * (kBf16 ? 2 : 4);
+    int id;
+    float w;
+    route_row<kNe, kBf16>(row, E, k, renormalize, lane, id, w);
+    if (lane < k) {
+        ids[t * k + lane] = id;
+        weights[t * k + lane] = w;
+    }
+}
+
+template <bool kBf16>
+void launch_kind(const void *logits, int64_t T, int E, int64_t ldl, int k, bool renormalize, int32_t *ids,
+                 float *weights, hipStream_t s)
+{
+    const dim3 grid((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock)), block(kTokensPerBlock * kWave);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, s, logits, T, E, ldl, k, renormalize, ids, weights);
+    };
+    if (E <= 64)
+        go(moe_route_kernel<1, kBf16>);
+    else if (E <= 128)
+        go(moe_route_kernel<2, kBf16>);
+    else if (E <= 256)
+        go(moe_route_kernel<4, kBf16>);
+    else
+        go(moe_route_kernel<16, kBf16>);
+}
+
+}  // namespace
+
+int launch_moe_route(const void *logits, bool bf16, int64_t T, int E, int64_t ldl, int k, bool renormalize,
+                     int32_t *ids, float *weights, void *stream)
+{
+    if (T <= 0)
+        return 0;
+    if (E < 1 || E > kRouteMaxExperts || k < 1 || k > kRouteMaxK)
+        return (int)hipErrorInvalidValue;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (bf16)
+        launch_kind<true>(logits, T, E, ldl, k, renormalize, ids, weights, s);
+    else
+        launch_kind<false>(logits, T, E, ldl, k, renormalize, ids, weights, s);
+    return (int)hipGetLastError();
+}
+
+}  // namespace ck

@@ -1,0 +1,76 @@
+// Internal launch interface of the operators that choose weights row by row
+// (the mixture-of-experts layer and the low-rank adapters), between
+// ck_rows_api.cpp and their kernels.  Arguments were validated by the caller;
+// each launcher returns the hipError_t of its launches as an int (0 = success).
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ck {
+
+// ---- router -------------------------------------------------------------
+constexpr int kRouteMaxExperts = 1024;  // 16 logits per lane of a wave
+constexpr int kRouteMaxK = 32;
+int launch_moe_route(const void *logits, bool bf16, int64_t T, int E, int64_t ldl, int k, bool renormalize,
+                     int32_t *ids, float *weights, void *stream);
+
+// ---- experts ------------------------------------------------------------
+// One pass takes at most kMoePairs (token, slot) pairs; more tokens run as
+// several passes over the same workspace.
+constexpr int kMoePairs = 1024;
+// Workspace of one pass of P pairs over E experts of inner width I:
+//   ints: [0] number of chosen experts A, [4 ..] A records {expert, first, count, 0}
+//   (int4), then P pair numbers sorted by expert; then the hidden activations.
+inline int64_t moe_plan_records(int64_t E, int64_t P) { return E < P ? E : P; }
+inline int64_t moe_plan_bytes(int64_t E, int64_t P)
+{
+    return ((4 + 4 * moe_plan_records(E, P) + P) * 4 + 255) / 256 * 256;
+}
+inline int64_t moe_hidden_bytes(int64_t P, int64_t I) { return P * I * 4; }
+
+struct MoeExperts {
+    const uint8_t *w1;          // [E, 2 I, H / 2]: I gate rows, then I up rows
+    const uint16_t *s1, *z1;    // [E, H / 64, 2 I]; z1 may be null
+    const uint8_t *w2;          // [E, H, I / 2]
+    const uint16_t *s2, *z2;    // [E, I / 64, H]; z2 may be null
+    int E, H, I;
+};
+// logits null: ids and weights are inputs; otherwise they are written.
+struct MoeRouting {
+    const void *logits;
+    bool bf16, renormalize;
+    int64_t ldl;
+    int k;
+    int32_t *ids;
+    float *weights;
+};
+// One pass: T * k <= kMoePairs, T >= 1.
+int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const MoeExperts &w, uint16_t *out,
+               int64_t ldo, void *ws, void *stream);
+
+// ---- low-rank adapters --------------------------------------------------
+constexpr int kLoraWindow = 64;     // rows that share one look at the adapter indices
+constexpr int kLoraMaxRank = 256;
+constexpr int64_t kLoraPerRowMax = 256;  // rows up to which a workgroup is started per row
+constexpr int kLoraRankBlock = 64;
+inline int64_t lora_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// Parts the K columns are split into, so that few rows still fill the chip.
+inline int lora_splits(int64_t M, int64_t K, int64_t R, int64_t L)
+{
+    // About one workgroup for each of the 256 CUs; a wave keeps a 64-column
+    // group at least, and the second product adds at most 16 parts.
+    const bool per_row = M <= kLoraPerRowMax;
+    const int64_t groups = K / 64, waves = per_row ? 4 : 8;
+    const int64_t sets = per_row ? (M < L * lora_ceil(M, kLoraWindow) ? M : L * lora_ceil(M, kLoraWindow))
+                                 : lora_ceil(M, 32);
+    int64_t s = 256 / (sets * lora_ceil(R, kLoraRankBlock));
+    const int64_t most = groups / waves < 16 ? groups / waves : 16;
+    s = s > most ? most : s;
+    return (int)(s < 1 ? 1 : s);
+}
+int launch_lora(const uint16_t *x, int64_t M, int K, int64_t ldx, const int32_t *index, int64_t L, int R,
+                const uint16_t *a, const uint16_t *b, const float *scaling, const int32_t *ranks, int N,
+                const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo, float *ws, void *stream);
+
+}  // namespace ck
