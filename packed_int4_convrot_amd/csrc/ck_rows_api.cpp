@@ -60,16 +60,30 @@ int ck_moe_route_impl(const void *logits, int32_t kind, int64_t T, int64_t E, in
                       fn);
 }
 
-// Tokens of one pass: as many whole tokens as its pairs hold.
-int64_t moe_pass_tokens(int64_t T, int32_t k) { return T * k <= ck::kMoePairs ? T : ck::kMoePairs / k; }
+// The workspace of T tokens holds P pairs at H <= 8192; a wider layer takes fewer
+// tokens a pass (one at least: k <= 32 pairs of H <= 32768 need four times k pairs' room).
+int64_t moe_room_pairs(int64_t T, int32_t k)
+{
+    const int64_t most = ck::kMoePairs / k * k, P = T * k < most ? T * k : most;
+    return P < 4 * k ? 4 * k : P;
+}
 
 size_t moe_workspace(int64_t T, int64_t I, int64_t E, int32_t k)
 {
     if (T <= 0 || I <= 0 || E < 1 || E > ck::kRouteMaxExperts || k < 1 || k > ck::kRouteMaxK || I > kMaxK ||
         T > kMaxRows)
         return 0;
-    const int64_t P = moe_pass_tokens(T, k) * k;
-    return (size_t)ck::moe_plan_bytes(E, P) + round_up((size_t)ck::moe_hidden_bytes(P, I), kWsAlign);
+    const int64_t P = moe_room_pairs(T, k);
+    return (size_t)ck::moe_hidden_bytes(P, I) + (size_t)ck::moe_pass_columns(P) * 4;
+}
+
+// Tokens of one pass: the pairs a pass takes, and the results its room holds.
+int64_t moe_pass_tokens(int64_t T, int64_t H, int32_t k)
+{
+    const int64_t by_pairs = ck::kMoePairs / k;
+    const int64_t by_room = ck::moe_pass_columns(moe_room_pairs(T, k)) / H / k;
+    const int64_t n = by_pairs < by_room ? by_pairs : by_room;
+    return T < n ? T : n;
 }
 
 // logits null: ids and weights are inputs.
@@ -129,7 +143,7 @@ int moe_common(const char *fn, const uint16_t *x, int64_t T, int64_t H, int64_t 
     }
 
     const ck::MoeExperts w{w1, s1, z1, w2, s2, z2, (int)E, (int)H, (int)I};
-    const int64_t pass = moe_pass_tokens(T, k);
+    const int64_t pass = moe_pass_tokens(T, H, k);
     for (int64_t t = 0; t < T; t += pass) {
         const int64_t n = T - t < pass ? T - t : pass;
         const ck::MoeRouting r{routed ? static_cast<const uint8_t *>(logits) + t * ldl * logit_size(kind) : nullptr,

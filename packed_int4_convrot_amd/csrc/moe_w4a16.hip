@@ -4,318 +4,376 @@
 //   h = silu(W1[e][:I] x) * (W1[e][I:] x),  y = W2[e] h,
 //   out[t] = sum over the token's slots j of weight_j y_{e_j}.
 //
-// Three launches: the plan (routing, then the (token, slot) pairs sorted by
-// expert), the first product with the gate, the second with the weighted sum.
-// Few tokens make this a matter of streaming the chosen experts' weights once,
-// so every kernel multiplies on the 16 x 16 bf16 MFMA whatever the number of
-// tokens and the weights go straight to registers.  Per 64-column group g,
-//   sum_c x_c W[n, c] = s P + (z - 136 s) X,  P = sum x_c (128 + q_c), X = sum x_c,
-// where bf16(128 + q) costs an and-or per pair of codes, and X comes from an
-// MFMA against ones in the register layout that P has.  Sums are fp32.
+// Few tokens make this a matter of streaming the chosen experts' weights once
+// (w4_stream.h), whatever the number of tokens each has.  Sums are fp32; h goes
+// to the second product as two bf16 (16 significant bits), as two rows of A.
+//
+// Launches, for P = tokens * k (token, slot) pairs:
+//   few pairs:  first product (each workgroup routes its token itself), second
+//               product with the weighted sum: two launches;
+//   otherwise:  router, first product, second product, weighted sum.  Each
+//               workgroup collects its expert's pairs from the ids with ballots.
 #include "moe_route.h"
 #include "rows_launch.h"
+#include "w4_stream.h"
 
 namespace ck {
 namespace {
 
-struct Chosen {
-    int expert, first, count, pad;
+// The expert of unit y of a launch over min(E, P) units, and its pairs in
+// ascending order.  With more experts than pairs, unit y is pair y's expert, if
+// y is the first pair to choose it.  count 0: nothing to do.
+struct Picked {
+    int expert, count;
 };
-__device__ __forceinline__ const Chosen *plan_records(const int *plan)
+__device__ __forceinline__ Picked pick(const int32_t *ids, int P, int E, int y, uint16_t *s_list)
 {
-    return reinterpret_cast<const Chosen *>(plan + 4);
-}
-
-constexpr int kPlanThreads = 1024;
-
-// One workgroup: routes the tokens (a wave each) or reads given ids, then
-// sorts the pairs by expert.  The order of an expert's pairs is that of the
-// LDS atomics; no result depends on it, since a pair's sums do not depend on
-// which row of which tile it takes.
-template <int kNe, bool kBf16, bool kRoute>
-__global__ __launch_bounds__(kPlanThreads) void moe_plan_kernel(const void *__restrict__ logits, int T, int E,
-                                                                int64_t ldl, int k, bool renormalize,
-                                                                int32_t *__restrict__ ids,
-                                                                float *__restrict__ weights,
-                                                                int *__restrict__ plan)
-{
-    __shared__ int s_id[kMoePairs];
-    __shared__ int s_count[kRouteMaxExperts];
-    __shared__ int s_start[kRouteMaxExperts];
-    __shared__ int s_wave[kPlanThreads / kWave];
-    const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
-    const int P = T * k;
-    s_count[t] = 0;
-    if constexpr (kRoute) {
-#pragma unroll 1
-        for (int tok = wave; tok < T; tok += kPlanThreads / kWave) {
-            int id;
-            float w;
-            route_row<kNe, kBf16>(static_cast<const uint8_t *>(logits) + (int64_t)tok * ldl * (kBf16 ? 2 : 4), E, k,
-                                  renormalize, lane, id, w);
-            if (lane < k) {
-                s_id[tok * k + lane] = id;
-                ids[tok * k + lane] = id;
-                weights[tok * k + lane] = w;
-            }
+    const int lane = threadIdx.x % kWave;
+    const bool writes = threadIdx.x < kWave;
+    const int e = E <= P ? y : __builtin_amdgcn_readfirstlane(ids[y]);
+    Picked r{e, 0};
+    if (e < 0 || e >= E)
+        return r;
+    int first = -1;
+    for (int c = 0; c < P; c += kWave) {
+        const int v = c + lane < P ? ids[c + lane] : -1;
+        const uint64_t mask = __ballot(v == e);
+        if (mask) {
+            if (first < 0)
+                first = c + __builtin_ctzll(mask);
+            if (writes && v == e)
+                s_list[r.count + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1))] = (uint16_t)(c + lane);
+            r.count += __builtin_popcountll(mask);
         }
-    } else {
-        if (t < P)
-            s_id[t] = ids[t];
     }
-    __syncthreads();
-    int e = -1, at = 0;
-    if (t < P) {
-        e = s_id[t];
-        if (e < 0 || e >= E)
-            e = -1;
-        else
-            at = atomicAdd(&s_count[e], 1);
-    }
-    __syncthreads();
-    // Exclusive scan over the experts of (chosen, pairs) as two 16-bit halves.
-    const int c = s_count[t];
-    int v = (c > 0 ? 1 << 16 : 0) + c;
-    const int own = v;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int u = __shfl_up(v, d);
-        if (lane >= d)
-            v += u;
-    }
-    if (lane == kWave - 1)
-        s_wave[wave] = v;
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanThreads / kWave; ++w) {
-        if (w < wave)
-            before += s_wave[w];
-        total += s_wave[w];
-    }
-    const int excl = before + v - own;
-    s_start[t] = excl & 0xffff;
-    Chosen *rec = reinterpret_cast<Chosen *>(plan + 4);
-    if (c > 0)
-        rec[excl >> 16] = Chosen{t, excl & 0xffff, c, 0};
-    if (t == 0)
-        plan[0] = total >> 16;
-    __syncthreads();
-    int *pairs = plan + 4 + 4 * min(E, P);
-    if (e >= 0)
-        pairs[s_start[e] + at] = t;
+    if (E > P && first != y)
+        r.count = 0;
+    return r;
 }
 
 // ---------------------------------------------------------------- first product
 
-constexpr int kUpWaves = 4;
-constexpr int kUpAhead = 4;  // groups per load batch
+constexpr int kWaves = 4;
 
-// A workgroup owns 16 hidden columns (16 gate rows and 16 up rows) of one
-// chosen expert; its waves split the H columns and are summed through LDS.
-// Neighbouring column tiles share lines of the scales, so runs of four tiles
-// go to one XCD, and the runs go round the XCDs (the chosen experts come first).
-__global__ __launch_bounds__(kUpWaves * kWave) void moe_up_kernel(
-    const uint16_t *__restrict__ x, int64_t ldx, int k, const uint8_t *__restrict__ w1,
-    const uint16_t *__restrict__ s1, const uint16_t *__restrict__ z1, int H, int I, const int *__restrict__ plan,
-    int records, uint16_t *__restrict__ hidden)
+struct UpArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    int k;
+    const uint8_t *w1;
+    const uint16_t *s1, *z1;
+    int E, H, I, P;
+    MoeRouting r;
+    uint16_t *hidden;         // [P][2][I]: first parts, second parts, in operand order
+};
+
+// silu(g) u of hidden column n of a pair, as two bf16.
+__device__ __forceinline__ void put_hidden(uint16_t *hidden, int pair, int I, int n, float g, float u)
 {
-    __shared__ float s_red[kUpWaves][2][256];
-    const int tiles = I / 16;
-    const int local = blockIdx.x / kXcds;
-    const int unit = (local / 4) * kXcds + blockIdx.x % kXcds;
-    const int a = unit / (tiles / 4), n0 = (unit % (tiles / 4) * 4 + local % 4) * 16;
-    if (a >= plan[0])
+    uint16_t hi, lo;
+    split_bf16(g / (1.f + expf(-g)) * u, hi, lo);
+    uint16_t *dst = hidden + (int64_t)pair * 2 * I + n / 8 * 8 + act_slot8(n % 8);
+    dst[0] = hi;
+    dst[I] = lo;
+}
+
+// Few pairs.  A unit is a pair, routed here (kNe logits a lane) or by the given
+// ids (kNe 0); a workgroup owns 16 hidden columns of it, a wave's tile being
+// their 16 gate and 16 up rows, and the waves split the H columns.
+template <int kNe, bool kBf16>
+__global__ __launch_bounds__(kWaves * kWave) void moe_up_few_kernel(const UpArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // rings, operands, sums
+    __shared__ float s_red[kWaves][32];
+    const int H = p.H, I = p.I, G = H / 64, tiles = I / 16;
+    // Neighbouring tiles share lines of the scales: runs of four go to one XCD.
+    const int local = blockIdx.x / kXcds, run = local / 4 * kXcds + blockIdx.x % kXcds;
+    const int y = run / (tiles / 4), n0 = (run % (tiles / 4) * 4 + local % 4) * 16;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32;
+    if (y >= p.P)
         return;
-    const Chosen ch = plan_records(plan)[a];
-    const int *pairs = plan + 4 + 4 * records;
-
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int l16 = lane % 16, quarter = lane / 16;
-    const int G = H / 64;
-    const int g0 = wave * G / kUpWaves, g1 = (wave + 1) * G / kUpWaves;
-    const uint8_t *wrow[2];
-    const uint16_t *srow[2], *zrow[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int n = j * I + n0 + l16;
-        wrow[j] = w1 + ((int64_t)ch.expert * 2 * I + n) * (H / 2) + 8 * quarter;
-        srow[j] = s1 + (int64_t)ch.expert * G * 2 * I + n;
-        zrow[j] = z1 ? z1 + (int64_t)ch.expert * G * 2 * I + n : nullptr;
+    const int t = y / p.k, slot = y - t * p.k;
+    int e;
+    if constexpr (kNe > 0) {
+        int id;
+        float wt;
+        route_row<kNe, kBf16>(static_cast<const uint8_t *>(p.r.logits) + (int64_t)t * p.r.ldl * (kBf16 ? 2 : 4), p.E,
+                              p.k, p.r.renormalize, lane, id, wt);
+        if (slot == 0 && n0 == 0 && threadIdx.x < p.k) {
+            p.r.ids[t * p.k + lane] = id;
+            p.r.weights[t * p.k + lane] = wt;
+        }
+        e = __builtin_amdgcn_readlane(id, slot);
+    } else {
+        e = __builtin_amdgcn_readfirstlane(p.r.ids[y]);
     }
-    const v8bf ones = bf16_ones();
+    if (e < 0 || e >= p.E)
+        return;
+    const int stages = (G + kStageGroups - 1) / kStageGroups;
+    const int st0 = wave * stages / kWaves, st1 = (wave + 1) * stages / kWaves;
+    const WeightStream ws(p.w1, p.s1, p.z1, e, 2 * I, G, n0, I, smem + wave * kRingBytes);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+        if (st0 + i < st1)
+            ws.issue(st0 + i);
+    uint8_t *operands = smem + kWaves * kRingBytes;
+    float *sums = reinterpret_cast<float *>(operands + H * 2);
+    const uint16_t *x = p.x + (int64_t)t * p.ldx;
+    for (int c = threadIdx.x; c < H / 8; c += kWaves * kWave)
+        put_chunk<1>(operands, sums, 0, c,
+                     __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + c * 8))));
+    __syncthreads();
+    float tot[1] = {0.f};
+    stream_stages<1>(ws, p.z1 != nullptr, st0, st1, st1, 0, ARows<1>{operands, sums}, tot);
+    if (lane < 32)
+        s_red[wave][l32] = tot[0];
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            g += s_red[w][l32], u += s_red[w][l32 + 16];
+        put_hidden(p.hidden, y, I, n0 + l32, g, u);
+    }
+}
 
-    for (int p0 = 0; p0 < ch.count; p0 += 16) {
-        const int pr = pairs[ch.first + min(p0 + l16, ch.count - 1)];
-        const uint16_t *xrow = x + (int64_t)(pr / k) * ldx + 16 * quarter;
-        v4f tot[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        for (int gb = g0; gb < g1; gb += kUpAhead) {
-            u32x2 w[kUpAhead][2];
-            u32x4 xv[kUpAhead][2];
-            uint32_t sv[kUpAhead][2], zv[kUpAhead][2];
+// Otherwise: a workgroup owns 64 hidden columns of one expert, 16 a wave (their
+// gate and up rows), for tiles of kRows of its pairs.
+struct Shared {
+    uint8_t ring[kWaves][kRingBytes];
+    uint8_t operands[kChunkOperands];
+    float sums[kChunkElems / 64];
+    uint16_t list[kMoePairs];
+};
+
+template <int kRows>
+__device__ __forceinline__ void up_tile(const UpArgs &p, const Picked &pk, int p0, int n0, Shared &s)
+{
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
+    const WeightStream ws(p.w1, p.s1, p.z1, pk.expert, 2 * p.I, p.H / 64, n0, p.I, s.ring[wave]);
+    float tot[ARows<kRows>::kRegs];
 #pragma unroll
-            for (int u = 0; u < kUpAhead; ++u) {
-                const int g = min(gb + u, g1 - 1);
+    for (int i = 0; i < ARows<kRows>::kRegs; ++i)
+        tot[i] = 0.f;
+    const auto load = [&](int row, int ch) {
+        const int pr = s.list[min(p0 + row, pk.count - 1)];
+        return __builtin_bit_cast(
+            u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.x + (int64_t)(pr / p.k) * p.ldx + ch * 8)));
+    };
+    stream_rows<kRows, kWaves>(ws, p.z1 != nullptr, true, s.operands, s.sums, load, tot);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    w[u][j] = *reinterpret_cast<const u32x2 *>(wrow[j] + g * 32);
-                    sv[u][j] = srow[j][(int64_t)g * 2 * I];
-                    zv[u][j] = z1 ? zrow[j][(int64_t)g * 2 * I] : 0;
-                    xv[u][j] = *reinterpret_cast<const u32x4 *>(xrow + g * 64 + 8 * j);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUpAhead; ++u) {
-                if (gb + u < g1) {
-                    const v8bf x0 = act_order8(xv[u][0]), x1 = act_order8(xv[u][1]);
-                    const v4f zero = {0.f, 0.f, 0.f, 0.f};
-                    const v4f X = mfma16(x1, ones, mfma16(x0, ones, zero));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const v4f acc = mfma16(x1, w4_bf16_plus128(w[u][j][1]),
-                                               mfma16(x0, w4_bf16_plus128(w[u][j][0]), zero));
-                        const float s = bf16_to_f32(sv[u][j]);
-                        const float zc = __builtin_fmaf(-136.f, s, bf16_to_f32(zv[u][j]));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tot[j][i] = __builtin_fmaf(s, acc[i], __builtin_fmaf(zc, X[i], tot[j][i]));
-                    }
-                }
-            }
-        }
-        __syncthreads();  // the previous tile's sums have been read
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s_red[wave][j][i * kWave + lane] = tot[j][i];
-        __syncthreads();
-        const int row = threadIdx.x / 16, col = threadIdx.x % 16;
-        if (p0 + row < ch.count) {
-            const int at = (row % 4) * kWave + (row / 4) * 16 + col;
-            float g = s_red[0][0][at], u = s_red[0][1][at];
-#pragma unroll
-            for (int w = 1; w < kUpWaves; ++w)
-                g += s_red[w][0][at], u += s_red[w][1][at];
-            const float h = g / (1.f + expf(-g)) * u;
-            uint16_t hi, lo;
-            split_bf16(h, hi, lo);
-            // Per eight columns: 8 first parts, then 8 second parts, in MFMA order.
-            uint16_t *dst = hidden + (int64_t)(ch.first + p0 + row) * 2 * I + (n0 + col) / 8 * 16 + act_slot8(col % 8);
-            dst[0] = hi;
-            dst[8] = lo;
-        }
+    for (int i = 0; i < ARows<kRows>::kRegs; ++i) {
+        const float u = __shfl_xor(tot[i], 16);
+        const int row = i / 4 * 8 + 4 * half + i % 4;
+        if (l32 < 16 && row < kRows && p0 + row < pk.count)
+            put_hidden(p.hidden, s.list[p0 + row], p.I, n0 + l32, tot[i], u);
+    }
+}
+
+__global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    Shared &s = *reinterpret_cast<Shared *>(smem);
+    const int tiles = p.I / 64, y = blockIdx.x / tiles;
+    const Picked pk = pick(p.r.ids, p.P, p.E, y, s.list);
+    if (pk.count == 0)
+        return;
+    __syncthreads();  // list
+    const int n0 = blockIdx.x % tiles * 64 + threadIdx.x / kWave * 16;
+    for (int p0 = 0; p0 < pk.count;) {
+        const int left = pk.count - p0;
+        if (left <= 4)
+            up_tile<4>(p, pk, p0, n0, s), p0 += 4;
+        else if (left <= 8)
+            up_tile<8>(p, pk, p0, n0, s), p0 += 8;
+        else
+            up_tile<16>(p, pk, p0, n0, s), p0 += 16;
     }
 }
 
 // --------------------------------------------------------------- second product
 
-constexpr int kDownWaves = 8;
-constexpr int kDownAhead = 4;
+struct DownArgs {
+    const uint16_t *hidden;
+    const uint8_t *w2;
+    const uint16_t *s2, *z2;
+    int E, H, I, T, k;
+    const int32_t *ids;
+    const float *weights;
+    float *y;                 // [P][H]
+    uint16_t *out;
+    int64_t ldo;
+};
 
-// A workgroup owns 16 output columns of every token.  Its waves take the
-// chosen experts (or slices of the I columns, where there are fewer experts than
-// waves) in turn and leave one sum per pair and slice in LDS; then each output
-// adds its token's slots in order.  A tile is eight pairs: the first parts of
-// h are its rows 0-7, the second parts its rows 8-15, added at the end.
-__global__ __launch_bounds__(kDownWaves * kWave) void moe_down_kernel(
-    const uint16_t *__restrict__ hidden, const uint8_t *__restrict__ w2, const uint16_t *__restrict__ s2,
-    const uint16_t *__restrict__ z2, int H, int I, int T, int k, int E, const int *__restrict__ plan, int records,
-    const int32_t *__restrict__ ids, const float *__restrict__ weights, uint16_t *__restrict__ out, int64_t ldo)
+constexpr int kFewWaves = 8;
+
+// Few pairs: a workgroup owns 32 output columns; its waves take the pairs (or
+// slices of the I columns, where there are fewer pairs than waves), then every
+// output adds its token's slots in order.  A has a pair's first parts in its even
+// rows' place and the second parts in the odd (rows 0 and 4 of the result: the
+// two halves of the wave).
+__global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const DownArgs p)
 {
-    extern __shared__ float s_sum[];  // [slices][pairs][16]
-    const int n0 = xcd_block(blockIdx.x, gridDim.x) * 16;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // rings, operands, group sums, results
+    const int H = p.H, I = p.I, G = I / 64, P = p.T * p.k;
+    const int n0 = xcd_block(blockIdx.x, gridDim.x) * 32;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int l16 = lane % 16, quarter = lane / 16;
-    const int P = T * k, G = I / 64;
-    const int A = plan[0];
-    const int *pairs = plan + 4 + 4 * records;
-    const int slices = A > 0 ? max(1, min(min(kDownWaves / A, kMoePairs / P), G)) : 1;
-    const v8bf ones = bf16_ones();
+    const int l32 = lane % 32, half = lane / 32;
+    const int stages = (G + kStageGroups - 1) / kStageGroups;
+    const int slices = max(1, min(kFewWaves / P, stages));
+    uint8_t *operands = smem + kFewWaves * kRingBytes;                      // [P][2][I]
+    float *sums = reinterpret_cast<float *>(operands + P * I * 4);          // [P][2][G]
+    float *s_sum = sums + 2 * P * G;                                        // [slices][P][32]
 
-    for (int it = wave; it < A * slices; it += kDownWaves) {
-        const int sl = it % slices;
-        const Chosen ch = plan_records(plan)[it / slices];
-        const int g0 = sl * G / slices, g1 = (sl + 1) * G / slices;
-        const uint8_t *wrow = w2 + ((int64_t)ch.expert * H + n0 + l16) * (I / 2) + 8 * quarter;
-        const uint16_t *srow = s2 + (int64_t)ch.expert * G * H + n0 + l16;
-        const uint16_t *zrow = z2 ? z2 + (int64_t)ch.expert * G * H + n0 + l16 : nullptr;
-        for (int p0 = 0; p0 < ch.count; p0 += 8) {
-            const uint16_t *hrow = hidden + (int64_t)(ch.first + min(p0 + l16 % 8, ch.count - 1)) * 2 * I +
-                                   32 * quarter + (l16 >= 8 ? 8 : 0);
-            v4f tot = {0.f, 0.f, 0.f, 0.f};
-            for (int gb = g0; gb < g1; gb += kDownAhead) {
-                u32x2 w[kDownAhead];
-                u32x4 hv[kDownAhead][2];
-                uint32_t sv[kDownAhead], zv[kDownAhead];
+    for (int c = threadIdx.x; c < P * I / 4; c += kFewWaves * kWave)        // 2 P rows of I / 8 chunks
+        put_chunk<1>(operands, sums, 0, c, *reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)c * 8));
+    __syncthreads();
+    for (int it = wave; it < P * slices; it += kFewWaves) {
+        const int pr = it / slices, sl = it % slices;
+        const int e = __builtin_amdgcn_readfirstlane(p.ids[pr]);
+        if (e < 0 || e >= p.E)
+            continue;
+        const int st0 = sl * stages / slices, st1 = (sl + 1) * stages / slices;
+        const WeightStream ws(p.w2, p.s2, p.z2, e, H, G, n0, 16, smem + wave * kRingBytes);
+        wait_lds();  // the ring's last operands have been read
 #pragma unroll
-                for (int u = 0; u < kDownAhead; ++u) {
-                    const int g = min(gb + u, g1 - 1);
-                    w[u] = *reinterpret_cast<const u32x2 *>(wrow + g * 32);
-                    sv[u] = srow[(int64_t)g * H];
-                    zv[u] = z2 ? zrow[(int64_t)g * H] : 0;
-                    hv[u][0] = *reinterpret_cast<const u32x4 *>(hrow + g * 128);
-                    hv[u][1] = *reinterpret_cast<const u32x4 *>(hrow + g * 128 + 16);
-                }
-#pragma unroll
-                for (int u = 0; u < kDownAhead; ++u) {
-                    if (gb + u < g1) {
-                        const v8bf h0 = __builtin_bit_cast(v8bf, hv[u][0]), h1 = __builtin_bit_cast(v8bf, hv[u][1]);
-                        const v4f zero = {0.f, 0.f, 0.f, 0.f};
-                        const v4f X = mfma16(h1, ones, mfma16(h0, ones, zero));
-                        const v4f acc =
-                            mfma16(h1, w4_bf16_plus128(w[u][1]), mfma16(h0, w4_bf16_plus128(w[u][0]), zero));
-                        const float s = bf16_to_f32(sv[u]);
-                        const float zc = __builtin_fmaf(-136.f, s, bf16_to_f32(zv[u]));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tot[i] = __builtin_fmaf(s, acc[i], __builtin_fmaf(zc, X[i], tot[i]));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float y = tot[i] + __shfl_xor(tot[i], 32);
-                const int row = p0 + 4 * quarter + i;
-                if (quarter < 2 && row < ch.count)
-                    s_sum[((int64_t)sl * P + pairs[ch.first + row]) * 16 + l16] = y;
-            }
-        }
+        for (int i = 0; i < kStages; ++i)
+            if (st0 + i < st1)
+                ws.issue(st0 + i);
+        float tot[1] = {0.f};
+        stream_stages<1>(ws, p.z2 != nullptr, st0, st1, st1, 0,
+                         ARows<1>{operands + (2 * pr + l32 / 4 % 2) * I * 2, sums + (2 * pr + half) * G}, tot);
+        const float v = tot[0] + __shfl_xor(tot[0], 32);
+        if (half == 0)
+            s_sum[(sl * P + pr) * 32 + l32] = v;
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < T * 16; o += kDownWaves * kWave) {
-        const int t = o / 16, col = o % 16;
+    for (int o = threadIdx.x; o < p.T * 32; o += kFewWaves * kWave) {
+        const int t = o / 32, col = o % 32;
         float y = 0.f;
-        for (int j = 0; j < k; ++j) {
-            const int p = t * k + j, e = ids[p];
-            if (e >= 0 && e < E) {
-                float v = s_sum[p * 16 + col];
+        for (int j = 0; j < p.k; ++j) {
+            const int pr = t * p.k + j, e = p.ids[pr];
+            if (e >= 0 && e < p.E) {
+                float v = s_sum[pr * 32 + col];
                 for (int sl = 1; sl < slices; ++sl)
-                    v += s_sum[(sl * P + p) * 16 + col];
-                y = __builtin_fmaf(weights[p], v, y);
+                    v += s_sum[(sl * P + pr) * 32 + col];
+                y = __builtin_fmaf(p.weights[pr], v, y);
             }
         }
-        out[(int64_t)t * ldo + n0 + col] = f32_to_bf16(y);
+        p.out[(int64_t)t * p.ldo + n0 + col] = f32_to_bf16(y);
     }
 }
 
-template <bool kBf16>
-void launch_plan(const MoeRouting &r, int T, int E, int *plan, hipStream_t s)
+// Otherwise: a workgroup owns 128 output columns (32 a wave) of one expert and
+// writes the sums of its pairs, which moe_combine_kernel adds.  A's rows are the
+// first parts of a tile's pairs, then the second parts.
+template <int kPairs>
+__device__ __forceinline__ void down_tile(const DownArgs &p, const Picked &pk, int p0, int n0, Shared &s)
 {
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(1), dim3(kPlanThreads), 0, s, r.logits, T, E, r.ldl, r.k, r.renormalize,
-                           r.ids, r.weights, plan);
+    constexpr int kRows = 2 * kPairs, kRegs = ARows<kRows>::kRegs;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
+    const bool live = n0 < p.H;
+    const WeightStream ws(p.w2, p.s2, p.z2, pk.expert, p.H, p.I / 64, live ? n0 : 0, 16, s.ring[wave]);
+    float tot[kRegs];
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i)
+        tot[i] = 0.f;
+    const auto load = [&](int row, int ch) {
+        const int pr = s.list[min(p0 + row % kPairs, pk.count - 1)];
+        return *reinterpret_cast<const u32x4 *>(p.hidden + ((int64_t)pr * 2 + row / kPairs) * p.I + ch * 8);
     };
-    if (!r.logits)
-        go(moe_plan_kernel<1, false, false>);
-    else if (E <= 64)
-        go(moe_plan_kernel<1, kBf16, true>);
-    else if (E <= 128)
-        go(moe_plan_kernel<2, kBf16, true>);
-    else if (E <= 256)
-        go(moe_plan_kernel<4, kBf16, true>);
-    else
-        go(moe_plan_kernel<16, kBf16, true>);
+    stream_rows<kRows, kWaves>(ws, p.z2 != nullptr, live, s.operands, s.sums, load, tot);
+    if (!live)
+        return;
+#pragma unroll
+    for (int i = 0; i < kPairs / 2 || i < 4; ++i) {
+        // kPairs 4: the second parts are the other half of the wave; above, the upper registers.
+        const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[(kRegs / 2 + i) % kRegs];
+        const int at = kPairs == 4 ? i : i / 4 * 8 + 4 * half + i % 4;
+        if (p0 + at < pk.count && (kPairs > 4 || half == i / 2))
+            p.y[(int64_t)s.list[p0 + at] * p.H + n0 + l32] = v;
+    }
+}
+
+__global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    Shared &s = *reinterpret_cast<Shared *>(smem);
+    const int tiles = (p.H + 32 * kWaves - 1) / (32 * kWaves);
+    const Picked pk = pick(p.ids, p.T * p.k, p.E, blockIdx.x / tiles, s.list);
+    if (pk.count == 0)
+        return;
+    __syncthreads();  // list
+    const int n0 = (blockIdx.x % tiles * kWaves + threadIdx.x / kWave) * 32;
+    for (int p0 = 0; p0 < pk.count;) {
+        const int left = pk.count - p0;
+        if (left <= 4)
+            down_tile<4>(p, pk, p0, n0, s), p0 += 4;
+        else if (left <= 8)
+            down_tile<8>(p, pk, p0, n0, s), p0 += 8;
+        else
+            down_tile<16>(p, pk, p0, n0, s), p0 += 16;
+    }
+}
+
+// out[t] = sum over the slots, in order; four columns a thread.
+__global__ __launch_bounds__(256) void moe_combine_kernel(const DownArgs p)
+{
+    const int per = p.H / 4;
+    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (o >= (int64_t)p.T * per)
+        return;
+    const int t = (int)(o / per), n = (int)(o % per) * 4;
+    v4f y = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < p.k; ++j) {
+        const int pr = t * p.k + j, e = p.ids[pr];
+        if (e >= 0 && e < p.E) {
+            const v4f v = *reinterpret_cast<const v4f *>(p.y + (int64_t)pr * p.H + n);
+            const float w = p.weights[pr];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] = __builtin_fmaf(w, v[i], y[i]);
+        }
+    }
+    *reinterpret_cast<u32x2 *>(p.out + (int64_t)t * p.ldo + n) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+}
+
+// More than 64 KiB of dynamic LDS needs the kernel's attribute raised once.
+constexpr int kMaxLds = 150 * 1024;
+template <auto kernel>
+hipError_t allow_lds()
+{
+    static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+    return e;
+}
+
+template <int kNe, bool kBf16>
+hipError_t launch_up_few(const UpArgs &a, hipStream_t s)
+{
+    constexpr auto kernel = moe_up_few_kernel<kNe, kBf16>;
+    const hipError_t e = allow_lds<kernel>();
+    if (e != hipSuccess)
+        return e;
+    const int runs = a.P * (a.I / 64);  // of four workgroups, rounded up to whole rounds of the XCDs
+    const int lds = kWaves * kRingBytes + a.H * 2 + a.H / 16;
+    hipLaunchKernelGGL(kernel, dim3((runs + kXcds - 1) / kXcds * kXcds * 4), dim3(kWaves * kWave), lds, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_up(const UpArgs &a, bool few, int units, hipStream_t s)
+{
+    if (!few) {
+        const hipError_t e = allow_lds<moe_up_kernel>();
+        if (e != hipSuccess)
+            return e;
+        hipLaunchKernelGGL(moe_up_kernel, dim3(units * (a.I / 64)), dim3(kWaves * kWave), sizeof(Shared), s, a);
+        return hipGetLastError();
+    }
+    if (!a.r.logits)
+        return launch_up_few<0, false>(a, s);
+    if (a.E <= 256)
+        return a.r.bf16 ? launch_up_few<4, true>(a, s) : launch_up_few<4, false>(a, s);
+    return a.r.bf16 ? launch_up_few<16, true>(a, s) : launch_up_few<16, false>(a, s);
 }
 
 }  // namespace
@@ -328,20 +386,37 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
         w.I % 64 != 0)
         return (int)hipErrorInvalidValue;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    int *plan = static_cast<int *>(ws);
-    const int records = (int)moe_plan_records(w.E, P);
-    uint16_t *hidden = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + moe_plan_bytes(w.E, P));
-    if (r.bf16)
-        launch_plan<true>(r, T, w.E, plan, s);
-    else
-        launch_plan<false>(r, T, w.E, plan, s);
-    const int units = records * (w.I / 64);  // runs of four tiles, rounded up to whole rounds of the XCDs
-    const int blocks = (units + kXcds - 1) / kXcds * kXcds * 4;
-    hipLaunchKernelGGL(moe_up_kernel, dim3(blocks), dim3(kUpWaves * kWave), 0, s, x, ldx, r.k, w.w1, w.s1, w.z1, w.H,
-                       w.I, plan, records, hidden);
-    const int slots = P * kDownWaves < kMoePairs ? P * kDownWaves : kMoePairs;
-    hipLaunchKernelGGL(moe_down_kernel, dim3(w.H / 16), dim3(kDownWaves * kWave), slots * 64, s, hidden, w.w2, w.s2,
-                       w.z2, w.H, w.I, T, r.k, w.E, plan, records, r.ids, r.weights, out, ldo);
+    uint16_t *hidden = static_cast<uint16_t *>(ws);
+    float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + moe_hidden_bytes(P, w.I));
+
+    const int few_lds = kFewWaves * kRingBytes + P * w.I * 4 + 2 * P * (w.I / 64) * 4 +
+                        (P > kFewWaves ? P : kFewWaves) * 32 * 4;
+    const bool few = P <= kMoeFewPairs && few_lds <= kMaxLds;
+    if (r.logits && !few) {
+        const int e = launch_moe_route(r.logits, r.bf16, T, w.E, r.ldl, r.k, r.renormalize, r.ids, r.weights, stream);
+        if (e != 0)
+            return e;
+    }
+    const int units = w.E < P ? w.E : P;
+    const UpArgs ua{x, ldx, r.k, w.w1, w.s1, w.z1, w.E, w.H, w.I, P, r, hidden};
+    hipError_t e = launch_up(ua, few, units, s);
+    if (e != hipSuccess)
+        return (int)e;
+    const DownArgs da{hidden, w.w2, w.s2, w.z2, w.E, w.H, w.I, T, r.k, r.ids, r.weights, y, out, ldo};
+    if (few) {
+        e = allow_lds<moe_down_few_kernel>();
+        if (e != hipSuccess)
+            return (int)e;
+        hipLaunchKernelGGL(moe_down_few_kernel, dim3(w.H / 32), dim3(kFewWaves * kWave), few_lds, s, da);
+    } else {
+        e = allow_lds<moe_down_kernel>();
+        if (e != hipSuccess)
+            return (int)e;
+        const int tiles = (w.H + 32 * kWaves - 1) / (32 * kWaves);
+        hipLaunchKernelGGL(moe_down_kernel, dim3(units * tiles), dim3(kWaves * kWave), sizeof(Shared), s, da);
+        const int64_t quads = (int64_t)T * (w.H / 4);
+        hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, da);
+    }
     return (int)hipGetLastError();
 }
 

@@ -16,18 +16,14 @@ int launch_moe_route(const void *logits, bool bf16, int64_t T, int E, int64_t ld
                      int32_t *ids, float *weights, void *stream);
 
 // ---- experts ------------------------------------------------------------
-// One pass takes at most kMoePairs (token, slot) pairs; more tokens run as
-// several passes over the same workspace.
+// One pass takes at most kMoePairs (token, slot) pairs, and at most 8192 result
+// columns a pair on average; more tokens, or wider layers, run as several passes
+// over the same workspace: the hidden activations of P pairs (two bf16 each),
+// then their fp32 results.
 constexpr int kMoePairs = 1024;
-// Workspace of one pass of P pairs over E experts of inner width I:
-//   ints: [0] number of chosen experts A, [4 ..] A records {expert, first, count, 0}
-//   (int4), then P pair numbers sorted by expert; then the hidden activations.
-inline int64_t moe_plan_records(int64_t E, int64_t P) { return E < P ? E : P; }
-inline int64_t moe_plan_bytes(int64_t E, int64_t P)
-{
-    return ((4 + 4 * moe_plan_records(E, P) + P) * 4 + 255) / 256 * 256;
-}
-inline int64_t moe_hidden_bytes(int64_t P, int64_t I) { return P * I * 4; }
+constexpr int kMoeFewPairs = 16;
+inline int64_t moe_hidden_bytes(int64_t P, int64_t I) { return (P * I * 4 + 255) / 256 * 256; }
+inline int64_t moe_pass_columns(int64_t P) { return P * 8192; }
 
 struct MoeExperts {
     const uint8_t *w1;          // [E, 2 I, H / 2]: I gate rows, then I up rows
