@@ -116,11 +116,15 @@ __global__ __launch_bounds__(kWaves * kWave) void moe_up_few_kernel(const UpArgs
         if (st0 + i < st1)
             ws.issue(st0 + i);
     uint8_t *operands = smem + kWaves * kRingBytes;
-    float *sums = reinterpret_cast<float *>(operands + H * 2);
+    const int GP = stage_groups(G);
+    float *sums = reinterpret_cast<float *>(operands + GP * 128);
     const uint16_t *x = p.x + (int64_t)t * p.ldx;
-    for (int c = threadIdx.x; c < H / 8; c += kWaves * kWave)
-        put_chunk<1>(operands, sums, 0, c,
-                     __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + c * 8))));
+    for (int c = threadIdx.x; c < GP * 8; c += kWaves * kWave) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (c < G * 8)
+            v = __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + c * 8)));
+        put_chunk<1>(operands, sums, 0, c, v);
+    }
     __syncthreads();
     float tot[1] = {0.f};
     stream_stages<1>(ws, p.z1 != nullptr, st0, st1, st1, 0, ARows<1>{operands, sums}, tot);
@@ -220,12 +224,18 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
     const int l32 = lane % 32, half = lane / 32;
     const int stages = (G + kStageGroups - 1) / kStageGroups;
     const int slices = max(1, min(kFewWaves / P, stages));
-    uint8_t *operands = smem + kFewWaves * kRingBytes;                      // [P][2][I]
-    float *sums = reinterpret_cast<float *>(operands + P * I * 4);          // [P][2][G]
-    float *s_sum = sums + 2 * P * G;                                        // [slices][P][32]
+    const int GP = stage_groups(G);
+    uint8_t *operands = smem + kFewWaves * kRingBytes;                      // [P][2][64 GP]
+    float *sums = reinterpret_cast<float *>(operands + P * GP * 256);       // [P][2][GP]
+    float *s_sum = sums + 2 * P * GP;                                       // [slices][P][32]
 
-    for (int c = threadIdx.x; c < P * I / 4; c += kFewWaves * kWave)        // 2 P rows of I / 8 chunks
-        put_chunk<1>(operands, sums, 0, c, *reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)c * 8));
+    for (int c = threadIdx.x; c < 2 * P * GP * 8; c += kFewWaves * kWave) {
+        const int row = c / (GP * 8), ch = c % (GP * 8);
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (ch < G * 8)
+            v = *reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)row * I + ch * 8);
+        put_chunk<1>(operands, sums, 0, c, v);
+    }
     __syncthreads();
     for (int it = wave; it < P * slices; it += kFewWaves) {
         const int pr = it / slices, sl = it % slices;
@@ -241,7 +251,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
                 ws.issue(st0 + i);
         float tot[1] = {0.f};
         stream_stages<1>(ws, p.z2 != nullptr, st0, st1, st1, 0,
-                         ARows<1>{operands + (2 * pr + l32 / 4 % 2) * I * 2, sums + (2 * pr + half) * G}, tot);
+                         ARows<1>{operands + (2 * pr + l32 / 4 % 2) * GP * 128, sums + (2 * pr + half) * GP}, tot);
         const float v = tot[0] + __shfl_xor(tot[0], 32);
         if (half == 0)
             s_sum[(sl * P + pr) * 32 + l32] = v;
@@ -285,10 +295,10 @@ __device__ __forceinline__ void down_tile(const DownArgs &p, const Picked &pk, i
     if (!live)
         return;
 #pragma unroll
-    for (int i = 0; i < kPairs / 2 || i < 4; ++i) {
-        // kPairs 4: the second parts are the other half of the wave; above, the upper registers.
-        const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[(kRegs / 2 + i) % kRegs];
-        const int at = kPairs == 4 ? i : i / 4 * 8 + 4 * half + i % 4;
+    for (int i = 0; i < 4; ++i) {
+        // The second parts are in the other half of the wave (4 pairs) or the other four registers (8).
+        const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[kRegs - 4 + i];
+        const int at = kPairs == 4 ? i : 4 * half + i;
         if (p0 + at < pk.count && (kPairs > 4 || half == i / 2))
             p.y[(int64_t)s.list[p0 + at] * p.H + n0 + l32] = v;
     }
@@ -308,10 +318,8 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownA
         const int left = pk.count - p0;
         if (left <= 4)
             down_tile<4>(p, pk, p0, n0, s), p0 += 4;
-        else if (left <= 8)
-            down_tile<8>(p, pk, p0, n0, s), p0 += 8;
         else
-            down_tile<16>(p, pk, p0, n0, s), p0 += 16;
+            down_tile<8>(p, pk, p0, n0, s), p0 += 8;
     }
 }
 
@@ -355,7 +363,7 @@ hipError_t launch_up_few(const UpArgs &a, hipStream_t s)
     if (e != hipSuccess)
         return e;
     const int runs = a.P * (a.I / 64);  // of four workgroups, rounded up to whole rounds of the XCDs
-    const int lds = kWaves * kRingBytes + a.H * 2 + a.H / 16;
+    const int lds = kWaves * kRingBytes + stage_groups(a.H / 64) * (128 + 4);
     hipLaunchKernelGGL(kernel, dim3((runs + kXcds - 1) / kXcds * kXcds * 4), dim3(kWaves * kWave), lds, s, a);
     return hipGetLastError();
 }
@@ -389,7 +397,7 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
     uint16_t *hidden = static_cast<uint16_t *>(ws);
     float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + moe_hidden_bytes(P, w.I));
 
-    const int few_lds = kFewWaves * kRingBytes + P * w.I * 4 + 2 * P * (w.I / 64) * 4 +
+    const int few_lds = kFewWaves * kRingBytes + 2 * P * stage_groups(w.I / 64) * (128 + 4) +
                         (P > kFewWaves ? P : kFewWaves) * 32 * 4;
     const bool few = P <= kMoeFewPairs && few_lds <= kMaxLds;
     if (r.logits && !few) {

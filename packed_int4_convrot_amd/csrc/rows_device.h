@@ -10,11 +10,16 @@ namespace ck {
 // (3,7), two operations a pair; act_order8() puts activations in the same order.
 __device__ __forceinline__ v8bf w4_bf16_plus128(uint32_t d)
 {
+    // The mask in a vector and the pattern in a scalar register, for v_and_or_b32
+    // (an instruction takes one scalar operand).
+    uint32_t mask = 0x000f000fu, pattern = 0x43004300u;
+    asm("" : "+v"(mask));
+    asm("" : "+s"(pattern));
     u32x4 r;
-    r[0] = (d & 0x000f000fu) | 0x43004300u;
-    r[1] = ((d >> 4) & 0x000f000fu) | 0x43004300u;
-    r[2] = ((d >> 8) & 0x000f000fu) | 0x43004300u;
-    r[3] = ((d >> 12) & 0x000f000fu) | 0x43004300u;
+    r[0] = (d & mask) | pattern;
+    r[1] = ((d >> 4) & mask) | pattern;
+    r[2] = ((d >> 8) & mask) | pattern;
+    r[3] = ((d >> 12) & mask) | pattern;
     return __builtin_bit_cast(v8bf, r);
 }
 

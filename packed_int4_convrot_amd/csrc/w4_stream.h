@@ -38,6 +38,10 @@ __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c)
 
 // 32 rows of one expert's packed weight [N, 32 G] bytes with scales [G, N]: rows
 // n0 .. n0 + 15 and n0 + far .. n0 + far + 15.
+__host__ __device__ constexpr int stage_groups(int groups)
+{
+    return (groups + kStageGroups - 1) / kStageGroups * kStageGroups;
+}
 struct WeightStream {
     const uint8_t *w;       // this lane's row, of each eight
     const uint16_t *sz;     // this lane's 8 scales or zero points of group 0
@@ -77,12 +81,17 @@ struct WeightStream {
     }
 };
 
-// Waits until at most the newest stage's instructions (more: they are in flight
-// behind it) are outstanding.
-__device__ __forceinline__ void wait_stage(bool more)
+// Waits for a stage behind which `newer` more have been issued: loads retire in
+// order, five instructions a stage.
+__device__ __forceinline__ void wait_stage(int newer)
 {
-    if (more)
-        __builtin_amdgcn_s_waitcnt(5 | 0x0F70);  // vmcnt(5)
+    static_assert(kStages <= 4, "vmcnt");
+    if (newer >= 3)
+        __builtin_amdgcn_s_waitcnt(15 | 0x0F70);
+    else if (newer == 2)
+        __builtin_amdgcn_s_waitcnt(10 | 0x0F70);
+    else if (newer == 1)
+        __builtin_amdgcn_s_waitcnt(5 | 0x0F70);
     else
         wait_vmcnt0();
 }
@@ -90,7 +99,7 @@ __device__ __forceinline__ void wait_stage(bool more)
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
 // Rows of A in LDS: 16-byte operands [group][4][2 halves][kRows] and group sums
-// [group][kRows].
+// [group][kRows], with zeros for the groups that fill up the last stage.
 template <int kRows>
 struct ARows {
     static constexpr int kRegs = kRows <= 2 ? 1 : kRows <= 8 ? 4 : kRows / 2;
@@ -108,32 +117,33 @@ __device__ __forceinline__ void stream_stages(const WeightStream &ws, bool zeros
     constexpr int kRegs = ARows<kRows>::kRegs;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
     for (int st = st0; st < st1; ++st) {
-        wait_stage(st + 1 < last);
+        wait_stage(min(last - 1 - st, kStages - 1));
         __builtin_amdgcn_sched_barrier(0);
         const lds_u8 *stage = ws.ring + st % kStages * kStageBytes;
-        const int ng = min(kStageGroups, ws.G - st * kStageGroups);
         const uint8_t *ap = A.operands + ((st * kStageGroups - a0) * 8 + half) * kRows * 16 + l32 % kRows * 16;
         const float *xp = A.sums + (st * kStageGroups - a0) * kRows + (kRows > 4 ? 4 * half : 0);
+        // Straight-line code for the stage's four groups, so that one group's
+        // reads and decode overlap another's MFMAs.
 #pragma unroll
         for (int u = 0; u < kStageGroups; ++u) {
-            if (u < ng) {
-                const u32x4 w = *(__attribute__((address_space(3))) const u32x4 *)(stage + l32 * 128 +
-                                                                                  ((2 * u + half) ^ (l32 % 8)) * 16);
-                const uint32_t sb = *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales +
-                                                                                          u * 128 + l32 * 2);
-                const uint32_t zb = *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales +
-                                                                                          u * 128 + 64 + l32 * 2);
-                v16f acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const u32x4 w = *(__attribute__((address_space(3))) const u32x4 *)(stage + l32 * 128 +
+                                                                              ((2 * u + half) ^ (l32 % 8)) * 16);
+            const uint32_t sb =
+                *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + l32 * 2);
+            const uint32_t zb =
+                *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + 64 + l32 * 2);
+            v16f acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc = mfma32(*reinterpret_cast<const v8bf *>(ap + (u * 8 + 2 * j) * kRows * 16),
-                                 w4_bf16_plus128(w[j]), acc);
-                const float s = bf16_to_f32(sb);
-                const float zc = __builtin_fmaf(-136.f, s, zeros ? bf16_to_f32(zb) : 0.f);
+            for (int j = 0; j < 4; ++j)
+                acc = mfma32(*reinterpret_cast<const v8bf *>(ap + (u * 8 + 2 * j) * kRows * 16),
+                             w4_bf16_plus128(w[j]), acc);
+            const float s = bf16_to_f32(sb);
+            const float zc = __builtin_fmaf(-136.f, s, zeros ? bf16_to_f32(zb) : 0.f);
 #pragma unroll
-                for (int i = 0; i < kRegs; ++i)
-                    tot[i] = __builtin_fmaf(s, acc[i], __builtin_fmaf(zc, xp[u * kRows + i / 4 * 8 + i % 4], tot[i]));
-            }
+            for (int i = 0; i < kRegs; ++i)
+                tot[i] = __builtin_fmaf(s, acc[i], __builtin_fmaf(zc, xp[u * kRows + i / 4 * 8 + i % 4], tot[i]));
+            if (kRows > 16 || (kRows > 8 && u % 2 == 1))
+                __builtin_amdgcn_sched_barrier(0);  // many rows: fewer groups' registers at a time
         }
         if (st + kStages < last) {
             wait_lds();  // the slot's operands have been read
@@ -177,13 +187,15 @@ __device__ __forceinline__ void stream_rows(const WeightStream &ws, bool zeros, 
     static_assert(kGroups % kStageGroups == 0, "a chunk is whole stages");
     const int G = ws.G, last = (G + kStageGroups - 1) / kStageGroups;
     for (int g0 = 0; g0 < G; g0 += kGroups) {
-        const int chunks = min(kGroups, G - g0) * 8;
+        const int rows_groups = min(kGroups, stage_groups(G) - g0) * kRows;
         u32x4 v[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int o = i * kThreads + threadIdx.x;
-            if (o / 8 < chunks / 8 * kRows)
-                v[i] = load(o / 8 % kRows, g0 * 8 + o / 8 / kRows * 8 + o % 8);
+            const int g = g0 + o / 8 / kRows;
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+            if (o / 8 < rows_groups && g < G)
+                v[i] = load(o / 8 % kRows, g * 8 + o % 8);
         }
         __builtin_amdgcn_sched_barrier(0);  // A's loads before the weights': they retire in order
         if (g0 == 0) {
@@ -197,7 +209,7 @@ __device__ __forceinline__ void stream_rows(const WeightStream &ws, bool zeros, 
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int o = i * kThreads + threadIdx.x;
-            if (o / 8 < chunks / 8 * kRows)
+            if (o / 8 < rows_groups)
                 put_chunk<kRows>(operands, sums, o / 8 % kRows, o / 8 / kRows * 8 + o % 8, v[i]);
         }
         __syncthreads();
