@@ -20,40 +20,7 @@
 namespace ck {
 namespace {
 
-// The expert of unit y of a launch over min(E, P) units, and its pairs in
-// ascending order.  With more experts than pairs, unit y is pair y's expert, if
-// y is the first pair to choose it.  count 0: nothing to do.
-struct Picked {
-    int expert, count;
-};
-__device__ __forceinline__ Picked pick(const int32_t *ids, int P, int E, int y, uint16_t *s_list)
-{
-    const int lane = threadIdx.x % kWave;
-    const bool writes = threadIdx.x < kWave;
-    const int e = E <= P ? y : __builtin_amdgcn_readfirstlane(ids[y]);
-    Picked r{e, 0};
-    if (e < 0 || e >= E)
-        return r;
-    int first = -1;
-    for (int c = 0; c < P; c += kWave) {
-        const int v = c + lane < P ? ids[c + lane] : -1;
-        const uint64_t mask = __ballot(v == e);
-        if (mask) {
-            if (first < 0)
-                first = c + __builtin_ctzll(mask);
-            if (writes && v == e)
-                s_list[r.count + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1))] = (uint16_t)(c + lane);
-            r.count += __builtin_popcountll(mask);
-        }
-    }
-    if (E > P && first != y)
-        r.count = 0;
-    return r;
-}
-
 // ---------------------------------------------------------------- first product
-
-constexpr int kWaves = 4;
 
 struct UpArgs {
     const uint16_t *x;
@@ -63,7 +30,7 @@ struct UpArgs {
     const uint16_t *s1, *z1;
     int E, H, I, P;
     MoeRouting r;
-    uint16_t *hidden;         // [P][2][I]: first parts, second parts, in operand order
+    uint16_t *hidden;         // [P][2][I]: first parts, second parts
 };
 
 // silu(g) u of hidden column n of a pair, as two bf16.
@@ -71,19 +38,21 @@ __device__ __forceinline__ void put_hidden(uint16_t *hidden, int pair, int I, in
 {
     uint16_t hi, lo;
     split_bf16(g / (1.f + expf(-g)) * u, hi, lo);
-    uint16_t *dst = hidden + (int64_t)pair * 2 * I + n / 8 * 8 + act_slot8(n % 8);
+    uint16_t *dst = hidden + (int64_t)pair * 2 * I + n;
     dst[0] = hi;
     dst[I] = lo;
 }
+
+constexpr int kFewUpWaves = 4;
 
 // Few pairs.  A unit is a pair, routed here (kNe logits a lane) or by the given
 // ids (kNe 0); a workgroup owns 16 hidden columns of it, a wave's tile being
 // their 16 gate and 16 up rows, and the waves split the H columns.
 template <int kNe, bool kBf16>
-__global__ __launch_bounds__(kWaves * kWave) void moe_up_few_kernel(const UpArgs p)
+__global__ __launch_bounds__(kFewUpWaves * kWave) void moe_up_few_kernel(const UpArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // rings, operands, sums
-    __shared__ float s_red[kWaves][32];
+    __shared__ float s_red[kFewUpWaves][32];
     const int H = p.H, I = p.I, G = H / 64, tiles = I / 16;
     // Neighbouring tiles share lines of the scales: runs of four go to one XCD.
     const int local = blockIdx.x / kXcds, run = local / 4 * kXcds + blockIdx.x % kXcds;
@@ -109,17 +78,16 @@ __global__ __launch_bounds__(kWaves * kWave) void moe_up_few_kernel(const UpArgs
     if (e < 0 || e >= p.E)
         return;
     const int stages = (G + kStageGroups - 1) / kStageGroups;
-    const int st0 = wave * stages / kWaves, st1 = (wave + 1) * stages / kWaves;
-    const WeightStream ws(p.w1, p.s1, p.z1, e, 2 * I, G, n0, I, smem + wave * kRingBytes);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-        if (st0 + i < st1)
-            ws.issue(st0 + i);
-    uint8_t *operands = smem + kWaves * kRingBytes;
+    const int st0 = wave * stages / kFewUpWaves, st1 = (wave + 1) * stages / kFewUpWaves;
+    WeightStream ws(p.w1, p.s1, p.z1, 2 * I, G, I, smem + wave * kRingBytes);
+    OneTile cursor{st0, st1};
+    ws.tile(e, n0);
+    ws.start(cursor);
+    uint8_t *operands = smem + kFewUpWaves * kRingBytes;
     const int GP = stage_groups(G);
     float *sums = reinterpret_cast<float *>(operands + GP * 128);
     const uint16_t *x = p.x + (int64_t)t * p.ldx;
-    for (int c = threadIdx.x; c < GP * 8; c += kWaves * kWave) {
+    for (int c = threadIdx.x; c < GP * 8; c += kFewUpWaves * kWave) {
         u32x4 v = {0u, 0u, 0u, 0u};
         if (c < G * 8)
             v = __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + c * 8)));
@@ -127,70 +95,218 @@ __global__ __launch_bounds__(kWaves * kWave) void moe_up_few_kernel(const UpArgs
     }
     __syncthreads();
     float tot[1] = {0.f};
-    stream_stages<1>(ws, p.z1 != nullptr, st0, st1, st1, 0, ARows<1>{operands, sums}, tot);
+    stream_stages<1>(ws, cursor, p.z1 != nullptr, st0, st1, 0, ARows<1>{operands, sums}, tot, [] {});
     if (lane < 32)
         s_red[wave][l32] = tot[0];
     __syncthreads();
     if (threadIdx.x < 16) {
         float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < kFewUpWaves; ++w)
             g += s_red[w][l32], u += s_red[w][l32 + 16];
         put_hidden(p.hidden, y, I, n0 + l32, g, u);
     }
 }
 
-// Otherwise: a workgroup owns 64 hidden columns of one expert, 16 a wave (their
-// gate and up rows), for tiles of kRows of its pairs.
+// ------------------------------------------------------------- many pairs: work
+//
+// An expert's pairs are taken in sets of up to eight (a second set reads the
+// weights again), and a set's 32-row weight tiles in octets, a tile for each wave.
+// One workgroup fits a CU, and each takes an equal run of the octets of all
+// sets, so that no CU ends late because an expert has many pairs or because
+// the chosen experts do not divide the chip.  A workgroup finds its run from the
+// ids itself; a wave's weights are one stream through all its tiles.
+constexpr int kWaves = 8, kSetPairs = 8, kMaxSets = 8;
+
 struct Shared {
     uint8_t ring[kWaves][kRingBytes];
     uint8_t operands[kChunkOperands];
-    float sums[kChunkElems / 64];
-    uint16_t list[kMoePairs];
+    float sums[kChunkSums];
+    int expert[kMaxSets], count[kMaxSets];
+    uint16_t pairs[kMaxSets][kSetPairs];
+};
+static_assert(sizeof(int) * kRouteMaxExperts <= kChunkOperands, "the experts' counts lie in the operands' place");
+
+struct Run {
+    int q0, q1;      // octets, counted through all sets
+    int first_set;   // its sets are in Shared from here on
 };
 
-template <int kRows>
-__device__ __forceinline__ void up_tile(const UpArgs &p, const Picked &pk, int p0, int n0, Shared &s)
+__device__ __forceinline__ int wave_sum_int(int v)
 {
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
-    const WeightStream ws(p.w1, p.s1, p.z1, pk.expert, 2 * p.I, p.H / 64, n0, p.I, s.ring[wave]);
-    float tot[ARows<kRows>::kRegs];
 #pragma unroll
-    for (int i = 0; i < ARows<kRows>::kRegs; ++i)
-        tot[i] = 0.f;
+    for (int d = 32; d >= 1; d >>= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int E, int octets, Shared &s)
+{
+    int *cnt = reinterpret_cast<int *>(s.operands);
+    const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
+    for (int e = t; e < E; e += kWaves * kWave)
+        cnt[e] = 0;
+    __syncthreads();
+    for (int p = t; p < P; p += kWaves * kWave) {
+        const int e = ids[p];
+        if (e >= 0 && e < E)
+            atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    int sets = 0;
+    for (int c = 0; c < E; c += kWave)
+        sets += c + lane < E ? (cnt[c + lane] + kSetPairs - 1) / kSetPairs : 0;
+    sets = wave_sum_int(sets);
+    const int total = sets * octets;
+    Run r;
+    r.q0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
+    r.q1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+    r.first_set = r.q0 / octets;
+    // Wave i finds the run's i-th set: its expert, and its pairs in ascending order.
+    const int set = r.first_set + wave;
+    if (r.q0 < r.q1 && set <= (r.q1 - 1) / octets) {
+        int before = 0, expert = 0, first = 0, count = 0;
+        for (int c = 0; c < E; c += kWave) {
+            const int n = c + lane < E ? cnt[c + lane] : 0;
+            int v = (n + kSetPairs - 1) / kSetPairs;
+            const int own = v;
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int u = __shfl_up(v, d);
+                if (lane >= d)
+                    v += u;
+            }
+            const uint64_t here = __ballot(before + v - own <= set && set < before + v);
+            if (here) {
+                const int l = __builtin_ctzll(here);
+                expert = c + l;
+                first = (set - before - __builtin_amdgcn_readlane(v - own, l)) * kSetPairs;
+                count = __builtin_amdgcn_readlane(n, l) - first;
+                break;
+            }
+            before += __builtin_amdgcn_readlane(v, kWave - 1);
+        }
+        int seen = -first;
+        for (int c = 0; c < P && seen < kSetPairs; c += kWave) {
+            const uint64_t mask = __ballot(c + lane < P && ids[c + lane] == expert);
+            const int at = seen + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
+            if ((mask >> lane & 1) && at >= 0 && at < kSetPairs)
+                s.pairs[wave][at] = (uint16_t)(c + lane);
+            seen += __builtin_popcountll(mask);
+        }
+        if (lane == 0)
+            s.expert[wave] = expert, s.count[wave] = min(count, kSetPairs);
+    }
+    __syncthreads();
+    return r;
+}
+
+// Cursor over a wave's tiles of a run: tile `wave` of each octet, where there is one.
+struct RunCursor {
+    const int *expert;
+    int q, q1, first_set, octets, tiles, rows, wave, st, stages;
+    __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int octets_, int tiles_, int rows_, int stages_)
+        : expert(s.expert), q(r.q0), q1(r.q1), first_set(r.first_set), octets(octets_), tiles(tiles_), rows(rows_),
+          wave(threadIdx.x / kWave), st(0), stages(stages_)
+    {
+    }
+    __device__ __forceinline__ bool next(WeightStream &ws, int &stage)
+    {
+        if (st == 0) {
+            while (q < q1 && q % octets * kWaves + wave >= tiles)
+                ++q;
+            if (q >= q1)
+                return false;
+            ws.tile(__builtin_amdgcn_readfirstlane(expert[q / octets - first_set]),
+                    (q % octets * kWaves + wave) * rows);
+        }
+        stage = st;
+        if (++st == stages)
+            st = 0, ++q;
+        return true;
+    }
+};
+
+// Octets [q0, q1) of one set against kRows rows of A.  done(tile, tot).
+template <int kRows, class Load, class Done>
+__device__ __forceinline__ void stream_set(WeightStream &ws, RunCursor &cursor, bool zeros, int q0, int q1, bool start,
+                                           Shared &s, Load &&load, Done &&done)
+{
+    constexpr int kGroups = kChunkElems / 64 / kRows, kRegs = ARows<kRows>::kRegs;
+    const int G = ws.G, stages = cursor.stages, wave = threadIdx.x / kWave;
+    const ARows<kRows> A{s.operands, s.sums};
+    const bool whole = G <= kGroups;
+    float tot[kRegs], held[kRegs];
+    int held_tile = -1;
+    const auto flush = [&] {
+        if (held_tile >= 0)
+            done(held_tile, held);
+        held_tile = -1;
+    };
+    for (int q = q0; q < q1; ++q) {
+        const int tile = q % cursor.octets * kWaves + wave;
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i)
+            tot[i] = 0.f;
+        for (int g0 = 0; g0 < G; g0 += kGroups) {
+            if (!whole || q == q0)
+                fill_rows<kRows, kWaves>(G, g0, s.operands, s.sums, load, [&] {
+                    if (start && q == q0 && g0 == 0)
+                        ws.start(cursor);
+                });
+            if (tile < cursor.tiles)
+                stream_stages<kRows>(ws, cursor, zeros, g0 / kStageGroups,
+                                     min(stages, (g0 + kGroups) / kStageGroups), g0, A, tot, flush);
+        }
+        if (tile < cursor.tiles) {
+            held_tile = tile;
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i)
+                held[i] = tot[i];
+        }
+    }
+    flush();
+}
+
+// The first product of many pairs: a tile is 16 hidden columns (their gate and up
+// rows); A's rows are the set's tokens.
+template <int kRows>
+__device__ __forceinline__ void up_set(const UpArgs &p, WeightStream &ws, RunCursor &cursor, int set, int q0, int q1,
+                                       bool start, Shared &s)
+{
+    const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
-        const int pr = s.list[min(p0 + row, pk.count - 1)];
+        const int pr = s.pairs[set][min(row, count - 1)];
         return __builtin_bit_cast(
             u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.x + (int64_t)(pr / p.k) * p.ldx + ch * 8)));
     };
-    stream_rows<kRows, kWaves>(ws, p.z1 != nullptr, true, s.operands, s.sums, load, tot);
+    const auto done = [&](int tile, const float(&tot)[ARows<kRows>::kRegs]) {
 #pragma unroll
-    for (int i = 0; i < ARows<kRows>::kRegs; ++i) {
-        const float u = __shfl_xor(tot[i], 16);
-        const int row = i / 4 * 8 + 4 * half + i % 4;
-        if (l32 < 16 && row < kRows && p0 + row < pk.count)
-            put_hidden(p.hidden, s.list[p0 + row], p.I, n0 + l32, tot[i], u);
-    }
+        for (int i = 0; i < ARows<kRows>::kRegs; ++i) {
+            const float u = __shfl_xor(tot[i], 16);
+            const int row = (kRows > 4 ? 4 * half : 0) + i;
+            if (l32 < 16 && (kRows > 4 || half == 0) && row < count)
+                put_hidden(p.hidden, s.pairs[set][row], p.I, tile * 16 + l32, tot[i], u);
+        }
+    };
+    stream_set<kRows>(ws, cursor, p.z1 != nullptr, q0, q1, start, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    const int tiles = p.I / 64, y = blockIdx.x / tiles;
-    const Picked pk = pick(p.r.ids, p.P, p.E, y, s.list);
-    if (pk.count == 0)
-        return;
-    __syncthreads();  // list
-    const int n0 = blockIdx.x % tiles * 64 + threadIdx.x / kWave * 16;
-    for (int p0 = 0; p0 < pk.count;) {
-        const int left = pk.count - p0;
-        if (left <= 4)
-            up_tile<4>(p, pk, p0, n0, s), p0 += 4;
-        else if (left <= 8)
-            up_tile<8>(p, pk, p0, n0, s), p0 += 8;
+    const int tiles = p.I / 16, octets = (tiles + kWaves - 1) / kWaves, G = p.H / 64;
+    const Run r = plan_run(p.r.ids, p.P, p.E, octets, s);
+    WeightStream ws(p.w1, p.s1, p.z1, 2 * p.I, G, p.I, s.ring[threadIdx.x / kWave]);
+    RunCursor cursor(r, s, octets, tiles, 16, stage_groups(G) / kStageGroups);
+    for (int q = r.q0; q < r.q1;) {
+        const int set = q / octets - r.first_set, end = min(r.q1, (q / octets + 1) * octets);
+        if (s.count[set] <= 4)
+            up_set<4>(p, ws, cursor, set, q, end, q == r.q0, s);
         else
-            up_tile<16>(p, pk, p0, n0, s), p0 += 16;
+            up_set<8>(p, ws, cursor, set, q, end, q == r.q0, s);
+        q = end;
     }
 }
 
@@ -233,7 +349,8 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
         const int row = c / (GP * 8), ch = c % (GP * 8);
         u32x4 v = {0u, 0u, 0u, 0u};
         if (ch < G * 8)
-            v = *reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)row * I + ch * 8);
+            v = __builtin_bit_cast(
+                u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)row * I + ch * 8)));
         put_chunk<1>(operands, sums, 0, c, v);
     }
     __syncthreads();
@@ -243,15 +360,13 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
         if (e < 0 || e >= p.E)
             continue;
         const int st0 = sl * stages / slices, st1 = (sl + 1) * stages / slices;
-        const WeightStream ws(p.w2, p.s2, p.z2, e, H, G, n0, 16, smem + wave * kRingBytes);
-        wait_lds();  // the ring's last operands have been read
-#pragma unroll
-        for (int i = 0; i < kStages; ++i)
-            if (st0 + i < st1)
-                ws.issue(st0 + i);
+        WeightStream ws(p.w2, p.s2, p.z2, H, G, 16, smem + wave * kRingBytes);
+        OneTile cursor{st0, st1};
+        ws.tile(e, n0);
+        ws.start(cursor);  // the ring's last stage has been read into registers
         float tot[1] = {0.f};
-        stream_stages<1>(ws, p.z2 != nullptr, st0, st1, st1, 0,
-                         ARows<1>{operands + (2 * pr + l32 / 4 % 2) * GP * 128, sums + (2 * pr + half) * GP}, tot);
+        const ARows<1> A{operands + (2 * pr + l32 / 4 % 2) * GP * 128, sums + (2 * pr + half) * GP};
+        stream_stages<1>(ws, cursor, p.z2 != nullptr, st0, st1, 0, A, tot, [] {});
         const float v = tot[0] + __shfl_xor(tot[0], 32);
         if (half == 0)
             s_sum[(sl * P + pr) * 32 + l32] = v;
@@ -273,53 +388,48 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
     }
 }
 
-// Otherwise: a workgroup owns 128 output columns (32 a wave) of one expert and
-// writes the sums of its pairs, which moe_combine_kernel adds.  A's rows are the
-// first parts of a tile's pairs, then the second parts.
+// The second product of many pairs: a tile is 32 output columns, A's rows are the
+// first parts of the set's pairs, then the second parts; the sums of each pair go
+// to moe_combine_kernel.
 template <int kPairs>
-__device__ __forceinline__ void down_tile(const DownArgs &p, const Picked &pk, int p0, int n0, Shared &s)
+__device__ __forceinline__ void down_set(const DownArgs &p, WeightStream &ws, RunCursor &cursor, int set, int q0,
+                                         int q1, bool start, Shared &s)
 {
     constexpr int kRows = 2 * kPairs, kRegs = ARows<kRows>::kRegs;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
-    const bool live = n0 < p.H;
-    const WeightStream ws(p.w2, p.s2, p.z2, pk.expert, p.H, p.I / 64, live ? n0 : 0, 16, s.ring[wave]);
-    float tot[kRegs];
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i)
-        tot[i] = 0.f;
+    const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
-        const int pr = s.list[min(p0 + row % kPairs, pk.count - 1)];
-        return *reinterpret_cast<const u32x4 *>(p.hidden + ((int64_t)pr * 2 + row / kPairs) * p.I + ch * 8);
+        const int pr = s.pairs[set][min(row % kPairs, count - 1)];
+        return __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(
+                                             p.hidden + ((int64_t)pr * 2 + row / kPairs) * p.I + ch * 8)));
     };
-    stream_rows<kRows, kWaves>(ws, p.z2 != nullptr, live, s.operands, s.sums, load, tot);
-    if (!live)
-        return;
+    const auto done = [&](int tile, const float(&tot)[kRegs]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        // The second parts are in the other half of the wave (4 pairs) or the other four registers (8).
-        const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[kRegs - 4 + i];
-        const int at = kPairs == 4 ? i : 4 * half + i;
-        if (p0 + at < pk.count && (kPairs > 4 || half == i / 2))
-            p.y[(int64_t)s.list[p0 + at] * p.H + n0 + l32] = v;
-    }
+        for (int i = 0; i < 4; ++i) {
+            // The second parts are in the other half of the wave (4 pairs) or the other four registers (8).
+            const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[kRegs - 4 + i];
+            const int at = kPairs == 4 ? i : 4 * half + i;
+            if (at < count && (kPairs > 4 || half == i / 2))
+                p.y[(int64_t)s.pairs[set][at] * p.H + tile * 32 + l32] = v;
+        }
+    };
+    stream_set<kRows>(ws, cursor, p.z2 != nullptr, q0, q1, start, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    const int tiles = (p.H + 32 * kWaves - 1) / (32 * kWaves);
-    const Picked pk = pick(p.ids, p.T * p.k, p.E, blockIdx.x / tiles, s.list);
-    if (pk.count == 0)
-        return;
-    __syncthreads();  // list
-    const int n0 = (blockIdx.x % tiles * kWaves + threadIdx.x / kWave) * 32;
-    for (int p0 = 0; p0 < pk.count;) {
-        const int left = pk.count - p0;
-        if (left <= 4)
-            down_tile<4>(p, pk, p0, n0, s), p0 += 4;
+    const int tiles = p.H / 32, octets = (tiles + kWaves - 1) / kWaves, G = p.I / 64;
+    const Run r = plan_run(p.ids, p.T * p.k, p.E, octets, s);
+    WeightStream ws(p.w2, p.s2, p.z2, p.H, G, 16, s.ring[threadIdx.x / kWave]);
+    RunCursor cursor(r, s, octets, tiles, 32, stage_groups(G) / kStageGroups);
+    for (int q = r.q0; q < r.q1;) {
+        const int set = q / octets - r.first_set, end = min(r.q1, (q / octets + 1) * octets);
+        if (s.count[set] <= 4)
+            down_set<4>(p, ws, cursor, set, q, end, q == r.q0, s);
         else
-            down_tile<8>(p, pk, p0, n0, s), p0 += 8;
+            down_set<8>(p, ws, cursor, set, q, end, q == r.q0, s);
+        q = end;
     }
 }
 
@@ -346,7 +456,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const DownArgs p)
 }
 
 // More than 64 KiB of dynamic LDS needs the kernel's attribute raised once.
-constexpr int kMaxLds = 150 * 1024;
+constexpr int kMaxLds = 150 * 1024, kCus = 256;
 template <auto kernel>
 hipError_t allow_lds()
 {
@@ -363,18 +473,18 @@ hipError_t launch_up_few(const UpArgs &a, hipStream_t s)
     if (e != hipSuccess)
         return e;
     const int runs = a.P * (a.I / 64);  // of four workgroups, rounded up to whole rounds of the XCDs
-    const int lds = kWaves * kRingBytes + stage_groups(a.H / 64) * (128 + 4);
-    hipLaunchKernelGGL(kernel, dim3((runs + kXcds - 1) / kXcds * kXcds * 4), dim3(kWaves * kWave), lds, s, a);
+    const int lds = kFewUpWaves * kRingBytes + stage_groups(a.H / 64) * (128 + 4);
+    hipLaunchKernelGGL(kernel, dim3((runs + kXcds - 1) / kXcds * kXcds * 4), dim3(kFewUpWaves * kWave), lds, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_up(const UpArgs &a, bool few, int units, hipStream_t s)
+hipError_t launch_up(const UpArgs &a, bool few, int blocks, hipStream_t s)
 {
     if (!few) {
         const hipError_t e = allow_lds<moe_up_kernel>();
         if (e != hipSuccess)
             return e;
-        hipLaunchKernelGGL(moe_up_kernel, dim3(units * (a.I / 64)), dim3(kWaves * kWave), sizeof(Shared), s, a);
+        hipLaunchKernelGGL(moe_up_kernel, dim3(blocks), dim3(kWaves * kWave), sizeof(Shared), s, a);
         return hipGetLastError();
     }
     if (!a.r.logits)
@@ -405,9 +515,15 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
         if (e != 0)
             return e;
     }
-    const int units = w.E < P ? w.E : P;
     const UpArgs ua{x, ldx, r.k, w.w1, w.s1, w.z1, w.E, w.H, w.I, P, r, hidden};
-    hipError_t e = launch_up(ua, few, units, s);
+    // One workgroup a CU, and no more than there can be octets; at most kMaxSets
+    // sets a workgroup, which 256 workgroups keep to by far (up to 1152 sets).
+    const int most_sets = (w.E < P ? w.E : P) + P / kSetPairs;
+    const auto grid = [&](int tiles) {
+        const int64_t octets = (int64_t)most_sets * ((tiles + kWaves - 1) / kWaves);
+        return octets < kCus ? (int)octets : kCus;
+    };
+    hipError_t e = launch_up(ua, few, grid(w.I / 16), s);
     if (e != hipSuccess)
         return (int)e;
     const DownArgs da{hidden, w.w2, w.s2, w.z2, w.E, w.H, w.I, T, r.k, r.ids, r.weights, y, out, ldo};
@@ -420,8 +536,7 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
         e = allow_lds<moe_down_kernel>();
         if (e != hipSuccess)
             return (int)e;
-        const int tiles = (w.H + 32 * kWaves - 1) / (32 * kWaves);
-        hipLaunchKernelGGL(moe_down_kernel, dim3(units * tiles), dim3(kWaves * kWave), sizeof(Shared), s, da);
+        hipLaunchKernelGGL(moe_down_kernel, dim3(grid(w.H / 32)), dim3(kWaves * kWave), sizeof(Shared), s, da);
         const int64_t quads = (int64_t)T * (w.H / 4);
         hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, da);
     }

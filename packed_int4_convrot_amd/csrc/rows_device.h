@@ -33,9 +33,6 @@ __device__ __forceinline__ v8bf act_order8(u32x4 w)
     r[3] = perm(w[3], w[1], 0x07060302u);
     return __builtin_bit_cast(v8bf, r);
 }
-// Where column c of eight lands in that order.
-__device__ __forceinline__ int act_slot8(int c) { return c < 4 ? 2 * c : 2 * c - 7; }
-
 // 16 x 16 x 32 bf16 MFMA.  Lane l holds row (a) or column (b) l % 16 and the 8
 // k-values of quarter l / 16; the result's lane l holds column l % 16, rows
 // 4 (l / 16) + i.

@@ -36,48 +36,79 @@ __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// 32 rows of one expert's packed weight [N, 32 G] bytes with scales [G, N]: rows
-// n0 .. n0 + 15 and n0 + far .. n0 + far + 15.
 __host__ __device__ constexpr int stage_groups(int groups)
 {
     return (groups + kStageGroups - 1) / kStageGroups * kStageGroups;
 }
+
+// Packed weights [experts][N, 32 G] bytes with scales [experts][G, N], read by
+// tiles of 32 rows of one expert: n0 .. n0 + 15 and n0 + far .. n0 + far + 15.
+// A cursor says which stages to read: next() sets the tile of the next stage and
+// its number, or returns false at the end.
 struct WeightStream {
-    const uint8_t *w;       // this lane's row, of each eight
-    const uint16_t *sz;     // this lane's 8 scales or zero points of group 0
+    const uint8_t *packed, *w;      // w, sz: this lane's row of each eight, and its
+    const uint16_t *s, *z, *sz;     // 8 scales or zero points of group 0, in the tile
     int64_t far_bytes;
-    int row_bytes, G, N, slot;
-    bool scales;            // this lane loads scales
+    int row_bytes, G, N, far, slot;
+    int place, use;                 // ring slots of the next to issue and to consume
+    int ahead;                      // stages issued and not consumed
+    bool scales, zero_point;        // this lane loads scales; they are zero points
     lds_u8 *ring;
 
-    __device__ __forceinline__ WeightStream(const uint8_t *packed, const uint16_t *s, const uint16_t *z, int64_t expert,
-                                            int rows, int groups, int n0, int far, void *lds)
+    __device__ __forceinline__ WeightStream(const uint8_t *packed_, const uint16_t *s_, const uint16_t *z_, int rows,
+                                            int groups, int far_, void *lds)
     {
         const int lane = threadIdx.x % kWave;
-        G = groups, N = rows, row_bytes = 32 * groups;
+        packed = packed_, s = s_, z = z_, G = groups, N = rows, far = far_, row_bytes = 32 * groups;
         far_bytes = (int64_t)far * row_bytes;
-        w = packed + (expert * rows + n0 + lane / 8) * row_bytes;
         slot = (lane % 8) ^ (lane / 8);
-        const int zero_point = lane / 4 % 2, piece = lane % 4;
+        zero_point = lane / 4 % 2;
         scales = lane < 32 && (z || !zero_point);
-        sz = (zero_point && z ? z : s) + expert * groups * rows + n0 + piece % 2 * 8 + piece / 2 * far;
         ring = (lds_u8 *)lds;
+        place = use = ahead = 0;
     }
-
-    // Global -> ring for stage st (groups 4 st .. 4 st + 3; past the row's end the
-    // last ones again, which are not used): five instructions.
-    __device__ __forceinline__ void issue(int st) const
+    __device__ __forceinline__ void tile(int expert, int n0)
     {
-        lds_u8 *to = ring + st % kStages * kStageBytes;
-        const uint8_t *from = w + 16 * min(st * 8 + slot, 2 * G - 1);
+        const int lane = threadIdx.x % kWave, piece = lane % 4;
+        w = packed + ((int64_t)expert * N + n0 + lane / 8) * row_bytes;
+        sz = (zero_point && z ? z : s) + (int64_t)expert * G * N + n0 + piece % 2 * 8 + piece / 2 * far;
+    }
+    // Global -> ring for one stage of the tile (past the row's end the last columns
+    // again, which meet zeros): five instructions.
+    __device__ __forceinline__ void issue(int stage)
+    {
+        lds_u8 *to = ring + place * kStageBytes;
+        const uint8_t *from = w + 16 * min(stage * 8 + slot, 2 * G - 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             __builtin_amdgcn_global_load_lds(from + i / 2 * far_bytes + i % 2 * 8 * row_bytes,
                                              (__attribute__((address_space(3))) void *)(to + i * 1024), 16, 0, 0);
-        const int g = min(st * kStageGroups + (int)(threadIdx.x % 32) / 8, G - 1);
+        const int g = min(stage * kStageGroups + (int)(threadIdx.x % 32) / 8, G - 1);
         if (scales)
             __builtin_amdgcn_global_load_lds(sz + (int64_t)g * N,
                                              (__attribute__((address_space(3))) void *)(to + kStageScales), 16, 0, 0);
+        place = place + 1 == kStages ? 0 : place + 1;
+        ++ahead;
+    }
+    template <class Cursor>
+    __device__ __forceinline__ void start(Cursor &cursor)
+    {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) {
+            int stage;
+            if (cursor.next(*this, stage))
+                issue(stage);
+        }
+    }
+};
+
+// Cursor over stages [st, end) of the tile that is set.
+struct OneTile {
+    int st, end;
+    __device__ __forceinline__ bool next(WeightStream &, int &stage)
+    {
+        stage = st;
+        return st++ < end;
     }
 };
 
@@ -107,48 +138,60 @@ struct ARows {
     const float *sums;
 };
 
-// Stages [st0, st1) of a stream whose first min(kStages, st1 - st0) stages have
-// been issued, added to tot; stages up to `last` are issued behind them.  A's
-// first group is group a0.
-template <int kRows>
-__device__ __forceinline__ void stream_stages(const WeightStream &ws, bool zeros, int st0, int st1, int last, int a0,
-                                              const ARows<kRows> &A, float (&tot)[ARows<kRows>::kRegs])
+// Stages [st0, st1) of a tile, the stream's next to consume, added to tot; the
+// cursor's next stages are issued behind them.  A's first group is group a0.
+// after_first() runs between the first stage's reads and the issue behind it:
+// stores there are a stage old when they are waited for.
+template <int kRows, class Cursor, class Hook>
+__device__ __forceinline__ void stream_stages(WeightStream &ws, Cursor &cursor, bool zeros, int st0, int st1, int a0,
+                                              const ARows<kRows> &A, float (&tot)[ARows<kRows>::kRegs],
+                                              Hook &&after_first)
 {
     constexpr int kRegs = ARows<kRows>::kRegs;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
     for (int st = st0; st < st1; ++st) {
-        wait_stage(min(last - 1 - st, kStages - 1));
+        wait_stage(ws.ahead - 1);
         __builtin_amdgcn_sched_barrier(0);
-        const lds_u8 *stage = ws.ring + st % kStages * kStageBytes;
-        const uint8_t *ap = A.operands + ((st * kStageGroups - a0) * 8 + half) * kRows * 16 + l32 % kRows * 16;
-        const float *xp = A.sums + (st * kStageGroups - a0) * kRows + (kRows > 4 ? 4 * half : 0);
-        // Straight-line code for the stage's four groups, so that one group's
-        // reads and decode overlap another's MFMAs.
+        const lds_u8 *stage = ws.ring + ws.use * kStageBytes;
+        ws.use = ws.use + 1 == kStages ? 0 : ws.use + 1;
+        --ws.ahead;
+        // The stage into registers first, so that the next one can be issued into
+        // its slot before the multiplication.
+        u32x4 w[kStageGroups];
+        uint32_t sb[kStageGroups], zb[kStageGroups];
 #pragma unroll
         for (int u = 0; u < kStageGroups; ++u) {
-            const u32x4 w = *(__attribute__((address_space(3))) const u32x4 *)(stage + l32 * 128 +
-                                                                              ((2 * u + half) ^ (l32 % 8)) * 16);
-            const uint32_t sb =
-                *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + l32 * 2);
-            const uint32_t zb =
-                *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + 64 + l32 * 2);
+            w[u] = *(__attribute__((address_space(3))) const u32x4 *)(stage + l32 * 128 +
+                                                                     ((2 * u + half) ^ (l32 % 8)) * 16);
+            sb[u] = *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + l32 * 2);
+            zb[u] = *(__attribute__((address_space(3))) const uint16_t *)(stage + kStageScales + u * 128 + 64 + l32 * 2);
+        }
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        if (st == st0)
+            after_first();
+        int next;
+        if (cursor.next(ws, next))
+            ws.issue(next);
+        __builtin_amdgcn_sched_barrier(0);
+        // Straight-line code for the stage's four groups, so that one group's
+        // reads and decode overlap another's MFMAs.
+        const uint8_t *ap = A.operands + ((st * kStageGroups - a0) * 8 + half) * kRows * 16 + l32 % kRows * 16;
+        const float *xp = A.sums + (st * kStageGroups - a0) * kRows + (kRows > 4 ? 4 * half : 0);
+#pragma unroll
+        for (int u = 0; u < kStageGroups; ++u) {
             v16f acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc = mfma32(*reinterpret_cast<const v8bf *>(ap + (u * 8 + 2 * j) * kRows * 16),
-                             w4_bf16_plus128(w[j]), acc);
-            const float s = bf16_to_f32(sb);
-            const float zc = __builtin_fmaf(-136.f, s, zeros ? bf16_to_f32(zb) : 0.f);
+                             w4_bf16_plus128(w[u][j]), acc);
+            const float s = bf16_to_f32(sb[u]);
+            const float zc = __builtin_fmaf(-136.f, s, zeros ? bf16_to_f32(zb[u]) : 0.f);
 #pragma unroll
             for (int i = 0; i < kRegs; ++i)
                 tot[i] = __builtin_fmaf(s, acc[i], __builtin_fmaf(zc, xp[u * kRows + i / 4 * 8 + i % 4], tot[i]));
-            if (kRows > 16 || (kRows > 8 && u % 2 == 1))
+            if (kRows > 8 && u % 2 == 1)
                 __builtin_amdgcn_sched_barrier(0);  // many rows: fewer groups' registers at a time
-        }
-        if (st + kStages < last) {
-            wait_lds();  // the slot's operands have been read
-            __builtin_amdgcn_sched_barrier(0);
-            ws.issue(st + kStages);
         }
     }
 }
@@ -171,52 +214,43 @@ __device__ __forceinline__ void put_chunk(uint8_t *operands, float *sums, int ro
         sums[g * kRows + row] = t;
 }
 
-// All columns of a stream for kRows rows of A, by every wave of a workgroup of
-// kWaves; A goes through LDS in chunks of 16384 / kRows columns.  load(row, ch)
-// gives eight columns (chunk ch of the whole row) in operand order; waves that
-// are not live only help to load.
-constexpr int kChunkElems = 16384;
-constexpr int kChunkOperands = kChunkElems * 2, kChunkSums = kChunkElems / 64 * 4;
+// A for a workgroup of kWaves waves, in LDS: whole where it fits, else in chunks
+// of 32768 / kRows columns.  load(row, chunk of 8 columns) gives columns in operand
+// order.  started() runs between A's loads and the barrier: loads retire in
+// order, so weights issued there arrive behind A.
+constexpr int kChunkElems = 32768;
+constexpr int kChunkOperands = kChunkElems * 2, kChunkSums = kChunkElems / 64;
 
-template <int kRows, int kWaves, class Load>
-__device__ __forceinline__ void stream_rows(const WeightStream &ws, bool zeros, bool live, uint8_t *operands,
-                                            float *sums, Load &&load, float (&tot)[ARows<kRows>::kRegs])
+template <int kRows, int kWaves, class Load, class Started>
+__device__ __forceinline__ void fill_rows(int G, int g0, uint8_t *operands, float *sums, Load &&load, Started &&started)
 {
     constexpr int kThreads = kWaves * kWave, kLoads = kChunkElems / 8 / kThreads;
     constexpr int kGroups = kChunkElems / 64 / kRows;  // of a chunk
     static_assert(kGroups % kStageGroups == 0, "a chunk is whole stages");
-    const int G = ws.G, last = (G + kStageGroups - 1) / kStageGroups;
-    for (int g0 = 0; g0 < G; g0 += kGroups) {
-        const int rows_groups = min(kGroups, stage_groups(G) - g0) * kRows;
-        u32x4 v[kLoads];
+    const int rows_groups = min(kGroups, stage_groups(G) - g0) * kRows;
+    // Opaque, so that the addresses that follow from it are computed here and not
+    // kept in registers through the streaming loops.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    u32x4 v[kLoads];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int o = i * kThreads + threadIdx.x;
-            const int g = g0 + o / 8 / kRows;
-            v[i] = u32x4{0u, 0u, 0u, 0u};
-            if (o / 8 < rows_groups && g < G)
-                v[i] = load(o / 8 % kRows, g * 8 + o % 8);
-        }
-        __builtin_amdgcn_sched_barrier(0);  // A's loads before the weights': they retire in order
-        if (g0 == 0) {
-            if (live)
-#pragma unroll
-                for (int st = 0; st < kStages; ++st)
-                    if (st < last)
-                        ws.issue(st);
-        }
-        __syncthreads();  // the previous chunk has been read
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int o = i * kThreads + threadIdx.x;
-            if (o / 8 < rows_groups)
-                put_chunk<kRows>(operands, sums, o / 8 % kRows, o / 8 / kRows * 8 + o % 8, v[i]);
-        }
-        __syncthreads();
-        if (live)
-            stream_stages<kRows>(ws, zeros, g0 / kStageGroups, min(last, (g0 + kGroups) / kStageGroups), last, g0,
-                                 ARows<kRows>{operands, sums}, tot);
+    for (int i = 0; i < kLoads; ++i) {
+        const int o = i * kThreads + tid;
+        const int g = g0 + o / 8 / kRows;
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (o / 8 < rows_groups && g < G)
+            v[i] = load(o / 8 % kRows, g * 8 + o % 8);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    started();
+    __syncthreads();  // what was there has been read
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int o = i * kThreads + tid;
+        if (o / 8 < rows_groups)
+            put_chunk<kRows>(operands, sums, o / 8 % kRows, o / 8 / kRows * 8 + o % 8, v[i]);
+    }
+    __syncthreads();
 }
 
 }  // namespace ck
