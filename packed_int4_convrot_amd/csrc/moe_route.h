@@ -4,7 +4,8 @@
 // the order of the floats (NaN and -inf are key 0: never chosen), so that in each
 // of the k rounds the wave's maximum key, and among the lanes that hold it the
 // lowest, give the largest logit at its lowest index.  The rounds depend on one
-// another; a round is six fused shift-and-maximum operations and a ballot.
+// another; a round is six shift-and-maximum steps, a ballot and the winner's scan
+// of its own keys.
 #pragma once
 
 #include "rows_device.h"
@@ -32,45 +33,44 @@ __device__ __forceinline__ float logit_exp(uint32_t key, uint32_t top)
     return m == INFINITY ? (l == INFINITY ? 1.f : 0.f) : expf(l - m);
 }
 
-// On return lane j < k has slot j's expert (-1: none left) and weight.
+// One row's logits and the slots chosen so far: lane j has slot j's expert (-1:
+// none left) and its key.
+template <int kNe>
+struct Routed {
+    uint32_t all[kNe];  // the keys of this lane's experts
+    uint32_t top;
+    uint32_t mine;
+    int id;
+};
+
+// The first `rounds` slots of a row.
 template <int kNe, bool kBf16>
-__device__ __forceinline__ void route_row(const void *row, int E, int k, bool renormalize, int lane, int &id,
-                                          float &weight)
+__device__ __forceinline__ Routed<kNe> route_select(const void *row, int E, int rounds, int lane)
 {
-    uint32_t key[kNe];
+    Routed<kNe> r;
     uint32_t best = 0;
     int at = 0;
 #pragma unroll
     for (int i = 0; i < kNe; ++i) {
         const int e = lane * kNe + i;
-        key[i] = 0;
+        r.all[i] = 0;
         if (e < E) {
             if constexpr (kBf16)
-                key[i] = logit_key(bf16_to_f32(static_cast<const uint16_t *>(row)[e]));
+                r.all[i] = logit_key(bf16_to_f32(static_cast<const uint16_t *>(row)[e]));
             else
-                key[i] = logit_key(static_cast<const float *>(row)[e]);
+                r.all[i] = logit_key(static_cast<const float *>(row)[e]);
         }
     }
 #pragma unroll
     for (int i = 0; i < kNe; ++i)
-        if (key[i] > best)
-            best = key[i], at = i;
-    const uint32_t top = wave_max(best);
-    float all = 0.f;
-    if (!renormalize) {
-#pragma unroll
-        for (int i = 0; i < kNe; ++i) {
-            all += logit_exp(key[i], top);
-            if constexpr (kNe > 4)
-                __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
-        }
-        all = wave_sum(all);
-    }
-    id = -1;
-    uint32_t mine = 0;
-    uint32_t m = top;
+        if (r.all[i] > best)
+            best = r.all[i], at = i;
+    r.id = -1;
+    r.mine = 0;
+    r.top = wave_max(best);
+    uint32_t m = r.top;
 #pragma unroll 1
-    for (int j = 0; j < k; ++j) {
+    for (int j = 0; j < rounds; ++j) {
         if (j > 0)
             m = wave_max(best);
         if (m == 0)
@@ -78,22 +78,39 @@ __device__ __forceinline__ void route_row(const void *row, int E, int k, bool re
         const int src = __builtin_ctzll(__ballot(best == m));
         const int e = __builtin_amdgcn_readlane(lane * kNe + at, src);
         if (lane == j)
-            id = e, mine = m;
+            r.id = e, r.mine = m;
         if (lane == src) {
             // Its next: the largest key after (m, gone) in the order of choice.
             best = 0;
             const int gone = at;
 #pragma unroll
             for (int i = 0; i < kNe; ++i) {
-                const bool left = key[i] < m || (key[i] == m && i > gone);
-                if (left && key[i] > best)
-                    best = key[i], at = i;
+                const bool left = r.all[i] < m || (r.all[i] == m && i > gone);
+                if (left && r.all[i] > best)
+                    best = r.all[i], at = i;
             }
         }
     }
-    const float e = logit_exp(mine, top);
-    const float den = renormalize ? wave_sum(e) : all;
-    weight = den > 0.f ? e / den : 0.f;
+    return r;
+}
+
+// Lane j's weight, of a row whose slots have all been chosen.
+template <int kNe>
+__device__ __forceinline__ float route_weight(const Routed<kNe> &r, bool renormalize)
+{
+    const float e = logit_exp(r.mine, r.top);
+    float den = e;
+    if (!renormalize) {
+        den = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNe; ++i) {
+            den += logit_exp(r.all[i], r.top);
+            if constexpr (kNe > 4)
+                __builtin_amdgcn_sched_barrier(0);  // one exponential's registers at a time
+        }
+    }
+    den = wave_sum(den);
+    return den > 0.f ? e / den : 0.f;
 }
 
 }  // namespace ck

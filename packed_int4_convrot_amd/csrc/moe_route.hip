@@ -20,11 +20,10 @@ __global__ __launch_bounds__(kTokensPerBlock * kWave) void moe_route_kernel(
     if (t >= T)
         return;
     const void *row = static_cast<const uint8_t *>(logits) + t * ldl * (kBf16 ? 2 : 4);
-    int id;
-    float w;
-    route_row<kNe, kBf16>(row, E, k, renormalize, lane, id, w);
+    const Routed<kNe> r = route_select<kNe, kBf16>(row, E, k, lane);
+    const float w = route_weight(r, renormalize);
     if (lane < k) {
-        ids[t * k + lane] = id;
+        ids[t * k + lane] = r.id;
         weights[t * k + lane] = w;
     }
 }

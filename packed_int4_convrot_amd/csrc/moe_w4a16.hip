@@ -53,6 +53,7 @@ __global__ __launch_bounds__(kFewUpWaves * kWave) void moe_up_few_kernel(const U
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // rings, operands, sums
     __shared__ float s_red[kFewUpWaves][32];
+    __shared__ int s_expert;
     const int H = p.H, I = p.I, G = H / 64, tiles = I / 16;
     // Neighbouring tiles share lines of the scales: runs of four go to one XCD.
     const int local = blockIdx.x / kXcds, run = local / 4 * kXcds + blockIdx.x % kXcds;
@@ -61,41 +62,65 @@ __global__ __launch_bounds__(kFewUpWaves * kWave) void moe_up_few_kernel(const U
     if (y >= p.P)
         return;
     const int t = y / p.k, slot = y - t * p.k;
-    int e;
-    if constexpr (kNe > 0) {
-        int id;
-        float wt;
-        route_row<kNe, kBf16>(static_cast<const uint8_t *>(p.r.logits) + (int64_t)t * p.r.ldl * (kBf16 ? 2 : 4), p.E,
-                              p.k, p.r.renormalize, lane, id, wt);
-        if (slot == 0 && n0 == 0 && threadIdx.x < p.k) {
-            p.r.ids[t * p.k + lane] = id;
-            p.r.weights[t * p.k + lane] = wt;
+    const int GP = stage_groups(G);
+    uint8_t *operands = smem + kFewUpWaves * kRingBytes;
+    float *sums = reinterpret_cast<float *>(operands + GP * 128);
+    // One wave routes, as far as this slot, the others bring x to LDS meanwhile; one
+    // workgroup of the token chooses every slot and writes them.
+    const bool writes = slot == 0 && n0 == 0;
+    int e = 0;
+    Routed<(kNe > 0) ? kNe : 1> routed;
+    if (kNe == 0 || wave == 0) {
+        if constexpr (kNe > 0) {
+            routed = route_select<kNe, kBf16>(
+                static_cast<const uint8_t *>(p.r.logits) + (int64_t)t * p.r.ldl * (kBf16 ? 2 : 4), p.E,
+                writes ? p.k : slot + 1, lane);
+            if (lane == slot)
+                s_expert = routed.id;
+        } else {
+            e = __builtin_amdgcn_readfirstlane(p.r.ids[y]);
         }
-        e = __builtin_amdgcn_readlane(id, slot);
-    } else {
-        e = __builtin_amdgcn_readfirstlane(p.r.ids[y]);
+    }
+    constexpr int kFirst = kNe > 0 ? 1 : 0;  // first wave that stages x
+    if (wave >= kFirst) {
+        const uint16_t *x = p.x + (int64_t)t * p.ldx;
+        constexpr int kStride = (kFewUpWaves - kFirst) * kWave, kLoads = 4;
+        for (int c0 = threadIdx.x - kFirst * kWave; c0 < GP * 8; c0 += kLoads * kStride) {
+            u32x4 v[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                v[i] = u32x4{0u, 0u, 0u, 0u};
+                if (c0 + i * kStride < G * 8)
+                    v[i] = __builtin_bit_cast(
+                        u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + (c0 + i * kStride) * 8)));
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (c0 + i * kStride < GP * 8)
+                    put_chunk<1>(operands, sums, 0, c0 + i * kStride, v[i]);
+        }
+    }
+    __syncthreads();
+    if constexpr (kNe > 0) {
+        e = __builtin_amdgcn_readfirstlane(s_expert);
+        if (writes && wave == 0) {
+            const float wt = route_weight(routed, p.r.renormalize);
+            if (lane < p.k) {
+                p.r.ids[t * p.k + lane] = routed.id;
+                p.r.weights[t * p.k + lane] = wt;
+            }
+        }
     }
     if (e < 0 || e >= p.E)
         return;
-    const int stages = (G + kStageGroups - 1) / kStageGroups;
+    WeightStream<> ws(p.w1, p.s1, p.z1, 2 * I, G, I, smem + wave * kRingBytes);
+    const int stages = ws.stages();
     const int st0 = wave * stages / kFewUpWaves, st1 = (wave + 1) * stages / kFewUpWaves;
-    WeightStream ws(p.w1, p.s1, p.z1, 2 * I, G, I, smem + wave * kRingBytes);
     OneTile cursor{st0, st1};
     ws.tile(e, n0);
     ws.start(cursor);
-    uint8_t *operands = smem + kFewUpWaves * kRingBytes;
-    const int GP = stage_groups(G);
-    float *sums = reinterpret_cast<float *>(operands + GP * 128);
-    const uint16_t *x = p.x + (int64_t)t * p.ldx;
-    for (int c = threadIdx.x; c < GP * 8; c += kFewUpWaves * kWave) {
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (c < G * 8)
-            v = __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(x + c * 8)));
-        put_chunk<1>(operands, sums, 0, c, v);
-    }
-    __syncthreads();
     float tot[1] = {0.f};
-    stream_stages<1>(ws, cursor, p.z1 != nullptr, st0, st1, 0, ARows<1>{operands, sums}, tot, [] {});
+    stream_stages<1>(ws, cursor, p.z1 != nullptr, st0, st1, 0, ARows<1>{operands, sums}, tot, [] { return 0; });
     if (lane < 32)
         s_red[wave][l32] = tot[0];
     __syncthreads();
@@ -111,25 +136,30 @@ __global__ __launch_bounds__(kFewUpWaves * kWave) void moe_up_few_kernel(const U
 // ------------------------------------------------------------- many pairs: work
 //
 // An expert's pairs are taken in sets of up to eight (a second set reads the
-// weights again), and a set's 32-row weight tiles in octets, a tile for each wave.
-// One workgroup fits a CU, and each takes an equal run of the octets of all
-// sets, so that no CU ends late because an expert has many pairs or because
-// the chosen experts do not divide the chip.  A workgroup finds its run from the
-// ids itself; a wave's weights are one stream through all its tiles.
+// weights again), and a set's 32-row weight tiles in units of 8 / S, S waves to a
+// tile, each with a slice of the columns.  One workgroup fits a CU, and each takes
+// an equal run of the units of all sets, so that no CU ends late because an expert
+// has many pairs or because the chosen experts do not divide the chip; S is
+// the one whose runs are shortest.  A workgroup finds its run from the ids itself;
+// a wave's weights are one stream through all its tiles.
 constexpr int kWaves = 8, kSetPairs = 8, kMaxSets = 8;
 
 struct Shared {
     uint8_t ring[kWaves][kRingBytes];
     uint8_t operands[kChunkOperands];
     float sums[kChunkSums];
+    float part[2][kWaves][4][kWave];  // the slices' sums, of alternate units
     int expert[kMaxSets], count[kMaxSets];
-    uint16_t pairs[kMaxSets][kSetPairs];
+    uint16_t pairs[kMaxSets][kSetPairs], tokens[kMaxSets][kSetPairs];
 };
 static_assert(sizeof(int) * kRouteMaxExperts <= kChunkOperands, "the experts' counts lie in the operands' place");
+static_assert(sizeof(Shared) <= 160 * 1024, "LDS");
 
 struct Run {
-    int q0, q1;      // octets, counted through all sets
+    int q0, q1;      // units, counted through all sets
     int first_set;   // its sets are in Shared from here on
+    int slices;      // S
+    int units;       // of a set
 };
 
 __device__ __forceinline__ int wave_sum_int(int v)
@@ -140,7 +170,8 @@ __device__ __forceinline__ int wave_sum_int(int v)
     return v;
 }
 
-__device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int E, int octets, Shared &s)
+// whole: A lies in LDS whole, so that waves can have unlike columns.
+__device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int k, int E, int tiles, int stages, bool whole, Shared &s)
 {
     int *cnt = reinterpret_cast<int *>(s.operands);
     const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
@@ -157,14 +188,25 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int E, int oc
     for (int c = 0; c < E; c += kWave)
         sets += c + lane < E ? (cnt[c + lane] + kSetPairs - 1) / kSetPairs : 0;
     sets = wave_sum_int(sets);
-    const int total = sets * octets;
+    // The longest run of units, in stages (doubled; joining slices costs about half a stage).
     Run r;
+    int best = 0x7fffffff;
+    for (int S = 1; S <= kWaves; S *= 2) {
+        if (S > 1 && (!whole || S > stages))
+            break;
+        const int units = (tiles * S + kWaves - 1) / kWaves;
+        const int rounds = (sets * units + (int)gridDim.x - 1) / (int)gridDim.x;
+        const int cost = rounds * (2 * ((stages + S - 1) / S) + (S > 1 ? 1 : 0));
+        if (cost < best)
+            best = cost, r.slices = S, r.units = units;
+    }
+    const int total = sets * r.units;
     r.q0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
     r.q1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-    r.first_set = r.q0 / octets;
+    r.first_set = r.q0 / r.units;
     // Wave i finds the run's i-th set: its expert, and its pairs in ascending order.
     const int set = r.first_set + wave;
-    if (r.q0 < r.q1 && set <= (r.q1 - 1) / octets) {
+    if (r.q0 < r.q1 && set <= (r.q1 - 1) / r.units) {
         int before = 0, expert = 0, first = 0, count = 0;
         for (int c = 0; c < E; c += kWave) {
             const int n = c + lane < E ? cnt[c + lane] : 0;
@@ -191,7 +233,7 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int E, int oc
             const uint64_t mask = __ballot(c + lane < P && ids[c + lane] == expert);
             const int at = seen + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
             if ((mask >> lane & 1) && at >= 0 && at < kSetPairs)
-                s.pairs[wave][at] = (uint16_t)(c + lane);
+                s.pairs[wave][at] = (uint16_t)(c + lane), s.tokens[wave][at] = (uint16_t)((c + lane) / k);
             seen += __builtin_popcountll(mask);
         }
         if (lane == 0)
@@ -201,67 +243,91 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int E, int oc
     return r;
 }
 
-// Cursor over a wave's tiles of a run: tile `wave` of each octet, where there is one.
+// Cursor over a wave's tiles of a run: one in each unit, where there is one.
 struct RunCursor {
     const int *expert;
-    int q, q1, first_set, octets, tiles, rows, wave, st, stages;
-    __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int octets_, int tiles_, int rows_, int stages_)
-        : expert(s.expert), q(r.q0), q1(r.q1), first_set(r.first_set), octets(octets_), tiles(tiles_), rows(rows_),
-          wave(threadIdx.x / kWave), st(0), stages(stages_)
+    int q, q1, first_set, units, per_unit, tiles, rows, mine, st, st0, st1;
+    __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int tiles_, int rows_, int stages)
+        : expert(s.expert), q(r.q0), q1(r.q1), first_set(r.first_set), units(r.units), per_unit(kWaves / r.slices),
+          tiles(tiles_), rows(rows_)
     {
+        const int wave = threadIdx.x / kWave, slice = wave % r.slices;
+        mine = wave / r.slices;
+        st0 = slice * stages / r.slices, st1 = (slice + 1) * stages / r.slices;
+        st = st0;
     }
-    __device__ __forceinline__ bool next(WeightStream &ws, int &stage)
+    __device__ __forceinline__ int tile(int unit) const { return unit % units * per_unit + mine; }
+    __device__ __forceinline__ bool next(WeightStream<> &ws, int &stage)
     {
-        if (st == 0) {
-            while (q < q1 && q % octets * kWaves + wave >= tiles)
+        if (st == st0) {
+            while (q < q1 && tile(q) >= tiles)
                 ++q;
             if (q >= q1)
                 return false;
-            ws.tile(__builtin_amdgcn_readfirstlane(expert[q / octets - first_set]),
-                    (q % octets * kWaves + wave) * rows);
+            ws.tile(__builtin_amdgcn_readfirstlane(expert[q / units - first_set]), tile(q) * rows);
         }
         stage = st;
-        if (++st == stages)
-            st = 0, ++q;
+        if (++st == st1)
+            st = st0, ++q;
         return true;
     }
 };
 
-// Octets [q0, q1) of one set against kRows rows of A.  done(tile, tot).
+// Units [q0, q1) of one set against kRows rows of A.  With 16 rows, rows 8-15 are
+// added to rows 0-7.  done(tile, sum) stores a tile's results and returns how many
+// vector stores that is at least.
 template <int kRows, class Load, class Done>
-__device__ __forceinline__ void stream_set(WeightStream &ws, RunCursor &cursor, bool zeros, int q0, int q1, bool start,
-                                           Shared &s, Load &&load, Done &&done)
+__device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor, const Run &r, bool zeros, int q0,
+                                           int q1, Shared &s, Load &&load, Done &&done)
 {
     constexpr int kGroups = kChunkElems / 64 / kRows, kRegs = ARows<kRows>::kRegs;
-    const int G = ws.G, stages = cursor.stages, wave = threadIdx.x / kWave;
+    const int G = ws.G, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const ARows<kRows> A{s.operands, s.sums};
     const bool whole = G <= kGroups;
-    float tot[kRegs], held[kRegs];
+    float tot[kRegs], held[4];
     int held_tile = -1;
     const auto flush = [&] {
-        if (held_tile >= 0)
-            done(held_tile, held);
+        const int stores = held_tile >= 0 ? done(held_tile, held) : 0;
         held_tile = -1;
+        return stores;
     };
     for (int q = q0; q < q1; ++q) {
-        const int tile = q % cursor.octets * kWaves + wave;
+        const int tile = cursor.tile(q);
 #pragma unroll
         for (int i = 0; i < kRegs; ++i)
             tot[i] = 0.f;
         for (int g0 = 0; g0 < G; g0 += kGroups) {
             if (!whole || q == q0)
                 fill_rows<kRows, kWaves>(G, g0, s.operands, s.sums, load, [&] {
-                    if (start && q == q0 && g0 == 0)
+                    if (q == r.q0 && g0 == 0)
                         ws.start(cursor);
                 });
             if (tile < cursor.tiles)
-                stream_stages<kRows>(ws, cursor, zeros, g0 / kStageGroups,
-                                     min(stages, (g0 + kGroups) / kStageGroups), g0, A, tot, flush);
+                stream_stages<kRows>(ws, cursor, zeros, max(cursor.st0, g0 / kStageGroups),
+                                     min(cursor.st1, (g0 + kGroups) / kStageGroups), g0, A, tot, flush);
         }
-        if (tile < cursor.tiles) {
+        if constexpr (kRegs == 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tot[i] += tot[kRegs - 4 + i];
+        if (r.slices > 1) {
+            // Alternate units use alternate places: a place is written again only
+            // after the barrier of the unit between.
+            float(&part)[kWaves][4][kWave] = s.part[q % 2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[wave][i][lane] = tot[i];
+            __syncthreads();
+            if (wave % r.slices == 0)
+                for (int w = 1; w < r.slices; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tot[i] += part[wave + w][i][lane];
+        }
+        if (tile < cursor.tiles && wave % r.slices == 0) {
             held_tile = tile;
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i)
+            for (int i = 0; i < 4; ++i)
                 held[i] = tot[i];
         }
     }
@@ -271,41 +337,43 @@ __device__ __forceinline__ void stream_set(WeightStream &ws, RunCursor &cursor, 
 // The first product of many pairs: a tile is 16 hidden columns (their gate and up
 // rows); A's rows are the set's tokens.
 template <int kRows>
-__device__ __forceinline__ void up_set(const UpArgs &p, WeightStream &ws, RunCursor &cursor, int set, int q0, int q1,
-                                       bool start, Shared &s)
+__device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
+                                       int q1, Shared &s)
 {
+    const int set = q0 / r.units - r.first_set;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
-        const int pr = s.pairs[set][min(row, count - 1)];
+        const int t = s.tokens[set][min(row, count - 1)];
         return __builtin_bit_cast(
-            u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.x + (int64_t)(pr / p.k) * p.ldx + ch * 8)));
+            u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.x + (int64_t)t * p.ldx + ch * 8)));
     };
-    const auto done = [&](int tile, const float(&tot)[ARows<kRows>::kRegs]) {
+    const auto done = [&](int tile, const float(&tot)[4]) {
 #pragma unroll
-        for (int i = 0; i < ARows<kRows>::kRegs; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float u = __shfl_xor(tot[i], 16);
             const int row = (kRows > 4 ? 4 * half : 0) + i;
             if (l32 < 16 && (kRows > 4 || half == 0) && row < count)
                 put_hidden(p.hidden, s.pairs[set][row], p.I, tile * 16 + l32, tot[i], u);
         }
+        return 2 * min(4, count);  // of the lower half's rows at least
     };
-    stream_set<kRows>(ws, cursor, p.z1 != nullptr, q0, q1, start, s, load, done);
+    stream_set<kRows>(ws, cursor, r, p.z1 != nullptr, q0, q1, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    const int tiles = p.I / 16, octets = (tiles + kWaves - 1) / kWaves, G = p.H / 64;
-    const Run r = plan_run(p.r.ids, p.P, p.E, octets, s);
-    WeightStream ws(p.w1, p.s1, p.z1, 2 * p.I, G, p.I, s.ring[threadIdx.x / kWave]);
-    RunCursor cursor(r, s, octets, tiles, 16, stage_groups(G) / kStageGroups);
+    const int tiles = p.I / 16;
+    WeightStream<> ws(p.w1, p.s1, p.z1, 2 * p.I, p.H / 64, p.I, s.ring[threadIdx.x / kWave]);
+    const Run r = plan_run(p.r.ids, p.P, p.k, p.E, tiles, ws.stages(), p.H * kSetPairs <= kChunkElems, s);
+    RunCursor cursor(r, s, tiles, 16, ws.stages());
     for (int q = r.q0; q < r.q1;) {
-        const int set = q / octets - r.first_set, end = min(r.q1, (q / octets + 1) * octets);
-        if (s.count[set] <= 4)
-            up_set<4>(p, ws, cursor, set, q, end, q == r.q0, s);
+        const int end = min(r.q1, (q / r.units + 1) * r.units);
+        if (s.count[q / r.units - r.first_set] <= 4)
+            up_set<4>(p, ws, cursor, r, q, end, s);
         else
-            up_set<8>(p, ws, cursor, set, q, end, q == r.q0, s);
+            up_set<8>(p, ws, cursor, r, q, end, s);
         q = end;
     }
 }
@@ -324,64 +392,91 @@ struct DownArgs {
     int64_t ldo;
 };
 
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 8, kFewDepth = 3;
+__host__ __device__ constexpr int few_half(int groups) { return stage_groups((groups + 1) / 2); }
+int few_down_lds(int P, int G)
+{
+    return kFewWaves * (kFewDepth * kStageBytes + few_half(G) * (512 + 16)) + (P > kFewWaves ? P : kFewWaves) * 64;
+}
 
-// Few pairs: a workgroup owns 32 output columns; its waves take the pairs (or
-// slices of the I columns, where there are fewer pairs than waves), then every
-// output adds its token's slots in order.  A has a pair's first parts in its even
-// rows' place and the second parts in the odd (rows 0 and 4 of the result: the
-// two halves of the wave).
+// Few pairs: a workgroup owns 16 output columns (so that the columns spread over
+// the chip); its waves take the pairs (or slices of the I columns, where there are
+// fewer pairs than waves), then every output adds its token's slots in order.
+// A tile's 32 rows are the 16 columns' weights of the first and of the second half
+// of the I columns; A's four rows are the pair's first and second parts of the
+// first half, then of the second.  A is the wave's own: no barriers until the end.
 __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const DownArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];  // rings, operands, group sums, results
-    const int H = p.H, I = p.I, G = I / 64, P = p.T * p.k;
-    const int n0 = xcd_block(blockIdx.x, gridDim.x) * 32;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int l32 = lane % 32, half = lane / 32;
-    const int stages = (G + kStageGroups - 1) / kStageGroups;
+    __shared__ int s_id[kMoeFewPairs];
+    __shared__ float s_weight[kMoeFewPairs];
+    const int I = p.I, G = I / 64, P = p.T * p.k;
+    const int n0 = xcd_block(blockIdx.x, gridDim.x) * 16;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l32 = lane % 32;
+    const int GH = (G + 1) / 2, GP = few_half(G), stages = GP / kStageGroups;
     const int slices = max(1, min(kFewWaves / P, stages));
-    const int GP = stage_groups(G);
-    uint8_t *operands = smem + kFewWaves * kRingBytes;                      // [P][2][64 GP]
-    float *sums = reinterpret_cast<float *>(operands + P * GP * 256);       // [P][2][GP]
-    float *s_sum = sums + 2 * P * GP;                                       // [slices][P][32]
+    constexpr int kRing = kFewDepth * kStageBytes;
+    uint8_t *operands = smem + kFewWaves * kRing + wave * GP * 512;                           // [GP][4][2][4] x 16 bytes
+    float *sums = reinterpret_cast<float *>(smem + kFewWaves * (kRing + GP * 512)) + wave * GP * 4;  // [GP][4]
+    float *s_sum = reinterpret_cast<float *>(smem + kFewWaves * (kRing + GP * 528));          // [slices][P][16]
 
-    for (int c = threadIdx.x; c < 2 * P * GP * 8; c += kFewWaves * kWave) {
-        const int row = c / (GP * 8), ch = c % (GP * 8);
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (ch < G * 8)
-            v = __builtin_bit_cast(
-                u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.hidden + (int64_t)row * I + ch * 8)));
-        put_chunk<1>(operands, sums, 0, c, v);
-    }
-    __syncthreads();
+    WeightStream<kFewDepth> ws(p.w2, p.s2, p.z2, p.H, G, 0, smem + wave * kRing);
+    const int id = threadIdx.x < P ? p.ids[threadIdx.x] : 0;
+    const float weight = threadIdx.x < P ? p.weights[threadIdx.x] : 0.f;
     for (int it = wave; it < P * slices; it += kFewWaves) {
-        const int pr = it / slices, sl = it % slices;
+        const int pr = it / slices, sl = it - pr * slices;
         const int e = __builtin_amdgcn_readfirstlane(p.ids[pr]);
         if (e < 0 || e >= p.E)
             continue;
         const int st0 = sl * stages / slices, st1 = (sl + 1) * stages / slices;
-        WeightStream ws(p.w2, p.s2, p.z2, H, G, 16, smem + wave * kRingBytes);
         OneTile cursor{st0, st1};
         ws.tile(e, n0);
-        ws.start(cursor);  // the ring's last stage has been read into registers
-        float tot[1] = {0.f};
-        const ARows<1> A{operands + (2 * pr + l32 / 4 % 2) * GP * 128, sums + (2 * pr + half) * GP};
-        stream_stages<1>(ws, cursor, p.z2 != nullptr, st0, st1, 0, A, tot, [] {});
-        const float v = tot[0] + __shfl_xor(tot[0], 32);
-        if (half == 0)
-            s_sum[(sl * P + pr) * 32 + l32] = v;
+        // A's loads, then the weights (loads retire in order), then A to LDS: two
+        // stages' chunks of the four rows at a time.
+        bool started = false;
+        for (int ch0 = st0 * kStageGroups * 8; ch0 < st1 * kStageGroups * 8; ch0 += kWave) {
+            const int ch = ch0 + lane;
+            u32x4 v[4];
+#pragma unroll
+            for (int row = 0; row < 4; ++row) {
+                const int col = ch + row / 2 * GH * 8;
+                v[row] = u32x4{0u, 0u, 0u, 0u};
+                if (ch < GH * 8 && col < G * 8)
+                    v[row] = *reinterpret_cast<const u32x4 *>(p.hidden + ((int64_t)pr * 2 + row % 2) * I + col * 8);
+            }
+            if (!started) {
+                __builtin_amdgcn_sched_barrier(0);
+                ws.start(cursor);
+                __builtin_amdgcn_sched_barrier(0);
+                started = true;
+            }
+            if (ch < st1 * kStageGroups * 8)
+#pragma unroll
+                for (int row = 0; row < 4; ++row)
+                    put_chunk<4>(operands, sums, row, ch, __builtin_bit_cast(u32x4, act_order8(v[row])));
+        }
+        wait_lds();
+        const ARows<4> A{operands, sums};
+        float tot[4] = {0.f, 0.f, 0.f, 0.f};
+        stream_stages<4>(ws, cursor, p.z2 != nullptr, st0, st1, 0, A, tot, [] { return 0; });
+        float v = l32 < 16 ? tot[0] + tot[1] : tot[2] + tot[3];
+        v += __shfl_xor(v, 16);
+        if (lane < 16)
+            s_sum[(sl * P + pr) * 16 + lane] = v;
     }
+    if (threadIdx.x < P)
+        s_id[threadIdx.x] = id, s_weight[threadIdx.x] = weight;
     __syncthreads();
-    for (int o = threadIdx.x; o < p.T * 32; o += kFewWaves * kWave) {
-        const int t = o / 32, col = o % 32;
+    for (int o = threadIdx.x; o < p.T * 16; o += kFewWaves * kWave) {
+        const int t = o / 16, col = o % 16;
         float y = 0.f;
         for (int j = 0; j < p.k; ++j) {
-            const int pr = t * p.k + j, e = p.ids[pr];
-            if (e >= 0 && e < p.E) {
-                float v = s_sum[pr * 32 + col];
+            const int pr = t * p.k + j;
+            if (s_id[pr] >= 0 && s_id[pr] < p.E) {
+                float v = s_sum[pr * 16 + col];
                 for (int sl = 1; sl < slices; ++sl)
-                    v += s_sum[(sl * P + pr) * 32 + col];
-                y = __builtin_fmaf(p.weights[pr], v, y);
+                    v += s_sum[(sl * P + pr) * 16 + col];
+                y = __builtin_fmaf(s_weight[pr], v, y);
             }
         }
         p.out[(int64_t)t * p.ldo + n0 + col] = f32_to_bf16(y);
@@ -392,76 +487,88 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
 // first parts of the set's pairs, then the second parts; the sums of each pair go
 // to moe_combine_kernel.
 template <int kPairs>
-__device__ __forceinline__ void down_set(const DownArgs &p, WeightStream &ws, RunCursor &cursor, int set, int q0,
-                                         int q1, bool start, Shared &s)
+__device__ __forceinline__ void down_set(const DownArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
+                                         int q1, Shared &s)
 {
-    constexpr int kRows = 2 * kPairs, kRegs = ARows<kRows>::kRegs;
+    constexpr int kRows = 2 * kPairs;
+    const int set = q0 / r.units - r.first_set;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
         const int pr = s.pairs[set][min(row % kPairs, count - 1)];
         return __builtin_bit_cast(u32x4, act_order8(*reinterpret_cast<const u32x4 *>(
                                              p.hidden + ((int64_t)pr * 2 + row / kPairs) * p.I + ch * 8)));
     };
-    const auto done = [&](int tile, const float(&tot)[kRegs]) {
+    const auto done = [&](int tile, const float(&tot)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // The second parts are in the other half of the wave (4 pairs) or the other four registers (8).
-            const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i] + tot[kRegs - 4 + i];
+            // Of four pairs the second parts are in the other half of the wave.
+            const float v = kPairs == 4 ? tot[i] + __shfl_xor(tot[i], 32) : tot[i];
             const int at = kPairs == 4 ? i : 4 * half + i;
             if (at < count && (kPairs > 4 || half == i / 2))
                 p.y[(int64_t)s.pairs[set][at] * p.H + tile * 32 + l32] = v;
         }
+        return min(4, count);
     };
-    stream_set<kRows>(ws, cursor, p.z2 != nullptr, q0, q1, start, s, load, done);
+    stream_set<kRows>(ws, cursor, r, p.z2 != nullptr, q0, q1, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    const int tiles = p.H / 32, octets = (tiles + kWaves - 1) / kWaves, G = p.I / 64;
-    const Run r = plan_run(p.ids, p.T * p.k, p.E, octets, s);
-    WeightStream ws(p.w2, p.s2, p.z2, p.H, G, 16, s.ring[threadIdx.x / kWave]);
-    RunCursor cursor(r, s, octets, tiles, 32, stage_groups(G) / kStageGroups);
+    const int tiles = p.H / 32;
+    WeightStream<> ws(p.w2, p.s2, p.z2, p.H, p.I / 64, 16, s.ring[threadIdx.x / kWave]);
+    const Run r = plan_run(p.ids, p.T * p.k, p.k, p.E, tiles, ws.stages(), p.I * 2 * kSetPairs <= kChunkElems, s);
+    RunCursor cursor(r, s, tiles, 32, ws.stages());
     for (int q = r.q0; q < r.q1;) {
-        const int set = q / octets - r.first_set, end = min(r.q1, (q / octets + 1) * octets);
-        if (s.count[set] <= 4)
-            down_set<4>(p, ws, cursor, set, q, end, q == r.q0, s);
+        const int end = min(r.q1, (q / r.units + 1) * r.units);
+        if (s.count[q / r.units - r.first_set] <= 4)
+            down_set<4>(p, ws, cursor, r, q, end, s);
         else
-            down_set<8>(p, ws, cursor, set, q, end, q == r.q0, s);
+            down_set<8>(p, ws, cursor, r, q, end, s);
         q = end;
     }
 }
 
-// out[t] = sum over the slots, in order; four columns a thread.
-__global__ __launch_bounds__(256) void moe_combine_kernel(const DownArgs p)
+// out[t] = sum over the slots, in order; four columns a thread, a token a grid row.
+// Eight slots' loads are in flight at a time.
+__global__ __launch_bounds__(64) void moe_combine_kernel(const DownArgs p)
 {
-    const int per = p.H / 4;
-    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (o >= (int64_t)p.T * per)
+    const int t = blockIdx.y, n = (blockIdx.x * 64 + threadIdx.x) * 4;
+    if (n >= p.H)
         return;
-    const int t = (int)(o / per), n = (int)(o % per) * 4;
     v4f y = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < p.k; ++j) {
-        const int pr = t * p.k + j, e = p.ids[pr];
-        if (e >= 0 && e < p.E) {
-            const v4f v = *reinterpret_cast<const v4f *>(p.y + (int64_t)pr * p.H + n);
-            const float w = p.weights[pr];
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        v4f v[8];
+        float w[8];
+        bool live[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[i] = __builtin_fmaf(w, v[i], y[i]);
+        for (int j = 0; j < 8; ++j) {
+            const int pr = t * p.k + min(j0 + j, p.k - 1), e = p.ids[pr];
+            live[j] = j0 + j < p.k && e >= 0 && e < p.E;
+            w[j] = p.weights[pr];
+            v[j] = v4f{0.f, 0.f, 0.f, 0.f};
+            if (live[j])
+                v[j] = *reinterpret_cast<const v4f *>(p.y + (int64_t)pr * p.H + n);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (live[j])
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = __builtin_fmaf(w[j], v[j][i], y[i]);
     }
     *reinterpret_cast<u32x2 *>(p.out + (int64_t)t * p.ldo + n) = u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
-// More than 64 KiB of dynamic LDS needs the kernel's attribute raised once.
-constexpr int kMaxLds = 150 * 1024, kCus = 256;
-template <auto kernel>
+// More than 64 KiB of dynamic LDS needs the kernel's attribute raised once; a
+// kernel's static LDS counts against the CU's 160 KiB too.
+constexpr int kMaxLds = 160 * 1024, kCus = 256;
+template <auto kernel, int bytes = kMaxLds>
 hipError_t allow_lds()
 {
     static const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     return e;
 }
 
@@ -469,7 +576,7 @@ template <int kNe, bool kBf16>
 hipError_t launch_up_few(const UpArgs &a, hipStream_t s)
 {
     constexpr auto kernel = moe_up_few_kernel<kNe, kBf16>;
-    const hipError_t e = allow_lds<kernel>();
+    const hipError_t e = allow_lds<kernel, kMaxLds - 1024>();
     if (e != hipSuccess)
         return e;
     const int runs = a.P * (a.I / 64);  // of four workgroups, rounded up to whole rounds of the XCDs
@@ -507,38 +614,33 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
     uint16_t *hidden = static_cast<uint16_t *>(ws);
     float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + moe_hidden_bytes(P, w.I));
 
-    const int few_lds = kFewWaves * kRingBytes + 2 * P * stage_groups(w.I / 64) * (128 + 4) +
-                        (P > kFewWaves ? P : kFewWaves) * 32 * 4;
-    const bool few = P <= kMoeFewPairs && few_lds <= kMaxLds;
+    const int few_lds = few_down_lds(P < kMoeFewPairs ? P : kMoeFewPairs, w.I / 64);
+    const bool few = P <= kMoeFewPairs && few_lds <= kMaxLds - 1024;
     if (r.logits && !few) {
         const int e = launch_moe_route(r.logits, r.bf16, T, w.E, r.ldl, r.k, r.renormalize, r.ids, r.weights, stream);
         if (e != 0)
             return e;
     }
     const UpArgs ua{x, ldx, r.k, w.w1, w.s1, w.z1, w.E, w.H, w.I, P, r, hidden};
-    // One workgroup a CU, and no more than there can be octets; at most kMaxSets
-    // sets a workgroup, which 256 workgroups keep to by far (up to 1152 sets).
-    const int most_sets = (w.E < P ? w.E : P) + P / kSetPairs;
-    const auto grid = [&](int tiles) {
-        const int64_t octets = (int64_t)most_sets * ((tiles + kWaves - 1) / kWaves);
-        return octets < kCus ? (int)octets : kCus;
-    };
+    // One workgroup a CU, and no more than there can be units.  A run has at most
+    // kMaxSets sets: 256 runs of up to 1152 sets, or less than a unit each.
+    const int64_t most_sets = (w.E < P ? w.E : P) + P / kSetPairs;
+    const auto grid = [&](int tiles) { return most_sets * tiles < kCus ? (int)most_sets * tiles : kCus; };
     hipError_t e = launch_up(ua, few, grid(w.I / 16), s);
     if (e != hipSuccess)
         return (int)e;
     const DownArgs da{hidden, w.w2, w.s2, w.z2, w.E, w.H, w.I, T, r.k, r.ids, r.weights, y, out, ldo};
     if (few) {
-        e = allow_lds<moe_down_few_kernel>();
+        e = allow_lds<moe_down_few_kernel, kMaxLds - 1024>();
         if (e != hipSuccess)
             return (int)e;
-        hipLaunchKernelGGL(moe_down_few_kernel, dim3(w.H / 32), dim3(kFewWaves * kWave), few_lds, s, da);
+        hipLaunchKernelGGL(moe_down_few_kernel, dim3(w.H / 16), dim3(kFewWaves * kWave), few_lds, s, da);
     } else {
         e = allow_lds<moe_down_kernel>();
         if (e != hipSuccess)
             return (int)e;
         hipLaunchKernelGGL(moe_down_kernel, dim3(grid(w.H / 32)), dim3(kWaves * kWave), sizeof(Shared), s, da);
-        const int64_t quads = (int64_t)T * (w.H / 4);
-        hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, s, da);
+        hipLaunchKernelGGL(moe_combine_kernel, dim3((w.H / 4 + 63) / 64, T), dim3(64), 0, s, da);
     }
     return (int)hipGetLastError();
 }

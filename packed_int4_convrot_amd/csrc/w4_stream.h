@@ -18,6 +18,7 @@
 // row's low bits, so that the operand reads are free of bank conflicts.
 #pragma once
 
+#include "gemv_reduce.h"
 #include "rows_device.h"
 
 namespace ck {
@@ -28,7 +29,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 constexpr int kStageGroups = 4;
 constexpr int kStageScales = 4096;               // byte offset of [group][s, z][32 rows] bf16
 constexpr int kStageBytes = kStageScales + 512;
-constexpr int kStages = 2;
+constexpr int kStages = 2;                       // of a ring, unless a kernel asks for more
 constexpr int kRingBytes = kStages * kStageBytes;
 
 __device__ __forceinline__ v16f mfma32(v8bf a, v8bf b, v16f c)
@@ -41,26 +42,38 @@ __host__ __device__ constexpr int stage_groups(int groups)
     return (groups + kStageGroups - 1) / kStageGroups * kStageGroups;
 }
 
-// Packed weights [experts][N, 32 G] bytes with scales [experts][G, N], read by
-// tiles of 32 rows of one expert: n0 .. n0 + 15 and n0 + far .. n0 + far + 15.
-// A cursor says which stages to read: next() sets the tile of the next stage and
-// its number, or returns false at the end.
+// Packed weights [experts][N, 32 row_groups] bytes with scales [experts][row_groups,
+// N], read by tiles of 32 "rows" of one expert: 16 from row n0 on and 16 far
+// ones, which are either rows far away (gate and up) or the second half of the
+// same rows' columns.  A cursor says which stages to read: next() sets the tile of
+// the next stage and its number, or returns false at the end.
+template <int kDepth = kStages>
 struct WeightStream {
     const uint8_t *packed, *w;      // w, sz: this lane's row of each eight, and its
     const uint16_t *s, *z, *sz;     // 8 scales or zero points of group 0, in the tile
-    int64_t far_bytes;
-    int row_bytes, G, N, far, slot;
+    int64_t far_bytes, far_scale;
+    int row_bytes, row_groups, N, slot;
+    int G, far_G;                   // groups of the near and the far rows
     int place, use;                 // ring slots of the next to issue and to consume
     int ahead;                      // stages issued and not consumed
     bool scales, zero_point;        // this lane loads scales; they are zero points
     lds_u8 *ring;
 
+    // far > 0: the far rows are `far` rows on; 0: column halves.
     __device__ __forceinline__ WeightStream(const uint8_t *packed_, const uint16_t *s_, const uint16_t *z_, int rows,
-                                            int groups, int far_, void *lds)
+                                            int groups, int far, void *lds)
     {
         const int lane = threadIdx.x % kWave;
-        packed = packed_, s = s_, z = z_, G = groups, N = rows, far = far_, row_bytes = 32 * groups;
-        far_bytes = (int64_t)far * row_bytes;
+        packed = packed_, s = s_, z = z_, N = rows, row_groups = groups, row_bytes = 32 * groups;
+        if (far > 0) {
+            G = far_G = groups;
+            far_bytes = (int64_t)far * row_bytes, far_scale = far;
+        } else {
+            G = (groups + 1) / 2, far_G = groups - G;
+            far_bytes = (int64_t)G * 32, far_scale = (int64_t)G * rows;
+            if (far_G == 0)  // a single group: the far rows meet zeros
+                far_G = G, far_bytes = far_scale = 0;
+        }
         slot = (lane % 8) ^ (lane / 8);
         zero_point = lane / 4 % 2;
         scales = lane < 32 && (z || !zero_point);
@@ -71,30 +84,34 @@ struct WeightStream {
     {
         const int lane = threadIdx.x % kWave, piece = lane % 4;
         w = packed + ((int64_t)expert * N + n0 + lane / 8) * row_bytes;
-        sz = (zero_point && z ? z : s) + (int64_t)expert * G * N + n0 + piece % 2 * 8 + piece / 2 * far;
+        sz = (zero_point && z ? z : s) + (int64_t)expert * row_groups * N + n0 + piece % 2 * 8 +
+             piece / 2 * far_scale;
     }
+    __device__ __forceinline__ int stages() const { return (G + kStageGroups - 1) / kStageGroups; }
     // Global -> ring for one stage of the tile (past the row's end the last columns
     // again, which meet zeros): five instructions.
     __device__ __forceinline__ void issue(int stage)
     {
         lds_u8 *to = ring + place * kStageBytes;
-        const uint8_t *from = w + 16 * min(stage * 8 + slot, 2 * G - 1);
+        const uint8_t *near = w + 16 * min(stage * 8 + slot, 2 * G - 1);
+        const uint8_t *far = w + far_bytes + 16 * min(stage * 8 + slot, 2 * far_G - 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_global_load_lds(from + i / 2 * far_bytes + i % 2 * 8 * row_bytes,
+            __builtin_amdgcn_global_load_lds((i < 2 ? near : far) + i % 2 * 8 * row_bytes,
                                              (__attribute__((address_space(3))) void *)(to + i * 1024), 16, 0, 0);
-        const int g = min(stage * kStageGroups + (int)(threadIdx.x % 32) / 8, G - 1);
+        const int lane = threadIdx.x % kWave;
+        const int g = min(stage * kStageGroups + lane % 32 / 8, (lane % 4 < 2 ? G : far_G) - 1);
         if (scales)
             __builtin_amdgcn_global_load_lds(sz + (int64_t)g * N,
                                              (__attribute__((address_space(3))) void *)(to + kStageScales), 16, 0, 0);
-        place = place + 1 == kStages ? 0 : place + 1;
+        place = place + 1 == kDepth ? 0 : place + 1;
         ++ahead;
     }
     template <class Cursor>
     __device__ __forceinline__ void start(Cursor &cursor)
     {
 #pragma unroll
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kDepth; ++i) {
             int stage;
             if (cursor.next(*this, stage))
                 issue(stage);
@@ -105,26 +122,43 @@ struct WeightStream {
 // Cursor over stages [st, end) of the tile that is set.
 struct OneTile {
     int st, end;
-    __device__ __forceinline__ bool next(WeightStream &, int &stage)
+    template <class Stream>
+    __device__ __forceinline__ bool next(Stream &, int &stage)
     {
         stage = st;
         return st++ < end;
     }
 };
 
-// Waits for a stage behind which `newer` more have been issued: loads retire in
-// order, five instructions a stage.
-__device__ __forceinline__ void wait_stage(int newer)
+// Waits for a stage behind which `newer` more have been issued, and at least
+// `stores` (0, 2, 4 or 8) vector stores: they retire in order, five instructions a
+// stage.  A count that is too low only waits for more.
+template <int kCount>
+__device__ __forceinline__ void wait_vmcnt_n()
 {
-    static_assert(kStages <= 4, "vmcnt");
-    if (newer >= 3)
-        __builtin_amdgcn_s_waitcnt(15 | 0x0F70);
-    else if (newer == 2)
-        __builtin_amdgcn_s_waitcnt(10 | 0x0F70);
-    else if (newer == 1)
-        __builtin_amdgcn_s_waitcnt(5 | 0x0F70);
+    static_assert(kCount < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((kCount & 15) | (kCount >> 4 << 14) | 0x0F70);
+}
+template <int kNewer>
+__device__ __forceinline__ void wait_behind(int stores)
+{
+    if (stores >= 8)
+        wait_vmcnt_n<5 * kNewer + 8>();
+    else if (stores >= 4)
+        wait_vmcnt_n<5 * kNewer + 4>();
+    else if (stores >= 2)
+        wait_vmcnt_n<5 * kNewer + 2>();
     else
-        wait_vmcnt0();
+        wait_vmcnt_n<5 * kNewer>();
+}
+__device__ __forceinline__ void wait_stage(int newer, int stores)
+{
+    if (newer >= 2)
+        wait_behind<2>(stores);
+    else if (newer == 1)
+        wait_behind<1>(stores);
+    else
+        wait_behind<0>(stores);
 }
 // This wave's LDS reads have returned.
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
@@ -140,20 +174,25 @@ struct ARows {
 
 // Stages [st0, st1) of a tile, the stream's next to consume, added to tot; the
 // cursor's next stages are issued behind them.  A's first group is group a0.
-// after_first() runs between the first stage's reads and the issue behind it:
-// stores there are a stage old when they are waited for.
-template <int kRows, class Cursor, class Hook>
-__device__ __forceinline__ void stream_stages(WeightStream &ws, Cursor &cursor, bool zeros, int st0, int st1, int a0,
-                                              const ARows<kRows> &A, float (&tot)[ARows<kRows>::kRegs],
+// after_first() runs between the first stage's reads and the issue behind it and
+// returns how many vector stores it issued at least: the next stage is older than
+// they are, so the wait for it lets them be outstanding.
+template <int kRows, int kDepth, class Cursor, class Hook>
+__device__ __forceinline__ void stream_stages(WeightStream<kDepth> &ws, Cursor &cursor, bool zeros, int st0, int st1,
+                                              int a0, const ARows<kRows> &A, float (&tot)[ARows<kRows>::kRegs],
                                               Hook &&after_first)
 {
+    static_assert(kDepth <= 3, "wait_stage");
     constexpr int kRegs = ARows<kRows>::kRegs;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
+    int stores = 0;
     for (int st = st0; st < st1; ++st) {
-        wait_stage(ws.ahead - 1);
+        // With more than two stages in flight the stores would be behind several.
+        wait_stage(ws.ahead - 1, kDepth == 2 ? stores : 0);
+        stores = 0;
         __builtin_amdgcn_sched_barrier(0);
         const lds_u8 *stage = ws.ring + ws.use * kStageBytes;
-        ws.use = ws.use + 1 == kStages ? 0 : ws.use + 1;
+        ws.use = ws.use + 1 == kDepth ? 0 : ws.use + 1;
         --ws.ahead;
         // The stage into registers first, so that the next one can be issued into
         // its slot before the multiplication.
@@ -169,7 +208,7 @@ __device__ __forceinline__ void stream_stages(WeightStream &ws, Cursor &cursor, 
         wait_lds();
         __builtin_amdgcn_sched_barrier(0);
         if (st == st0)
-            after_first();
+            stores = after_first();
         int next;
         if (cursor.next(ws, next))
             ws.issue(next);
@@ -203,13 +242,17 @@ __device__ __forceinline__ void put_chunk(uint8_t *operands, float *sums, int ro
 {
     const int g = ch / 8, half = ch / 4 % 2, j = ch % 4;
     *reinterpret_cast<u32x4 *>(operands + ((g * 8 + 2 * j + half) * kRows + row) * 16) = v;
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
     float t = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        t += bf16_to_f32(v[q] & 0xffffu) + __uint_as_float(v[q] & 0xffff0000u);
-#pragma unroll
-    for (int b = 1; b < 8; b <<= 1)
-        t += __shfl_xor(t, b);
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t pair = v[q];  // times (1, 1)
+        t = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, pair), __builtin_bit_cast(v2bf, 0x3F803F80u), t,
+                                            false);
+    }
+    t += __uint_as_float(lane_xor_u<1>(__float_as_uint(t)));
+    t += __uint_as_float(lane_xor_u<2>(__float_as_uint(t)));
+    t += __uint_as_float(lane_mirror8_u(__float_as_uint(t)));
     if (ch % 8 == 0)
         sums[g * kRows + row] = t;
 }
