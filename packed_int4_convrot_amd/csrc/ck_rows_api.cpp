@@ -193,9 +193,7 @@ int ck_lora_add_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const
     CK_TRY(check_out(fn, out, N, ldo, 2));
     if (base && (ldb < N || ldb % 8 != 0 || !aligned(base, 16)))
         return fail(CK_ERR_INVALID_ARG, "%s: base must be 16-byte aligned with ldb >= N, ldb %% 8 == 0", fn);
-    // The second product starts a workgroup of 256 threads per 64 rows (per row
-    // for few rows) and 256 (128) columns.
-    if (((M + 63) / 64) * ((N + 127) / 128) >= (int64_t(1) << 22))
+    if (ck::lora_blocks(M, N, L) >= (int64_t(1) << 24))
         return fail(CK_ERR_UNSUPPORTED, "%s: M * N too large for one launch (M=%lld, N=%lld)", fn, (long long)M,
                     (long long)N);
     const size_t need = lora_workspace(M, K, R, L);

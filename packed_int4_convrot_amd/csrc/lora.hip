@@ -1,69 +1,70 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   out[m] = base[m] + scaling[a] B_a (A_a x_m),  a = index[m] (outside [0, L): base[m]).
 //
-// Two launches.  The first forms v = A_a x_m (fp32, in parts of the K columns so
-// that few rows still fill the chip), the second adds B_a v to base.  Rows of
-// one adapter share its weights: the 64 lanes of a wave read the indices of a
-// window of rows, a ballot gives the rows of one adapter, and those rows
-// (wherever they lie in the window) fill the 16-row tiles of the bf16 MFMA.
-//   * up to kPerRowMax rows (decode), a workgroup is started for every row and
-//     the first row of each adapter in the window does the work for all of
-//     them: requests of unlike adapters run side by side;
-//   * above (prompts, where neighbours share an adapter), a workgroup
-//     takes a window and goes through its adapters one after the other.
-// v enters the second product as two bf16 (16 significant bits) side by side in
-// the MFMA's 32 columns of k: columns 0-15 the first parts, 16-31 the second,
-// both against the same 16 columns of B_a.
+// Two launches: v = A_a x_m (fp32, in parts of the K columns so that few rows still
+// fill the chip), then base + B_a v.  Rows of one adapter share its weights: the 64
+// lanes of a wave read the indices of a window of rows, a ballot gives the rows of
+// one adapter (a set), and those rows, wherever they lie in the window, fill
+// the 16-row tiles of the bf16 MFMA.  Few rows: a workgroup is started for every
+// set a window can have, so that requests of unlike adapters run side by
+// side; many rows (prompts, where neighbours share an adapter): a workgroup goes
+// through the sets of its window.
 // The work is bound by memory: x, base and out once, the used adapters once.
+#include <type_traits>
+
 #include "rows_device.h"
 #include "rows_launch.h"
 
 namespace ck {
 namespace {
 
-constexpr int64_t kPerRowMax = kLoraPerRowMax;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
 constexpr int kRankBlock = kLoraRankBlock;  // ranks per workgroup (first product) or pass (second)
 
-// The rows of a window of kWin, and those that share one adapter.
+// The rows of a window that share one adapter.
 struct RowSet {
-    int order;  // lane i: the i-th row of the set (window-relative)
+    int adapter;  // -1: none
+    int order;    // lane i: the i-th row of the set (window-relative)
     int count;
 };
-__device__ __forceinline__ int window_adapter(const int32_t *index, int64_t M, int64_t L, int64_t row0, int win,
-                                              int lane)
+
+// Lane i: the adapter of the window's row i (-1: none, -2: no such row).
+__device__ __forceinline__ int window_adapter(const int32_t *index, int64_t M, int64_t L, int64_t row0, int win)
 {
+    const int lane = threadIdx.x % kWave;
     if (lane >= win || row0 + lane >= M)
         return -2;
     const int a = index[row0 + lane];
     return a < 0 || a >= L ? -1 : a;
 }
-__device__ __forceinline__ RowSet row_set(uint64_t mask, int lane)
+// The set of the window's first row in `left`, which it leaves.
+__device__ __forceinline__ RowSet take_set(int mine, uint64_t &left)
 {
-    const uint64_t below = (uint64_t(1) << lane) - 1;
-    const int count = __builtin_popcountll(mask);
+    const int lane = threadIdx.x % kWave;
+    RowSet r;
+    r.adapter = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    const uint64_t mask = __ballot(mine == r.adapter), below = (uint64_t(1) << lane) - 1;
+    left &= ~mask;
+    r.count = __builtin_popcountll(mask);
     const int pos = (mask >> lane) & 1 ? __builtin_popcountll(mask & below)
-                                       : count + __builtin_popcountll(~mask & below);
-    return RowSet{__builtin_amdgcn_ds_permute(4 * pos, lane), count};
+                                       : r.count + __builtin_popcountll(~mask & below);
+    r.order = __builtin_amdgcn_ds_permute(4 * pos, lane);
+    return r;
 }
-
-// Calls f(adapter, rows) for each adapter of the window, or, per row, for the
-// adapter whose first row this workgroup was started for.
-template <bool kPerRow, class F>
-__device__ __forceinline__ void for_adapters(int mine, int me, int lane, F &&f)
+// Calls f for the slot-th set of a window (kSlots), if there is one, or for all.
+template <bool kSlots, class F>
+__device__ __forceinline__ void for_sets(int mine, int slot, F &&f)
 {
     uint64_t left = __ballot(mine != -2);
-    if constexpr (kPerRow) {
-        const int a = __builtin_amdgcn_readlane(mine, me);
-        const uint64_t mask = __ballot(mine == a);
-        if (__builtin_ctzll(mask) == me)
-            f(a, row_set(mask, lane));
+    if constexpr (kSlots) {
+        for (int i = 0; i < slot && left; ++i)
+            left &= ~__ballot(mine == __builtin_amdgcn_readlane(mine, __builtin_ctzll(left)));
+        if (left)
+            f(take_set(mine, left));
     } else {
-        while (left) {
-            const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-            const uint64_t mask = __ballot(mine == a);
-            left &= ~mask;
-            f(a, row_set(mask, lane));
-        }
+        while (left)
+            f(take_set(mine, left));
     }
 }
 
@@ -72,137 +73,260 @@ __device__ __forceinline__ int adapter_rank(const int32_t *ranks, int a, int R)
     return ranks ? min(max(ranks[a], 0), R) : R;
 }
 
-// First product.  Grid: (rows or windows, parts of K, blocks of 64 ranks); the
-// workgroup's waves split its part of K and are summed through LDS.
-template <bool kPerRow, int kWaves, int kTiles>
-__global__ __launch_bounds__(kWaves * kWave) void lora_shrink_kernel(
-    const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, const int32_t *__restrict__ index, int64_t L,
-    int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
-{
-    constexpr int kWin = kPerRow ? kLoraWindow : 16 * kTiles;
-    constexpr int kRT = kRankBlock / 16;
-    __shared__ float s_red[kWaves][kTiles][kRT][256];
-    __shared__ int s_rows[kWave];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int l16 = lane % 16, quarter = lane / 16;
-    const int64_t row0 = kPerRow ? (int64_t)blockIdx.x / kWin * kWin : (int64_t)blockIdx.x * kWin;
-    const int rb = blockIdx.z * kRankBlock;
-    const int KG = K / 64, parts = gridDim.y * kWaves, part = blockIdx.y * kWaves + wave;
-    const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
-    const int mine = window_adapter(index, M, L, row0, kWin, lane);
+// ---------------------------------------------------------------- first product
 
-    for_adapters<kPerRow>(mine, (int)(blockIdx.x % kWin), lane, [&](int ad, RowSet rows) {
-        if (ad < 0)
+constexpr int kRT = kRankBlock / 16;
+
+// Sums over the waves of the 16-row, 16-rank tiles in s_red, to v.
+template <int kWaves, int kTiles>
+__device__ __forceinline__ void store_v(const float (&s_red)[kWaves][kTiles][kRT][256], const int *s_rows, int p0, int count,
+                                        int nrt, int rb, int rank, int R, int64_t row0, float *v)
+{
+    for (int o = threadIdx.x; o < kTiles * nrt * 256; o += kWaves * kWave) {
+        const int r = o % 16, row = o / 16 % 16, tile = o / 256, rt = tile % nrt, mt = tile / nrt;
+        const int p = p0 + 16 * mt + row;
+        if (p < count && rb + 16 * rt + r < rank) {
+            const int at = (row % 4) * kWave + (row / 4) * 16 + r;
+            float t = s_red[0][mt][rt][at];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w)
+                t += s_red[w][mt][rt][at];
+            v[(row0 + s_rows[p]) * R + rb + 16 * rt + r] = t;
+        }
+    }
+}
+
+// Few rows.  Grid: (windows x slots, parts of K, blocks of 64 ranks); the
+// workgroup's waves split its part of K.  Operands come straight to registers:
+// these calls are bound by latency, not by the address path.
+constexpr int kFewShrinkWaves = 4;
+
+template <int kTiles>
+__device__ __forceinline__ void shrink_rows(const RowSet &rows, int p0, int64_t row0, const uint16_t *x, int64_t ldx,
+                                            const uint16_t *const (&arow)[kRT], int nrt, int g0, int g1,
+                                            float (&s_red)[kFewShrinkWaves][kTiles][kRT][256])
+{
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
+    const uint16_t *xrow[kTiles];
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+        xrow[mt] = x + (row0 + __shfl(rows.order, min(p0 + 16 * mt + l16, rows.count - 1))) * ldx + 16 * quarter;
+    v4f acc[kTiles][kRT];
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+            acc[mt][rt] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int g = g0; g < g1; ++g) {
+        u32x4 xv[kTiles][2], av[kRT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int mt = 0; mt < kTiles; ++mt)
+                xv[mt][h] = *reinterpret_cast<const u32x4 *>(xrow[mt] + g * 64 + 8 * h);
+#pragma unroll
+            for (int rt = 0; rt < kRT; ++rt)
+                if (rt < nrt)
+                    av[rt][h] = *reinterpret_cast<const u32x4 *>(arow[rt] + g * 64 + 8 * h);
+        }
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+            if (rt < nrt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int mt = 0; mt < kTiles; ++mt)
+                        acc[mt][rt] = mfma16(__builtin_bit_cast(v8bf, xv[mt][h]), __builtin_bit_cast(v8bf, av[rt][h]),
+                                             acc[mt][rt]);
+    }
+#pragma unroll
+    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+            if (rt < nrt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s_red[wave][mt][rt][i * kWave + lane] = acc[mt][rt][i];
+}
+
+__global__ __launch_bounds__(kFewShrinkWaves * kWave) void lora_shrink_few_kernel(
+    const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, const int32_t *__restrict__ index, int64_t L,
+    int slots, int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
+{
+    __shared__ float s_red[kFewShrinkWaves][2][kRT][256];
+    __shared__ int s_rows[kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
+    const int64_t row0 = (int64_t)(blockIdx.x / slots) * kLoraWindow;
+    const int rb = blockIdx.z * kRankBlock;
+    const int KG = K / 64, parts = gridDim.y * kFewShrinkWaves, part = blockIdx.y * kFewShrinkWaves + wave;
+    const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
+    const int mine = window_adapter(index, M, L, row0, kLoraWindow);
+    for_sets<true>(mine, blockIdx.x % slots, [&](const RowSet &rows) {
+        if (rows.adapter < 0)
             return;
-        const int rank = adapter_rank(ranks, ad, R);
+        const int rank = adapter_rank(ranks, rows.adapter, R);
         if (rank <= rb)
             return;
         const int nrt = min(kRT, (rank - rb + 15) / 16);
         const uint16_t *arow[kRT];
 #pragma unroll
         for (int rt = 0; rt < kRT; ++rt)
-            arow[rt] = a_w + ((int64_t)ad * R + min(rb + 16 * rt + l16, rank - 1)) * K + 16 * quarter;
-        for (int p0 = 0; p0 < rows.count; p0 += 16 * kTiles) {
-            const uint16_t *xrow[kTiles];
-#pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
-                xrow[mt] = x + (row0 + __shfl(rows.order, min(p0 + 16 * mt + l16, rows.count - 1))) * ldx + 16 * quarter;
-            v4f acc[kTiles][kRT];
-#pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                for (int rt = 0; rt < kRT; ++rt)
-                    acc[mt][rt] = v4f{0.f, 0.f, 0.f, 0.f};
-            for (int g = g0; g < g1; ++g) {
-                v8bf xv[kTiles][2];
-#pragma unroll
-                for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        xv[mt][h] = __builtin_bit_cast(
-                            v8bf, *reinterpret_cast<const u32x4 *>(xrow[mt] + g * 64 + 8 * h));
-#pragma unroll
-                for (int rt = 0; rt < kRT; ++rt) {
-                    if (rt < nrt) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const v8bf av = __builtin_bit_cast(
-                                v8bf, *reinterpret_cast<const u32x4 *>(arow[rt] + g * 64 + 8 * h));
-#pragma unroll
-                            for (int mt = 0; mt < kTiles; ++mt)
-                                acc[mt][rt] = mfma16(xv[mt][h], av, acc[mt][rt]);
-                        }
-                    }
-                }
-            }
-            __syncthreads();  // the previous tile's sums and rows have been read
-            if (wave == 0)
-                s_rows[lane] = rows.order;
-#pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                for (int rt = 0; rt < kRT; ++rt)
-                    if (rt < nrt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s_red[wave][mt][rt][i * kWave + lane] = acc[mt][rt][i];
+            arow[rt] = a_w + ((int64_t)rows.adapter * R + min(rb + 16 * rt + l16, rank - 1)) * K + 16 * quarter;
+        if (wave == 0)
+            s_rows[lane] = rows.order;
+        float *to = v + (int64_t)blockIdx.y * M * R;
+        if (rows.count <= 16) {
+            float(&red)[kFewShrinkWaves][1][kRT][256] =
+                *reinterpret_cast<float(*)[kFewShrinkWaves][1][kRT][256]>(&s_red);
+            shrink_rows<1>(rows, 0, row0, x, ldx, arow, nrt, g0, g1, red);
             __syncthreads();
-            // Threads in the order (tile, row, rank tile, rank): 16-rank runs.
-            for (int o = threadIdx.x; o < kTiles * 16 * nrt * 16; o += kWaves * kWave) {
-                const int r = o % 16, rt = o / 16 % nrt, row = o / (16 * nrt) % 16, mt = o / (256 * nrt);
-                const int p = p0 + 16 * mt + row;
-                if (p < rows.count && rb + 16 * rt + r < rank) {
-                    const int at = (row % 4) * kWave + (row / 4) * 16 + r;
-                    float t = s_red[0][mt][rt][at];
-#pragma unroll
-                    for (int w = 1; w < kWaves; ++w)
-                        t += s_red[w][mt][rt][at];
-                    v[((int64_t)blockIdx.y * M + row0 + s_rows[p]) * R + rb + 16 * rt + r] = t;
-                }
+            store_v<kFewShrinkWaves, 1>(red, s_rows, 0, rows.count, nrt, rb, rank, R, row0, to);
+        } else {
+            for (int p0 = 0; p0 < rows.count; p0 += 32) {
+                shrink_rows<2>(rows, p0, row0, x, ldx, arow, nrt, g0, g1, s_red);
+                __syncthreads();
+                store_v<kFewShrinkWaves, 2>(s_red, s_rows, p0, rows.count, nrt, rb, rank, R, row0, to);
+                __syncthreads();  // the sums have been read
             }
         }
     });
 }
 
-// The 8 ranks from r on of one row's v: parts summed in order, scaled, 0 from
-// `rank` on; the first or the second bf16 of each.
-__device__ __forceinline__ v8bf load_v8(const float *vrow, int64_t part_stride, int parts, int r, int rank,
-                                        float scale, bool second)
+// Larger sets.  Grid: (windows (x slots), parts of K, blocks of 64 ranks).  Each wave
+// streams its part of the columns of the set's rows of x and of the adapter's rows
+// through an LDS ring of its own: a stage is 64 columns, every instruction eight
+// rows of 128 contiguous bytes, with the 16-byte slots XORed by the row's low bits so
+// that the operand reads are free of bank conflicts.
+constexpr int kManyShrinkWaves = 4, kManyStages = 2, kMT = kLoraWindow / 16;
+constexpr int kManyStageBytes = (kLoraWindow + kRankBlock) * 128;
+
+// At most n instructions outstanding (n even, up to 16); they retire in order.
+__device__ __forceinline__ void wait_even(int n)
 {
-    float t[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        t[e] = 0.f;
-    if (r < rank) {  // v is written up to rank; the rest of its 8 are not used
-        for (int s = 0; s < parts; ++s) {
-            const float *p = vrow + s * part_stride + r;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const v4f u = *reinterpret_cast<const v4f *>(p + 4 * q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    t[4 * q + e] += u[e];
-            }
-        }
+    switch (n / 2) {
+    case 2: __builtin_amdgcn_s_waitcnt(4 | 0x0F70); break;
+    case 3: __builtin_amdgcn_s_waitcnt(6 | 0x0F70); break;
+    case 4: __builtin_amdgcn_s_waitcnt(8 | 0x0F70); break;
+    case 5: __builtin_amdgcn_s_waitcnt(10 | 0x0F70); break;
+    case 6: __builtin_amdgcn_s_waitcnt(12 | 0x0F70); break;
+    case 7: __builtin_amdgcn_s_waitcnt(14 | 0x0F70); break;
+    case 8: __builtin_amdgcn_s_waitcnt(0x4F70); break;  // 16
+    default: wait_vmcnt0(); break;
     }
-    u32x4 w;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint16_t hi[2], lo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            split_bf16(r + 2 * q + e < rank ? scale * t[2 * q + e] : 0.f, hi[e], lo[e]);
-        w[q] = second ? lo[0] | (uint32_t)lo[1] << 16 : hi[0] | (uint32_t)hi[1] << 16;
-    }
-    return __builtin_bit_cast(v8bf, w);
 }
 
-// The 8 ranks from r on of one row of B_a, 0 from `rank` on (whatever is stored there).
-__device__ __forceinline__ v8bf load_b8(const uint16_t *brow, int r, int rank)
+template <bool kSlots>
+__global__ __launch_bounds__(kManyShrinkWaves * kWave) void lora_shrink_many_kernel(
+    const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, const int32_t *__restrict__ index, int64_t L,
+    int slots, int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
 {
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (r < rank)
-        w = *reinterpret_cast<const u32x4 *>(brow + r);
+    // The rings; after the products, the waves' sums.
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring[kManyShrinkWaves][kManyStages * kManyStageBytes];
+    __shared__ int s_rows[kWave];
+    static_assert(sizeof s_ring >= kManyShrinkWaves * kMT * kRT * 256 * 4, "sums");
+    float(&s_red)[kManyShrinkWaves][kMT][kRT][256] =
+        *reinterpret_cast<float(*)[kManyShrinkWaves][kMT][kRT][256]>(&s_ring);
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
+    const int64_t row0 = (int64_t)(kSlots ? blockIdx.x / slots : blockIdx.x) * kLoraWindow;
+    const int rb = blockIdx.z * kRankBlock;
+    const int KG = K / 64, parts = gridDim.y * kManyShrinkWaves, part = blockIdx.y * kManyShrinkWaves + wave;
+    const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
+    const int mine = window_adapter(index, M, L, row0, kLoraWindow);
+    lds_u8 *ring = (lds_u8 *)s_ring[wave];
+    const int chunk = (lane % 8) ^ (lane / 8);
+    for_sets<kSlots>(mine, kSlots ? blockIdx.x % slots : 0, [&](const RowSet &rows) {
+        if (rows.adapter < 0)
+            return;
+        const int rank = adapter_rank(ranks, rows.adapter, R);
+        if (rank <= rb)
+            return;
+        const int nrt = min(kRT, (rank - rb + 15) / 16), nmt = (rows.count + 15) / 16;
+        const int each = 2 * nmt + 2 * nrt;  // instructions of a stage
+        // This lane's row of each eight of x, and of the adapter.
+        const uint16_t *xr[2 * kMT];
+#pragma unroll
+        for (int i = 0; i < 2 * kMT; ++i)
+            xr[i] = x + (row0 + __shfl(rows.order, min(8 * i + lane / 8, rows.count - 1))) * ldx + 8 * chunk;
+        const uint16_t *ar = a_w + ((int64_t)rows.adapter * R + rb) * K + 8 * chunk;
+        const auto issue = [&](int g, int place) {
+            lds_u8 *to = ring + place * kManyStageBytes;
+#pragma unroll
+            for (int i = 0; i < 2 * kMT; ++i)
+                if (i < 2 * nmt)
+                    __builtin_amdgcn_global_load_lds(
+                        xr[i] + g * 64, (__attribute__((address_space(3))) void *)(to + i * 1024), 16, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * kRT; ++i)
+                if (i < 2 * nrt)
+                    __builtin_amdgcn_global_load_lds(
+                        ar + (int64_t)min(8 * i + lane / 8, rank - rb - 1) * K + g * 64,
+                        (__attribute__((address_space(3))) void *)(to + (2 * kMT + i) * 1024), 16, 0, 0);
+        };
+        v4f acc[kMT][kRT];
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int rt = 0; rt < kRT; ++rt)
+                acc[mt][rt] = v4f{0.f, 0.f, 0.f, 0.f};
+        __syncthreads();  // the last set's sums have been read
+        if (g0 < g1)
+            issue(g0, 0);
+        for (int g = g0; g < g1; ++g) {
+            // The stage has landed once the newer one's instructions are all that is outstanding.
+            if (g + 1 < g1) {
+                issue(g + 1, (g + 1 - g0) % kManyStages);
+                wait_even(each);
+            } else {
+                wait_vmcnt0();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const lds_u8 *stage = ring + (g - g0) % kManyStages * kManyStageBytes;
+            const auto operand = [&](int row, int h) {
+                return __builtin_bit_cast(v8bf, *(__attribute__((address_space(3))) const u32x4 *)(
+                                                    stage + row * 128 + ((4 * h + quarter) ^ (row % 8)) * 16));
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v8bf av[kRT];
+#pragma unroll
+                for (int rt = 0; rt < kRT; ++rt)
+                    if (rt < nrt)
+                        av[rt] = operand(kLoraWindow + 16 * rt + l16, h);
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+                    if (mt < nmt) {
+                        const v8bf xv = operand(16 * mt + l16, h);
+#pragma unroll
+                        for (int rt = 0; rt < kRT; ++rt)
+                            if (rt < nrt)
+                                acc[mt][rt] = mfma16(xv, av[rt], acc[mt][rt]);
+                    }
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the stage has been read
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();  // the rings have been read
+        if (wave == 0)
+            s_rows[lane] = rows.order;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int rt = 0; rt < kRT; ++rt)
+                if (mt < nmt && rt < nrt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s_red[wave][mt][rt][i * kWave + lane] = acc[mt][rt][i];
+        __syncthreads();
+        store_v<kManyShrinkWaves, kMT>(s_red, s_rows, 0, rows.count, nrt, rb, rank, R, row0,
+                                       v + (int64_t)blockIdx.y * M * R);
+    });
+}
+
+// --------------------------------------------------------------- second product
+
+// The 8 ranks from r on of one row of B_a, 0 from `rank` on (whatever is stored there).
+__device__ __forceinline__ v8bf mask_ranks(u32x4 w, int r, int rank)
+{
     if (r + 8 > rank)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -210,88 +334,215 @@ __device__ __forceinline__ v8bf load_b8(const uint16_t *brow, int r, int rank)
     return __builtin_bit_cast(v8bf, w);
 }
 
-// Second product.  Grid: rows or windows, by columns / (32 kWaves kCols).  A wave
-// owns kCols tiles of 32 columns of the output; two MFMA tiles with interleaved
-// columns leave each lane 8 consecutive ones of its row, one 16-byte store.
-template <bool kPerRow, int kWaves, int kTiles, int kCols>
+// Grid: windows (x slots), by columns / (64 kWaves kCols).  The workgroup brings v of a
+// set's rows to LDS, scaled, as two bf16 a value (16 significant bits): per 16 ranks
+// 16 first parts, then 16 second parts, the 32 columns of k of one MFMA, whose
+// other operand is B_a's 16 ranks twice.  A wave then owns kCols tiles of 64 columns; the
+// sums of 16 rows go through LDS so that base and out are moved in 128-byte
+// runs of a row.
+template <bool kSlots, int kWaves, int kCols, int kSteps>
 __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
-    const float *__restrict__ v, int parts, int64_t M, const int32_t *__restrict__ index, int64_t L, int R,
+    const float *__restrict__ v, int parts, int64_t M, const int32_t *__restrict__ index, int64_t L, int slots, int R,
     const uint16_t *__restrict__ b_w, const float *__restrict__ scaling, const int32_t *__restrict__ ranks, int N,
     const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo)
 {
-    constexpr int kSteps = kRankBlock / 16;
+    constexpr int kPitch = 64 * 4 + 16;      // sums: 16 bytes on from row to row
+    constexpr int kAhead = kSlots ? 1 : 4;   // row tiles whose base is on its way
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ __attribute__((aligned(16))) uint8_t s_out[kWaves][16 * kPitch];
+    __shared__ int s_rows[kWave];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const int l16 = lane % 16, quarter = lane / 16;
-    const int ctiles = (N + 32 * kWaves * kCols - 1) / (32 * kWaves * kCols);
+    const int ctiles = (N + 64 * kWaves * kCols - 1) / (64 * kWaves * kCols);
     const int unit = blockIdx.x / ctiles;
-    const int64_t row0 = (int64_t)(kPerRow ? unit / kLoraWindow : unit) * kLoraWindow;
-    const int c0 = (blockIdx.x % ctiles * kWaves + wave) * 32 * kCols;
-    const int mine = window_adapter(index, M, L, row0, kLoraWindow, lane);
+    const int64_t row0 = (int64_t)(kSlots ? unit / slots : unit) * kLoraWindow;
+    const int c0 = (blockIdx.x % ctiles * kWaves + wave) * 64 * kCols;
+    const int vpitch = (R + 15) / 16 * 64 + 16;  // bytes of a row of v in LDS
+    const int mine = window_adapter(index, M, L, row0, kLoraWindow);
 
-    for_adapters<kPerRow>(mine, unit % kLoraWindow, lane, [&](int ad, RowSet rows) {
-        const int rank = ad < 0 ? 0 : adapter_rank(ranks, ad, R);
-        const float scale = ad >= 0 && scaling ? scaling[ad] : 1.f;
+    for_sets<kSlots>(mine, kSlots ? unit % slots : 0, [&](const RowSet &rows) {
+        const int rank = rows.adapter < 0 ? 0 : adapter_rank(ranks, rows.adapter, R);
+        const float scale = rows.adapter >= 0 && scaling ? scaling[rows.adapter] : 1.f;
         const int passes = max(1, (rank + kRankBlock - 1) / kRankBlock);
-        for (int p0 = 0; p0 < rows.count; p0 += 16 * kTiles) {
-            int64_t row[kTiles];
-            v8bf vf[kTiles][kSteps];
+        u32x4 bf[kSteps][4];
+        const auto load_b = [&](int n0, int pass) {
 #pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
-                row[mt] = row0 + __shfl(rows.order, min(p0 + 16 * mt + l16, rows.count - 1));
-            for (int ct = 0; ct < kCols; ++ct) {
-                const int n = c0 + 32 * ct + 8 * quarter;
-                if (c0 + 32 * ct >= N)
-                    break;
-                u32x4 bv[kTiles];
+            for (int st = 0; st < kSteps; ++st) {
+                const int r = pass * kRankBlock + 16 * st + 8 * (quarter % 2);
+                if (pass * kRankBlock + 16 * st < rank)
 #pragma unroll
-                for (int mt = 0; mt < kTiles; ++mt)
-                    bv[mt] = base && n < N ? *reinterpret_cast<const u32x4 *>(base + row[mt] * ldb + n)
-                                           : u32x4{0u, 0u, 0u, 0u};
-                v4f acc[kTiles][2];
-#pragma unroll
-                for (int mt = 0; mt < kTiles; ++mt)
-                    acc[mt][0] = acc[mt][1] = v4f{0.f, 0.f, 0.f, 0.f};
-                for (int pass = 0; pass < passes; ++pass) {
-                    const int r0 = pass * kRankBlock + 8 * (quarter % 2);
-                    if (ct == 0 || passes > 1) {
-#pragma unroll
-                        for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                            for (int st = 0; st < kSteps; ++st)
-                                if (pass * kRankBlock + 16 * st < rank)
-                                    vf[mt][st] = load_v8(v + row[mt] * R, M * R, parts, r0 + 16 * st, rank, scale,
-                                                         quarter >= 2);
+                    for (int h = 0; h < 4; ++h) {
+                        const int n = min(n0 + 16 * h + l16, N - 1);
+                        bf[st][h] = u32x4{0u, 0u, 0u, 0u};
+                        if (r < rank)
+                            bf[st][h] = *reinterpret_cast<const u32x4 *>(
+                                b_w + ((int64_t)rows.adapter * N + n) * R + r);
                     }
+            }
+        };
+        // base of a tile: two rows a lane, lane / 8 and 8 + lane / 8.
+        u32x4 bv[kAhead][2];
+        const auto load_base = [&](int n0, int p0, u32x4(&to)[2]) {
 #pragma unroll
-                    for (int st = 0; st < kSteps; ++st) {
-                        if (pass * kRankBlock + 16 * st < rank) {
+            for (int i = 0; i < 2; ++i) {
+                const int p = p0 + 8 * i + lane / 8, n = n0 + lane % 8 * 8;
+                const int row = __shfl(rows.order, p & 63);  // by every lane
+                to[i] = u32x4{0u, 0u, 0u, 0u};
+                if (base && p < rows.count && n < N)
+                    to[i] = *reinterpret_cast<const u32x4 *>(base + (row0 + row) * ldb + n);
+            }
+        };
+        if (c0 < N && passes == 1)
+            load_b(c0, 0);
+
+        if (!kSlots)
+            __syncthreads();  // the last set's v has been read
+        if (wave == 0)
+            s_rows[lane] = rows.order;
+        __syncthreads();
+        // v to LDS: a thread takes 8 ranks of a row, eight threads 64.
+        for (int p = threadIdx.x / 8; p < rows.count; p += kWaves * 8) {
+            for (int r = threadIdx.x % 8 * 8; r < rank; r += 64) {
+                float t[8];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int nb = min(c0 + 32 * ct + 8 * (l16 / 4) + 4 * h + l16 % 4, N - 1);
-                                const v8bf bf = load_b8(b_w + ((int64_t)ad * N + nb) * R, r0 + 16 * st, rank);
+                for (int e = 0; e < 8; ++e)
+                    t[e] = 0.f;
+                const float *from = v + (row0 + s_rows[p]) * R + r;
+#pragma unroll 4
+                for (int s = 0; s < parts; ++s, from += M * R)
 #pragma unroll
-                                for (int mt = 0; mt < kTiles; ++mt)
-                                    acc[mt][h] = mfma16(bf, vf[mt][st], acc[mt][h]);
+                    for (int q = 0; q < 2; ++q) {
+                        const v4f u = *reinterpret_cast<const v4f *>(from + 4 * q);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            t[4 * q + e] += u[e];
+                    }
+                u32x4 first, second;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint16_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)  // v is written up to rank
+                        split_bf16(r + 2 * q + e < rank ? scale * t[2 * q + e] : 0.f, hi[e], lo[e]);
+                    first[q] = hi[0] | (uint32_t)hi[1] << 16, second[q] = lo[0] | (uint32_t)lo[1] << 16;
+                }
+                uint8_t *to = smem + p * vpitch + r / 16 * 64 + r % 16 * 2;
+                *reinterpret_cast<u32x4 *>(to) = first;
+                *reinterpret_cast<u32x4 *>(to + 32) = second;
+            }
+            // The other half of the last 16 ranks.
+            const int end = (rank + 7) / 8 * 8;
+            if (threadIdx.x % 8 == 0 && end % 16 == 8) {
+                uint8_t *to = smem + p * vpitch + end / 16 * 64 + 16;
+                *reinterpret_cast<u32x4 *>(to) = *reinterpret_cast<u32x4 *>(to + 32) = u32x4{0u, 0u, 0u, 0u};
+            }
+        }
+        __syncthreads();
+        for (int ct = 0; ct < kCols; ++ct) {
+            const int n0 = c0 + 64 * ct, n = n0 + lane % 8 * 8;
+            if (n0 >= N)
+                break;
+            if (ct > 0 && passes == 1)
+                load_b(n0, 0);
+            for (int pb = 0; pb < rows.count; pb += 16 * kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    load_base(n0, pb + 16 * i, bv[i]);
+#pragma unroll
+                for (int tile = 0; tile < kAhead; ++tile) {
+                    const int p0 = pb + 16 * tile;
+                    if (p0 >= rows.count)
+                        break;
+                    v4f acc[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        acc[h] = v4f{0.f, 0.f, 0.f, 0.f};
+                    for (int pass = 0; pass < passes; ++pass) {
+                        if (passes > 1)
+                            load_b(n0, pass);
+#pragma unroll
+                        for (int st = 0; st < kSteps; ++st) {
+                            const int r = pass * kRankBlock + 16 * st;
+                            if (r < rank) {
+                                // Rows past the set repeat its last one and are not stored.
+                                const v8bf vf = *reinterpret_cast<const v8bf *>(
+                                    smem + min(p0 + l16, rows.count - 1) * vpitch + r * 4 + quarter * 16);
+#pragma unroll
+                                for (int h = 0; h < 4; ++h)
+                                    acc[h] = mfma16(mask_ranks(bf[st][h], r + 8 * (quarter % 2), rank), vf, acc[h]);
                             }
                         }
                     }
-                }
+                    // Lane l16 is the row, registers i the columns 16 h + 4 quarter + i.
+                    uint8_t *sums = s_out[wave];
 #pragma unroll
-                for (int mt = 0; mt < kTiles; ++mt) {
-                    if (p0 + 16 * mt + l16 < rows.count && n < N) {
-                        u32x4 o;
+                    for (int h = 0; h < 4; ++h)
+                        *reinterpret_cast<v4f *>(sums + l16 * kPitch + (16 * h + 4 * quarter) * 4) = acc[h];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const v4f &t = acc[mt][q / 2];
-                            o[q] = pack_bf16x2(t[2 * q % 4] + bf16_to_f32(bv[mt][q] & 0xffffu),
-                                               t[2 * q % 4 + 1] + __uint_as_float(bv[mt][q] & 0xffff0000u));
+                    for (int i = 0; i < 2; ++i) {
+                        const int p = p0 + 8 * i + lane / 8;
+                        const uint8_t *from = sums + (8 * i + lane / 8) * kPitch + lane % 8 * 32;
+                        const v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
+                        if (p < rows.count && n < N) {
+                            const u32x4 y = bv[tile][i];
+                            u32x4 o;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const v4f &t = q < 2 ? t0 : t1;
+                                o[q] = pack_bf16x2(t[2 * q % 4] + bf16_to_f32(y[q] & 0xffffu),
+                                                   t[2 * q % 4 + 1] + __uint_as_float(y[q] & 0xffff0000u));
+                            }
+                            *reinterpret_cast<u32x4 *>(out + (row0 + s_rows[p]) * ldo + n) = o;
                         }
-                        *reinterpret_cast<u32x4 *>(out + row[mt] * ldo + n) = o;
                     }
                 }
             }
         }
     });
+}
+
+struct ExpandArgs {
+    const float *v;
+    int parts;
+    int64_t M;
+    const int32_t *index;
+    int64_t L;
+    int slots, R;
+    const uint16_t *b;
+    const float *scaling;
+    const int32_t *ranks;
+    int N;
+    const uint16_t *base;
+    int64_t ldb;
+    uint16_t *out;
+    int64_t ldo;
+};
+
+template <bool kSlots, int kWaves, int kCols, int kSteps>
+hipError_t launch_expand(const ExpandArgs &a, hipStream_t s)
+{
+    const auto kernel = lora_expand_kernel<kSlots, kWaves, kCols, kSteps>;
+    const int lds = kLoraWindow * ((a.R + 15) / 16 * 64 + 16);  // at most 65 KiB
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
+    if (attr != hipSuccess)
+        return attr;
+    const int64_t blocks =
+        lora_ceil(a.M, kLoraWindow) * (kSlots ? a.slots : 1) * lora_ceil(a.N, 64 * kWaves * kCols);
+    if (blocks * kWaves * kWave >= int64_t(1) << 32)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kWaves * kWave), lds, s, a.v, a.parts, a.M, a.index, a.L,
+                       a.slots, a.R, a.b, a.scaling, a.ranks, a.N, a.base, a.ldb, a.out, a.ldo);
+    return hipGetLastError();
+}
+
+template <bool kSlots, int kWaves, int kCols>
+hipError_t launch_expand_steps(const ExpandArgs &a, hipStream_t s)
+{
+    // As many of B_a's operands in registers as R needs: fewer leave room for more waves.
+    return a.R <= 16   ? launch_expand<kSlots, kWaves, kCols, 1>(a, s)
+           : a.R <= 32 ? launch_expand<kSlots, kWaves, kCols, 2>(a, s)
+                       : launch_expand<kSlots, kWaves, kCols, 4>(a, s);
 }
 
 }  // namespace
@@ -305,21 +556,30 @@ int launch_lora(const uint16_t *x, int64_t M, int K, int64_t ldx, const int32_t 
     if (K % 64 != 0 || R % 8 != 0 || R < 8 || R > kLoraMaxRank || N % 16 != 0 || L < 1)
         return (int)hipErrorInvalidValue;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const int parts = lora_splits(M, K, R, L);
-    const unsigned rb = (unsigned)lora_ceil(R, kRankBlock);
-    if (M <= kPerRowMax) {
-        hipLaunchKernelGGL((lora_shrink_kernel<true, 4, 1>), dim3((unsigned)M, parts, rb), dim3(4 * kWave), 0, s, x, M,
-                           K, ldx, index, L, R, a, ranks, ws);
-        hipLaunchKernelGGL((lora_expand_kernel<true, 4, 1, 1>), dim3((unsigned)(lora_ceil(N, 128) * M)),
-                           dim3(4 * kWave), 0, s, ws, parts, M, index, L, R, b, scaling, ranks, N, base, ldb, out, ldo);
-    } else {
-        hipLaunchKernelGGL((lora_shrink_kernel<false, 8, 2>), dim3((unsigned)lora_ceil(M, 32), parts, rb),
-                           dim3(8 * kWave), 0, s, x, M, K, ldx, index, L, R, a, ranks, ws);
-        hipLaunchKernelGGL((lora_expand_kernel<false, 4, 4, 2>),
-                           dim3((unsigned)(lora_ceil(N, 256) * lora_ceil(M, kLoraWindow))), dim3(4 * kWave), 0, s,
-                           ws, parts, M, index, L, R, b, scaling, ranks, N, base, ldb, out, ldo);
-    }
-    return (int)hipGetLastError();
+    const int parts = lora_splits(M, K, R, L), slots = lora_slots(M, L);
+    const int64_t windows = lora_ceil(M, kLoraWindow);
+    const bool few = M <= kLoraFewRows;
+    const dim3 grid((unsigned)(windows * (few ? slots : 1)), parts, (unsigned)lora_ceil(R, kRankBlock));
+    if (!few)
+        hipLaunchKernelGGL(lora_shrink_many_kernel<false>, grid, dim3(kManyShrinkWaves * kWave), 0, s, x, M, K, ldx,
+                           index, L, 1, R, a, ranks, ws);
+    else if (lora_large_sets(M, L))
+        hipLaunchKernelGGL(lora_shrink_many_kernel<true>, grid, dim3(kManyShrinkWaves * kWave), 0, s, x, M, K, ldx,
+                           index, L, slots, R, a, ranks, ws);
+    else
+        hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kFewShrinkWaves * kWave), 0, s, x, M, K, ldx, index, L,
+                           slots, R, a, ranks, ws);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return (int)e;
+    const ExpandArgs ea{ws, parts, M, index, L, slots, R, b, scaling, ranks, N, base, ldb, out, ldo};
+    if (!few)
+        e = launch_expand_steps<false, 4, 2>(ea, s);
+    else if (windows * slots * lora_ceil(N, 256) < 256)
+        e = launch_expand_steps<true, 1, 1>(ea, s);
+    else
+        e = launch_expand_steps<true, 4, 1>(ea, s);
+    return (int)e;
 }
 
 }  // namespace ck

@@ -48,22 +48,37 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
 // ---- low-rank adapters --------------------------------------------------
 constexpr int kLoraWindow = 64;     // rows that share one look at the adapter indices
 constexpr int kLoraMaxRank = 256;
-constexpr int64_t kLoraPerRowMax = 256;  // rows up to which a workgroup is started per row
 constexpr int kLoraRankBlock = 64;
+// Rows up to which a workgroup is started for every set of rows a window can have.
+constexpr int64_t kLoraFewRows = 1024;
 inline int64_t lora_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// Parts the K columns are split into, so that few rows still fill the chip.
+// Sets a window can have: its rows' adapters, and the rows without one.
+inline int lora_slots(int64_t M, int64_t L)
+{
+    const int64_t rows = M < kLoraWindow ? M : kLoraWindow;
+    return (int)(rows < L + 1 ? rows : L + 1);
+}
+// Whether the sets of a few-row call can be large: several windows' rows over few
+// adapters.
+inline bool lora_large_sets(int64_t M, int64_t L) { return M > kLoraWindow && L < 16; }
+// Parts the K columns are split into, so that few rows still fill the chip: about
+// one workgroup for each of the 256 CUs; a wave keeps a 64-column group at least,
+// and the second product adds at most 8 parts.
 inline int lora_splits(int64_t M, int64_t K, int64_t R, int64_t L)
 {
-    // About one workgroup for each of the 256 CUs; a wave keeps a 64-column
-    // group at least, and the second product adds at most 16 parts.
-    const bool per_row = M <= kLoraPerRowMax;
-    const int64_t groups = K / 64, waves = per_row ? 4 : 8;
-    const int64_t sets = per_row ? (M < L * lora_ceil(M, kLoraWindow) ? M : L * lora_ceil(M, kLoraWindow))
-                                 : lora_ceil(M, 32);
+    const int64_t slots = M > kLoraFewRows ? 1 : lora_slots(M, L);
+    // Of the sets that windows of several requests' rows can have they have a few.
+    const int64_t sets = lora_ceil(M, kLoraWindow) * (lora_large_sets(M, L) && slots > 3 ? 3 : slots);
     int64_t s = 256 / (sets * lora_ceil(R, kLoraRankBlock));
-    const int64_t most = groups / waves < 16 ? groups / waves : 16;
+    const int64_t most = K / 64 / 4 < 8 ? K / 64 / 4 : 8;
     s = s > most ? most : s;
     return (int)(s < 1 ? 1 : s);
+}
+// Workgroups of 256 threads of the second product; a launch takes fewer than 2^24.
+inline int64_t lora_blocks(int64_t M, int64_t N, int64_t L)
+{
+    const int64_t windows = lora_ceil(M, kLoraWindow);
+    return M <= kLoraFewRows ? windows * lora_slots(M, L) * lora_ceil(N, 256) : windows * lora_ceil(N, 512);
 }
 int launch_lora(const uint16_t *x, int64_t M, int K, int64_t ldx, const int32_t *index, int64_t L, int R,
                 const uint16_t *a, const uint16_t *b, const float *scaling, const int32_t *ranks, int N,

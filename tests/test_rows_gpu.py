@@ -359,7 +359,8 @@ def lora_case(M, K, N, R, L, seed, ranks=True, base=True):
 
 LORA = [(1, 64, 16, 8, 1), (1, 3840, 512, 16, 3), (2, 128, 48, 8, 3), (17, 192, 272, 24, 2), (33, 320, 144, 40, 33),
         (64, 128, 128, 64, 5), (65, 448, 160, 72, 9), (200, 64, 32, 128, 3), (256, 192, 80, 16, 300),
-        (257, 192, 80, 16, 4), (300, 576, 528, 40, 2), (700, 128, 272, 256, 5), (1000, 1088, 304, 64, 40)]
+        (257, 192, 80, 16, 4), (300, 576, 528, 40, 2), (700, 128, 272, 256, 5), (1000, 1088, 304, 64, 40),
+        (1025, 192, 528, 24, 3), (1300, 640, 176, 136, 30), (2111, 320, 1040, 64, 2)]
 
 
 @pytest.mark.parametrize("M,K,N,R,L", LORA)
@@ -371,7 +372,7 @@ def test_lora(M, K, N, R, L, ranks, base):
     assert_within(out, *ref_lora(x, a, b, sc, rk, index, y))
 
 
-@pytest.mark.parametrize("M", [50, 600])
+@pytest.mark.parametrize("M", [50, 600, 1500])
 def test_lora_runs_of_rows_and_no_scaling(M):
     """Prompts packed one after the other, an adapter for each, some without."""
     x, a, b, _, _, _, y = lora_case(M, 256, 192, 32, 6, seed=M)
@@ -380,7 +381,7 @@ def test_lora_runs_of_rows_and_no_scaling(M):
     assert_within(out, *ref_lora(x, a, b, None, None, index, y))
 
 
-@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("M", [40, 300, 1200])
 def test_lora_rows_without_an_adapter_keep_base(M):
     x, a, b, sc, rk, _, y = lora_case(M, 128, 80, 16, 3, seed=M)
     index = torch.full((M,), -1, dtype=torch.int32, device=DEV)
@@ -397,7 +398,7 @@ def test_lora_rows_without_an_adapter_keep_base(M):
     assert_within(out, *ref_lora(x, a, b, sc, None, index, y))
 
 
-@pytest.mark.parametrize("M,R", [(37, 40), (290, 40), (5, 200), (280, 200)])
+@pytest.mark.parametrize("M,R", [(37, 40), (290, 40), (5, 200), (280, 200), (1100, 40)])
 def test_lora_ignores_what_lies_beyond_a_rank(M, R):
     x, a, b, sc, _, index, y = lora_case(M, 192, 144, R, 4, seed=M)
     rk = torch.tensor([R - 3, 1, R // 2, R], dtype=torch.int32, device=DEV)
@@ -407,7 +408,7 @@ def test_lora_ignores_what_lies_beyond_a_rank(M, R):
     assert_within(ck.lora_add(x, ck.LoraAdapters(a, b, sc, rk), index, base=y), *ref)
 
 
-@pytest.mark.parametrize("M", [30, 270])
+@pytest.mark.parametrize("M", [30, 270, 1070])
 def test_lora_strided_in_place_and_isolated_rows(M):
     K, N = 192, 96
     x, a, b, sc, rk, index, y = lora_case(M, K, N, 24, 3, seed=M)
@@ -431,7 +432,7 @@ def test_lora_strided_in_place_and_isolated_rows(M):
 
 
 def test_lora_same_bits_again_in_graphs_and_on_other_streams():
-    for M in (20, 400):
+    for M in (20, 400, 1400):
         x, a, b, sc, rk, index, y = lora_case(M, 640, 208, 32, 5, seed=M)
         adapters = ck.LoraAdapters(a, b, sc, rk)
         other = torch.flip(index, (0,)).contiguous()
