@@ -412,7 +412,7 @@ size_t ck_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
  *   ws      at least ck_lora_workspace_bytes(M, K, R, L) bytes, 256-byte aligned
  * K % 64 == 0, R % 8 == 0 (CK_ERR_INVALID_ARG); K <= 32768, R <= 256, N % 16
  * == 0, ceil(M / 64) * ceil(N / 512) < 2^24 (CK_ERR_UNSUPPORTED; up to 1024
- * rows, ceil(M / 64) * min(M, 64, L + 1) * ceil(N / 256) < 2^24).
+ * rows, ceil(M / 64) * 64 * ceil(N / 256) < 2^24 is enough).
  */
 ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const int32_t *index, int64_t L,
                       int64_t R, const uint16_t *a, const uint16_t *b, const float *scaling, const int32_t *ranks,

@@ -6,9 +6,9 @@
 // lanes of a wave read the indices of a window of rows, a ballot gives the rows of
 // one adapter (a set), and those rows, wherever they lie in the window, fill
 // the 16-row tiles of the bf16 MFMA.  Few rows: a workgroup is started for every
-// set a window can have, so that requests of unlike adapters run side by
-// side; many rows (prompts, where neighbours share an adapter): a workgroup goes
-// through the sets of its window.
+// tile the sets of a window can have, so that requests of unlike adapters run side
+// by side; many rows (prompts, where neighbours share an adapter): a workgroup
+// goes through the sets of its window.
 // The work is bound by memory: x, base and out once, the used adapters once.
 #include <type_traits>
 
@@ -52,19 +52,27 @@ __device__ __forceinline__ RowSet take_set(int mine, uint64_t &left)
     r.order = __builtin_amdgcn_ds_permute(4 * pos, lane);
     return r;
 }
-// Calls f for the slot-th set of a window (kSlots), if there is one, or for all.
-template <bool kSlots, class F>
+// Few rows (kTile): calls f(set, first row) for the slot-th tile of 16 rows of a
+// window's sets, if there is one.  Many: f(set, 0) for each set.
+template <bool kTile, class F>
 __device__ __forceinline__ void for_sets(int mine, int slot, F &&f)
 {
     uint64_t left = __ballot(mine != -2);
-    if constexpr (kSlots) {
-        for (int i = 0; i < slot && left; ++i)
-            left &= ~__ballot(mine == __builtin_amdgcn_readlane(mine, __builtin_ctzll(left)));
-        if (left)
-            f(take_set(mine, left));
+    if constexpr (kTile) {
+        while (left) {
+            const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            const uint64_t mask = __ballot(mine == a);
+            const int tiles = (__builtin_popcountll(mask) + 15) / 16;
+            if (slot < tiles) {
+                f(take_set(mine, left), 16 * slot);
+                break;
+            }
+            slot -= tiles;
+            left &= ~mask;
+        }
     } else {
         while (left)
-            f(take_set(mine, left));
+            f(take_set(mine, left), 0);
     }
 }
 
@@ -97,63 +105,17 @@ __device__ __forceinline__ void store_v(const float (&s_red)[kWaves][kTiles][kRT
 }
 
 // Few rows.  Grid: (windows x slots, parts of K, blocks of 64 ranks); the
-// workgroup's waves split its part of K.  Operands come straight to registers:
-// these calls are bound by latency, not by the address path.
+// workgroup's waves split its part of K.  Operands come straight to registers,
+// kAhead groups at a time: these calls are bound by latency, not by the address
+// path.
 constexpr int kFewShrinkWaves = 4;
-
-template <int kTiles>
-__device__ __forceinline__ void shrink_rows(const RowSet &rows, int p0, int64_t row0, const uint16_t *x, int64_t ldx,
-                                            const uint16_t *const (&arow)[kRT], int nrt, int g0, int g1,
-                                            float (&s_red)[kFewShrinkWaves][kTiles][kRT][256])
-{
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
-    const uint16_t *xrow[kTiles];
-#pragma unroll
-    for (int mt = 0; mt < kTiles; ++mt)
-        xrow[mt] = x + (row0 + __shfl(rows.order, min(p0 + 16 * mt + l16, rows.count - 1))) * ldx + 16 * quarter;
-    v4f acc[kTiles][kRT];
-#pragma unroll
-    for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-        for (int rt = 0; rt < kRT; ++rt)
-            acc[mt][rt] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int g = g0; g < g1; ++g) {
-        u32x4 xv[kTiles][2], av[kRT][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int mt = 0; mt < kTiles; ++mt)
-                xv[mt][h] = *reinterpret_cast<const u32x4 *>(xrow[mt] + g * 64 + 8 * h);
-#pragma unroll
-            for (int rt = 0; rt < kRT; ++rt)
-                if (rt < nrt)
-                    av[rt][h] = *reinterpret_cast<const u32x4 *>(arow[rt] + g * 64 + 8 * h);
-        }
-#pragma unroll
-        for (int rt = 0; rt < kRT; ++rt)
-            if (rt < nrt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt)
-                        acc[mt][rt] = mfma16(__builtin_bit_cast(v8bf, xv[mt][h]), __builtin_bit_cast(v8bf, av[rt][h]),
-                                             acc[mt][rt]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-        for (int rt = 0; rt < kRT; ++rt)
-            if (rt < nrt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s_red[wave][mt][rt][i * kWave + lane] = acc[mt][rt][i];
-}
 
 __global__ __launch_bounds__(kFewShrinkWaves * kWave) void lora_shrink_few_kernel(
     const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, const int32_t *__restrict__ index, int64_t L,
     int slots, int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
 {
-    __shared__ float s_red[kFewShrinkWaves][2][kRT][256];
+    constexpr int kAhead = 3;
+    __shared__ float s_red[kFewShrinkWaves][1][kRT][256];
     __shared__ int s_rows[kWave];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
     const int64_t row0 = (int64_t)(blockIdx.x / slots) * kLoraWindow;
@@ -161,38 +123,60 @@ __global__ __launch_bounds__(kFewShrinkWaves * kWave) void lora_shrink_few_kerne
     const int KG = K / 64, parts = gridDim.y * kFewShrinkWaves, part = blockIdx.y * kFewShrinkWaves + wave;
     const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
     const int mine = window_adapter(index, M, L, row0, kLoraWindow);
-    for_sets<true>(mine, blockIdx.x % slots, [&](const RowSet &rows) {
+    for_sets<true>(mine, blockIdx.x % slots, [&](const RowSet &rows, int p0) {
         if (rows.adapter < 0)
             return;
+        // All ranks of the slot: the loads do not wait for the adapter's own rank.
         const int rank = adapter_rank(ranks, rows.adapter, R);
-        if (rank <= rb)
-            return;
-        const int nrt = min(kRT, (rank - rb + 15) / 16);
+        const int nrt = min(kRT, (R - rb + 15) / 16);
         const uint16_t *arow[kRT];
 #pragma unroll
         for (int rt = 0; rt < kRT; ++rt)
-            arow[rt] = a_w + ((int64_t)rows.adapter * R + min(rb + 16 * rt + l16, rank - 1)) * K + 16 * quarter;
+            arow[rt] = a_w + ((int64_t)rows.adapter * R + min(rb + 16 * rt + l16, R - 1)) * K + 16 * quarter;
+        const uint16_t *xrow = x + (row0 + __shfl(rows.order, min(p0 + l16, rows.count - 1))) * ldx + 16 * quarter;
         if (wave == 0)
             s_rows[lane] = rows.order;
-        float *to = v + (int64_t)blockIdx.y * M * R;
-        if (rows.count <= 16) {
-            float(&red)[kFewShrinkWaves][1][kRT][256] =
-                *reinterpret_cast<float(*)[kFewShrinkWaves][1][kRT][256]>(&s_red);
-            shrink_rows<1>(rows, 0, row0, x, ldx, arow, nrt, g0, g1, red);
-            __syncthreads();
-            store_v<kFewShrinkWaves, 1>(red, s_rows, 0, rows.count, nrt, rb, rank, R, row0, to);
-        } else {
-            for (int p0 = 0; p0 < rows.count; p0 += 32) {
-                shrink_rows<2>(rows, p0, row0, x, ldx, arow, nrt, g0, g1, s_red);
-                __syncthreads();
-                store_v<kFewShrinkWaves, 2>(s_red, s_rows, p0, rows.count, nrt, rb, rank, R, row0, to);
-                __syncthreads();  // the sums have been read
-            }
+        v4f acc[kRT];
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+            acc[rt] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int gb = g0; gb < g1; gb += kAhead) {
+            u32x4 xv[kAhead][2], av[kAhead][kRT][2];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (gb + u < g1)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        xv[u][h] = *reinterpret_cast<const u32x4 *>(xrow + (gb + u) * 64 + 8 * h);
+#pragma unroll
+                        for (int rt = 0; rt < kRT; ++rt)
+                            if (rt < nrt)
+                                av[u][rt][h] = *reinterpret_cast<const u32x4 *>(arow[rt] + (gb + u) * 64 + 8 * h);
+                    }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (gb + u < g1)
+#pragma unroll
+                    for (int rt = 0; rt < kRT; ++rt)
+                        if (rt < nrt)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                acc[rt] = mfma16(__builtin_bit_cast(v8bf, xv[u][h]),
+                                                 __builtin_bit_cast(v8bf, av[u][rt][h]), acc[rt]);
         }
+#pragma unroll
+        for (int rt = 0; rt < kRT; ++rt)
+            if (rt < nrt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s_red[wave][0][rt][i * kWave + lane] = acc[rt][i];
+        __syncthreads();
+        store_v<kFewShrinkWaves, 1>(s_red, s_rows, p0, rows.count, nrt, rb, rank, R, row0,
+                                    v + (int64_t)blockIdx.y * M * R);
     });
 }
 
-// Larger sets.  Grid: (windows (x slots), parts of K, blocks of 64 ranks).  Each wave
+// Many rows.  Grid: (windows, parts of K, blocks of 64 ranks).  Each wave
 // streams its part of the columns of the set's rows of x and of the adapter's rows
 // through an LDS ring of its own: a stage is 64 columns, every instruction eight
 // rows of 128 contiguous bytes, with the 16-byte slots XORed by the row's low bits so
@@ -215,10 +199,9 @@ __device__ __forceinline__ void wait_even(int n)
     }
 }
 
-template <bool kSlots>
 __global__ __launch_bounds__(kManyShrinkWaves * kWave) void lora_shrink_many_kernel(
     const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, const int32_t *__restrict__ index, int64_t L,
-    int slots, int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
+    int R, const uint16_t *__restrict__ a_w, const int32_t *__restrict__ ranks, float *__restrict__ v)
 {
     // The rings; after the products, the waves' sums.
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[kManyShrinkWaves][kManyStages * kManyStageBytes];
@@ -227,14 +210,14 @@ __global__ __launch_bounds__(kManyShrinkWaves * kWave) void lora_shrink_many_ker
     float(&s_red)[kManyShrinkWaves][kMT][kRT][256] =
         *reinterpret_cast<float(*)[kManyShrinkWaves][kMT][kRT][256]>(&s_ring);
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, l16 = lane % 16, quarter = lane / 16;
-    const int64_t row0 = (int64_t)(kSlots ? blockIdx.x / slots : blockIdx.x) * kLoraWindow;
+    const int64_t row0 = (int64_t)blockIdx.x * kLoraWindow;
     const int rb = blockIdx.z * kRankBlock;
     const int KG = K / 64, parts = gridDim.y * kManyShrinkWaves, part = blockIdx.y * kManyShrinkWaves + wave;
     const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
     const int mine = window_adapter(index, M, L, row0, kLoraWindow);
     lds_u8 *ring = (lds_u8 *)s_ring[wave];
     const int chunk = (lane % 8) ^ (lane / 8);
-    for_sets<kSlots>(mine, kSlots ? blockIdx.x % slots : 0, [&](const RowSet &rows) {
+    for_sets<false>(mine, 0, [&](const RowSet &rows, int) {
         if (rows.adapter < 0)
             return;
         const int rank = adapter_rank(ranks, rows.adapter, R);
@@ -325,13 +308,12 @@ __global__ __launch_bounds__(kManyShrinkWaves * kWave) void lora_shrink_many_ker
 // --------------------------------------------------------------- second product
 
 // The 8 ranks from r on of one row of B_a, 0 from `rank` on (whatever is stored there).
-__device__ __forceinline__ v8bf mask_ranks(u32x4 w, int r, int rank)
+__device__ __forceinline__ u32x4 mask_ranks(u32x4 w, int r, int rank)
 {
-    if (r + 8 > rank)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            w[q] &= (r + 2 * q < rank ? 0xffffu : 0u) | (r + 2 * q + 1 < rank ? 0xffff0000u : 0u);
-    return __builtin_bit_cast(v8bf, w);
+    for (int q = 0; q < 4; ++q)
+        w[q] &= (r + 2 * q < rank ? 0xffffu : 0u) | (r + 2 * q + 1 < rank ? 0xffff0000u : 0u);
+    return w;
 }
 
 // Grid: windows (x slots), by columns / (64 kWaves kCols).  The workgroup brings v of a
@@ -347,7 +329,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
     const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo)
 {
     constexpr int kPitch = 64 * 4 + 16;      // sums: 16 bytes on from row to row
-    constexpr int kAhead = kSlots ? 1 : 4;   // row tiles whose base is on its way
+    constexpr int kAhead = kSlots ? 1 : 2;   // row tiles whose base is on its way
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ __attribute__((aligned(16))) uint8_t s_out[kWaves][16 * kPitch];
     __shared__ int s_rows[kWave];
@@ -360,25 +342,41 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
     const int vpitch = (R + 15) / 16 * 64 + 16;  // bytes of a row of v in LDS
     const int mine = window_adapter(index, M, L, row0, kLoraWindow);
 
-    for_sets<kSlots>(mine, kSlots ? unit % slots : 0, [&](const RowSet &rows) {
+    for_sets<kSlots>(mine, kSlots ? unit % slots : 0, [&](const RowSet &rows, int begin) {
+        const int last = kSlots ? min(begin + 16, rows.count) : rows.count;
         const int rank = rows.adapter < 0 ? 0 : adapter_rank(ranks, rows.adapter, R);
         const float scale = rows.adapter >= 0 && scaling ? scaling[rows.adapter] : 1.f;
-        const int passes = max(1, (rank + kRankBlock - 1) / kRankBlock);
+        // Few rows: every rank of the slot is loaded, so that no load waits for the
+        // adapter's own rank; what lies beyond it meets zeros, and is masked.
+        const int upto = kSlots ? (rows.adapter < 0 ? 0 : R) : rank;
+        const int passes = max(1, (upto + kRankBlock - 1) / kRankBlock);
         u32x4 bf[kSteps][4];
         const auto load_b = [&](int n0, int pass) {
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
                 const int r = pass * kRankBlock + 16 * st + 8 * (quarter % 2);
-                if (pass * kRankBlock + 16 * st < rank)
+                if (pass * kRankBlock + 16 * st < upto)
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const int n = min(n0 + 16 * h + l16, N - 1);
                         bf[st][h] = u32x4{0u, 0u, 0u, 0u};
-                        if (r < rank)
+                        if (r < upto)
                             bf[st][h] = *reinterpret_cast<const u32x4 *>(
                                 b_w + ((int64_t)rows.adapter * N + n) * R + r);
                     }
             }
+        };
+        const bool ragged = rank % 8 != 0 || rank < upto;
+        const auto mask_b = [&](int pass) {
+            if (!ragged)
+                return;
+            int end = rank;  // opaque: the masks are made here, not kept in registers
+            asm volatile("" : "+s"(end));
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        bf[st][h] = mask_ranks(bf[st][h], pass * kRankBlock + 16 * st + 8 * (quarter % 2), end);
         };
         // base of a tile: two rows a lane, lane / 8 and 8 + lane / 8.
         u32x4 bv[kAhead][2];
@@ -388,53 +386,42 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                 const int p = p0 + 8 * i + lane / 8, n = n0 + lane % 8 * 8;
                 const int row = __shfl(rows.order, p & 63);  // by every lane
                 to[i] = u32x4{0u, 0u, 0u, 0u};
-                if (base && p < rows.count && n < N)
+                if (base && p < last && n < N)
                     to[i] = *reinterpret_cast<const u32x4 *>(base + (row0 + row) * ldb + n);
             }
         };
         if (c0 < N && passes == 1)
             load_b(c0, 0);
+        if (kSlots && c0 < N)
+            load_base(c0, begin, bv[0]);
 
         if (!kSlots)
             __syncthreads();  // the last set's v has been read
         if (wave == 0)
             s_rows[lane] = rows.order;
         __syncthreads();
-        // v to LDS: a thread takes 8 ranks of a row, eight threads 64.
-        for (int p = threadIdx.x / 8; p < rows.count; p += kWaves * 8) {
-            for (int r = threadIdx.x % 8 * 8; r < rank; r += 64) {
-                float t[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[e] = 0.f;
+        // v to LDS: a thread takes 4 ranks of a row, 16 threads 64.
+        for (int p = begin + threadIdx.x / 16; p < last; p += kWaves * 4) {
+            for (int r = threadIdx.x % 16 * 4; r < upto; r += 64) {
+                v4f t = {0.f, 0.f, 0.f, 0.f};
                 const float *from = v + (row0 + s_rows[p]) * R + r;
 #pragma unroll 4
                 for (int s = 0; s < parts; ++s, from += M * R)
+                    t += *reinterpret_cast<const v4f *>(from);
+                uint16_t hi[4], lo[4];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const v4f u = *reinterpret_cast<const v4f *>(from + 4 * q);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            t[4 * q + e] += u[e];
-                    }
-                u32x4 first, second;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint16_t hi[2], lo[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)  // v is written up to rank
-                        split_bf16(r + 2 * q + e < rank ? scale * t[2 * q + e] : 0.f, hi[e], lo[e]);
-                    first[q] = hi[0] | (uint32_t)hi[1] << 16, second[q] = lo[0] | (uint32_t)lo[1] << 16;
-                }
-                uint8_t *to = smem + p * vpitch + r / 16 * 64 + r % 16 * 2;
-                *reinterpret_cast<u32x4 *>(to) = first;
-                *reinterpret_cast<u32x4 *>(to + 32) = second;
+                for (int e = 0; e < 4; ++e)  // v is written up to rank
+                    split_bf16(r + e < rank ? scale * t[e] : 0.f, hi[e], lo[e]);
+                uint8_t *to = smem + (p - begin) * vpitch + r / 16 * 64 + r % 16 * 2;
+                *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+                *reinterpret_cast<u32x2 *>(to + 32) =
+                    u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
             }
             // The other half of the last 16 ranks.
-            const int end = (rank + 7) / 8 * 8;
-            if (threadIdx.x % 8 == 0 && end % 16 == 8) {
-                uint8_t *to = smem + p * vpitch + end / 16 * 64 + 16;
-                *reinterpret_cast<u32x4 *>(to) = *reinterpret_cast<u32x4 *>(to + 32) = u32x4{0u, 0u, 0u, 0u};
+            const int end = (upto + 3) / 4 * 4;
+            for (int r = end + threadIdx.x % 16 * 4; r % 16 != 0 && r < (end + 15) / 16 * 16; r += 64) {
+                uint8_t *to = smem + (p - begin) * vpitch + r / 16 * 64 + r % 16 * 2;
+                *reinterpret_cast<u32x2 *>(to) = *reinterpret_cast<u32x2 *>(to + 32) = u32x2{0u, 0u};
             }
         }
         __syncthreads();
@@ -442,34 +429,41 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
             const int n0 = c0 + 64 * ct, n = n0 + lane % 8 * 8;
             if (n0 >= N)
                 break;
-            if (ct > 0 && passes == 1)
-                load_b(n0, 0);
-            for (int pb = 0; pb < rows.count; pb += 16 * kAhead) {
+            if (passes == 1) {
+                if (ct > 0)
+                    load_b(n0, 0);
+                mask_b(0);
+            }
+            for (int pb = begin; pb < last; pb += 16 * kAhead) {
+                if (!kSlots || ct > 0)
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    load_base(n0, pb + 16 * i, bv[i]);
+                    for (int i = 0; i < kAhead; ++i)
+                        load_base(n0, pb + 16 * i, bv[i]);
 #pragma unroll
                 for (int tile = 0; tile < kAhead; ++tile) {
                     const int p0 = pb + 16 * tile;
-                    if (p0 >= rows.count)
+                    if (p0 >= last)
                         break;
+                    __builtin_amdgcn_sched_barrier(0);
                     v4f acc[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
                         acc[h] = v4f{0.f, 0.f, 0.f, 0.f};
                     for (int pass = 0; pass < passes; ++pass) {
-                        if (passes > 1)
+                        if (passes > 1) {
                             load_b(n0, pass);
+                            mask_b(pass);
+                        }
 #pragma unroll
                         for (int st = 0; st < kSteps; ++st) {
                             const int r = pass * kRankBlock + 16 * st;
-                            if (r < rank) {
+                            if (r < upto) {
                                 // Rows past the set repeat its last one and are not stored.
                                 const v8bf vf = *reinterpret_cast<const v8bf *>(
-                                    smem + min(p0 + l16, rows.count - 1) * vpitch + r * 4 + quarter * 16);
+                                    smem + (min(p0 + l16, last - 1) - begin) * vpitch + r * 4 + quarter * 16);
 #pragma unroll
                                 for (int h = 0; h < 4; ++h)
-                                    acc[h] = mfma16(mask_ranks(bf[st][h], r + 8 * (quarter % 2), rank), vf, acc[h]);
+                                    acc[h] = mfma16(__builtin_bit_cast(v8bf, bf[st][h]), vf, acc[h]);
                             }
                         }
                     }
@@ -483,7 +477,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                         const int p = p0 + 8 * i + lane / 8;
                         const uint8_t *from = sums + (8 * i + lane / 8) * kPitch + lane % 8 * 32;
                         const v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
-                        if (p < rows.count && n < N) {
+                        if (p < last && n < N) {
                             const u32x4 y = bv[tile][i];
                             u32x4 o;
 #pragma unroll
@@ -522,7 +516,7 @@ template <bool kSlots, int kWaves, int kCols, int kSteps>
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t s)
 {
     const auto kernel = lora_expand_kernel<kSlots, kWaves, kCols, kSteps>;
-    const int lds = kLoraWindow * ((a.R + 15) / 16 * 64 + 16);  // at most 65 KiB
+    const int lds = (kSlots ? 16 : kLoraWindow) * ((a.R + 15) / 16 * 64 + 16);  // at most 65 KiB
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
     if (attr != hipSuccess)
@@ -560,15 +554,12 @@ int launch_lora(const uint16_t *x, int64_t M, int K, int64_t ldx, const int32_t 
     const int64_t windows = lora_ceil(M, kLoraWindow);
     const bool few = M <= kLoraFewRows;
     const dim3 grid((unsigned)(windows * (few ? slots : 1)), parts, (unsigned)lora_ceil(R, kRankBlock));
-    if (!few)
-        hipLaunchKernelGGL(lora_shrink_many_kernel<false>, grid, dim3(kManyShrinkWaves * kWave), 0, s, x, M, K, ldx,
-                           index, L, 1, R, a, ranks, ws);
-    else if (lora_large_sets(M, L))
-        hipLaunchKernelGGL(lora_shrink_many_kernel<true>, grid, dim3(kManyShrinkWaves * kWave), 0, s, x, M, K, ldx,
-                           index, L, slots, R, a, ranks, ws);
-    else
+    if (few)
         hipLaunchKernelGGL(lora_shrink_few_kernel, grid, dim3(kFewShrinkWaves * kWave), 0, s, x, M, K, ldx, index, L,
                            slots, R, a, ranks, ws);
+    else
+        hipLaunchKernelGGL(lora_shrink_many_kernel, grid, dim3(kManyShrinkWaves * kWave), 0, s, x, M, K, ldx, index, L,
+                           R, a, ranks, ws);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return (int)e;

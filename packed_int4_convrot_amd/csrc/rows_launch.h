@@ -49,27 +49,25 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
 constexpr int kLoraWindow = 64;     // rows that share one look at the adapter indices
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraRankBlock = 64;
-// Rows up to which a workgroup is started for every set of rows a window can have.
+// Rows up to which a workgroup is started for every tile a window can have.
 constexpr int64_t kLoraFewRows = 1024;
 inline int64_t lora_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
-// Sets a window can have: its rows' adapters, and the rows without one.
+// Tiles of 16 rows that the sets of a window can have, a set being the rows of one
+// adapter, or those without one: rows / 16 and 15 / 16 of a tile for each set.
 inline int lora_slots(int64_t M, int64_t L)
 {
-    const int64_t rows = M < kLoraWindow ? M : kLoraWindow;
-    return (int)(rows < L + 1 ? rows : L + 1);
+    const int64_t rows = M < kLoraWindow ? M : kLoraWindow, sets = rows < L + 1 ? rows : L + 1;
+    return (int)((rows + 15 * sets) / 16);
 }
-// Whether the sets of a few-row call can be large: several windows' rows over few
-// adapters.
-inline bool lora_large_sets(int64_t M, int64_t L) { return M > kLoraWindow && L < 16; }
 // Parts the K columns are split into, so that few rows still fill the chip: about
 // one workgroup for each of the 256 CUs; a wave keeps a 64-column group at least,
-// and the second product adds at most 8 parts.
+// and the second product adds at most 8 parts.  Of the tiles that a window's sets
+// can have, several requests' rows over few adapters use about six.
 inline int lora_splits(int64_t M, int64_t K, int64_t R, int64_t L)
 {
     const int64_t slots = M > kLoraFewRows ? 1 : lora_slots(M, L);
-    // Of the sets that windows of several requests' rows can have they have a few.
-    const int64_t sets = lora_ceil(M, kLoraWindow) * (lora_large_sets(M, L) && slots > 3 ? 3 : slots);
-    int64_t s = 256 / (sets * lora_ceil(R, kLoraRankBlock));
+    const int64_t tiles = lora_ceil(M, kLoraWindow) * (M > kLoraWindow && L < 16 && slots > 6 ? 6 : slots);
+    int64_t s = 256 / (tiles * lora_ceil(R, kLoraRankBlock));
     const int64_t most = K / 64 / 4 < 8 ? K / 64 / 4 : 8;
     s = s > most ? most : s;
     return (int)(s < 1 ? 1 : s);
