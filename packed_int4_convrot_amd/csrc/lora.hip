@@ -52,12 +52,13 @@ __device__ __forceinline__ RowSet take_set(int mine, uint64_t &left)
     r.order = __builtin_amdgcn_ds_permute(4 * pos, lane);
     return r;
 }
-// Few rows (kTile): calls f(set, first row) for the slot-th tile of 16 rows of a
-// window's sets, if there is one.  Many: f(set, 0) for each set.
+// The sets of the rows whose adapter is at least `from`.  Few rows (kTile): calls
+// f(set, first row) for the slot-th tile of 16 rows of them, if there is one.
+// Many: f(set, 0) for each set.
 template <bool kTile, class F>
-__device__ __forceinline__ void for_sets(int mine, int slot, F &&f)
+__device__ __forceinline__ void for_sets(int mine, int from, int slot, F &&f)
 {
-    uint64_t left = __ballot(mine != -2);
+    uint64_t left = __ballot(mine >= from);
     if constexpr (kTile) {
         while (left) {
             const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
@@ -123,9 +124,7 @@ __global__ __launch_bounds__(kFewShrinkWaves * kWave) void lora_shrink_few_kerne
     const int KG = K / 64, parts = gridDim.y * kFewShrinkWaves, part = blockIdx.y * kFewShrinkWaves + wave;
     const int g0 = (int)((int64_t)part * KG / parts), g1 = (int)((int64_t)(part + 1) * KG / parts);
     const int mine = window_adapter(index, M, L, row0, kLoraWindow);
-    for_sets<true>(mine, blockIdx.x % slots, [&](const RowSet &rows, int p0) {
-        if (rows.adapter < 0)
-            return;
+    for_sets<true>(mine, 0, blockIdx.x % slots, [&](const RowSet &rows, int p0) {
         // All ranks of the slot: the loads do not wait for the adapter's own rank.
         const int rank = adapter_rank(ranks, rows.adapter, R);
         const int nrt = min(kRT, (R - rb + 15) / 16);
@@ -217,9 +216,7 @@ __global__ __launch_bounds__(kManyShrinkWaves * kWave) void lora_shrink_many_ker
     const int mine = window_adapter(index, M, L, row0, kLoraWindow);
     lds_u8 *ring = (lds_u8 *)s_ring[wave];
     const int chunk = (lane % 8) ^ (lane / 8);
-    for_sets<false>(mine, 0, [&](const RowSet &rows, int) {
-        if (rows.adapter < 0)
-            return;
+    for_sets<false>(mine, 0, 0, [&](const RowSet &rows, int) {
         const int rank = adapter_rank(ranks, rows.adapter, R);
         if (rank <= rb)
             return;
@@ -329,7 +326,8 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
     const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo)
 {
     constexpr int kPitch = 64 * 4 + 16;      // sums: 16 bytes on from row to row
-    constexpr int kAhead = kSlots ? 1 : 2;   // row tiles whose base is on its way
+    constexpr int kVRows = kSlots ? 1 : 4;  // rows of v a thread has on their way
+    constexpr int kAhead = kSlots ? 1 : 4;   // row tiles whose base is on its way
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ __attribute__((aligned(16))) uint8_t s_out[kWaves][16 * kPitch];
     __shared__ int s_rows[kWave];
@@ -338,11 +336,18 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
     const int ctiles = (N + 64 * kWaves * kCols - 1) / (64 * kWaves * kCols);
     const int unit = blockIdx.x / ctiles;
     const int64_t row0 = (int64_t)(kSlots ? unit / slots : unit) * kLoraWindow;
-    const int c0 = (blockIdx.x % ctiles * kWaves + wave) * 64 * kCols;
+    const int c0 = (blockIdx.x % ctiles * kCols * kWaves + wave) * 64;  // and every 64 kWaves on
     const int vpitch = (R + 15) / 16 * 64 + 16;  // bytes of a row of v in LDS
-    const int mine = window_adapter(index, M, L, row0, kLoraWindow);
+    int mine = window_adapter(index, M, L, row0, kLoraWindow);
+    // Rows without an adapter join the window's first set, so that they cost no
+    // pass of their own; -0 is added to their base.
+    const uint64_t without = __ballot(mine == -1), with = __ballot(mine >= 0);
+    if (with) {
+        const int first = __builtin_amdgcn_readlane(mine, __builtin_ctzll(with));
+        mine = mine == -1 ? first : mine;
+    }
 
-    for_sets<kSlots>(mine, kSlots ? unit % slots : 0, [&](const RowSet &rows, int begin) {
+    for_sets<kSlots>(mine, -1, kSlots ? unit % slots : 0, [&](const RowSet &rows, int begin) {
         const int last = kSlots ? min(begin + 16, rows.count) : rows.count;
         const int rank = rows.adapter < 0 ? 0 : adapter_rank(ranks, rows.adapter, R);
         const float scale = rows.adapter >= 0 && scaling ? scaling[rows.adapter] : 1.f;
@@ -398,25 +403,41 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
         if (!kSlots)
             __syncthreads();  // the last set's v has been read
         if (wave == 0)
-            s_rows[lane] = rows.order;
+            s_rows[lane] = rows.order | (int)(without >> rows.order & 1) << 6;
         __syncthreads();
         // v to LDS: a thread takes 4 ranks of a row, 16 threads 64.
-        for (int p = begin + threadIdx.x / 16; p < last; p += kWaves * 4) {
+        for (int pb = begin + threadIdx.x / 16; pb < last; pb += kWaves * 4 * kVRows) {
             for (int r = threadIdx.x % 16 * 4; r < upto; r += 64) {
-                v4f t = {0.f, 0.f, 0.f, 0.f};
-                const float *from = v + (row0 + s_rows[p]) * R + r;
-#pragma unroll 4
-                for (int s = 0; s < parts; ++s, from += M * R)
-                    t += *reinterpret_cast<const v4f *>(from);
-                uint16_t hi[4], lo[4];
+                v4f t[kVRows];
+                const float *from[kVRows];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)  // v is written up to rank
-                    split_bf16(r + e < rank ? scale * t[e] : 0.f, hi[e], lo[e]);
-                uint8_t *to = smem + (p - begin) * vpitch + r / 16 * 64 + r % 16 * 2;
-                *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-                *reinterpret_cast<u32x2 *>(to + 32) =
-                    u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+                for (int i = 0; i < kVRows; ++i) {
+                    t[i] = v4f{0.f, 0.f, 0.f, 0.f};
+                    from[i] = v + (row0 + s_rows[min(pb + kWaves * 4 * i, last - 1)] % 64) * R + r;
+                }
+#pragma unroll kVRows == 1 ? 2 : 1
+                for (int s = 0; s < parts; ++s)
+#pragma unroll
+                    for (int i = 0; i < kVRows; ++i)
+                        t[i] += *reinterpret_cast<const v4f *>(from[i] + s * M * R);
+#pragma unroll
+                for (int i = 0; i < kVRows; ++i) {
+                    const int p = pb + kWaves * 4 * i;
+                    if (p >= last)
+                        break;
+                    const int end = s_rows[p] < 64 ? rank : 0;  // v is written up to there
+                    uint16_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        split_bf16(r + e < end ? scale * t[i][e] : 0.f, hi[e], lo[e]);
+                    uint8_t *to = smem + (p - begin) * vpitch + r / 16 * 64 + r % 16 * 2;
+                    *reinterpret_cast<u32x2 *>(to) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+                    *reinterpret_cast<u32x2 *>(to + 32) =
+                        u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+                }
             }
+        }
+        for (int p = begin + threadIdx.x / 16; p < last; p += kWaves * 4) {
             // The other half of the last 16 ranks.
             const int end = (upto + 3) / 4 * 4;
             for (int r = end + threadIdx.x % 16 * 4; r % 16 != 0 && r < (end + 15) / 16 * 16; r += 64) {
@@ -426,7 +447,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
         }
         __syncthreads();
         for (int ct = 0; ct < kCols; ++ct) {
-            const int n0 = c0 + 64 * ct, n = n0 + lane % 8 * 8;
+            const int n0 = c0 + 64 * kWaves * ct, n = n0 + lane % 8 * 8;
             if (n0 >= N)
                 break;
             if (passes == 1) {
@@ -476,8 +497,11 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                     for (int i = 0; i < 2; ++i) {
                         const int p = p0 + 8 * i + lane / 8;
                         const uint8_t *from = sums + (8 * i + lane / 8) * kPitch + lane % 8 * 32;
-                        const v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
+                        v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
                         if (p < last && n < N) {
+                            const int row = s_rows[p];
+                            if (row >= 64)
+                                t0 = t1 = v4f{-0.f, -0.f, -0.f, -0.f};
                             const u32x4 y = bv[tile][i];
                             u32x4 o;
 #pragma unroll
@@ -486,7 +510,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                                 o[q] = pack_bf16x2(t[2 * q % 4] + bf16_to_f32(y[q] & 0xffffu),
                                                    t[2 * q % 4 + 1] + __uint_as_float(y[q] & 0xffff0000u));
                             }
-                            *reinterpret_cast<u32x4 *>(out + (row0 + s_rows[p]) * ldo + n) = o;
+                            *reinterpret_cast<u32x4 *>(out + (row0 + row % 64) * ldo + n) = o;
                         }
                     }
                 }

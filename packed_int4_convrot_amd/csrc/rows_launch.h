@@ -53,10 +53,10 @@ constexpr int kLoraRankBlock = 64;
 constexpr int64_t kLoraFewRows = 1024;
 inline int64_t lora_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tiles of 16 rows that the sets of a window can have, a set being the rows of one
-// adapter, or those without one: rows / 16 and 15 / 16 of a tile for each set.
+// adapter (rows without one join the first): rows / 16 and 15 / 16 of a tile for each set.
 inline int lora_slots(int64_t M, int64_t L)
 {
-    const int64_t rows = M < kLoraWindow ? M : kLoraWindow, sets = rows < L + 1 ? rows : L + 1;
+    const int64_t rows = M < kLoraWindow ? M : kLoraWindow, sets = rows < L ? rows : L;
     return (int)((rows + 15 * sets) / 16);
 }
 // Parts the K columns are split into, so that few rows still fill the chip: about

@@ -398,6 +398,22 @@ def test_lora_rows_without_an_adapter_keep_base(M):
     assert_within(out, *ref_lora(x, a, b, sc, None, index, y))
 
 
+@pytest.mark.parametrize("M", [9, 70, 1100])
+def test_lora_rows_without_an_adapter_beside_rows_that_have_one(M):
+    """They keep every bit of base (-0 and NaN too), whatever the neighbours' adapter holds."""
+    x, a, b, _, _, _, y = lora_case(M, 128, 80, 16, 2, seed=M)
+    index = torch.randint(-1, 2, (M,), device=DEV, generator=gen(M), dtype=torch.int32)
+    index[0], index[-1] = -1, 1
+    b[1, 5, 3], b[1, 7, 0] = float("inf"), float("nan")
+    y[:, 3], y[:, 4], y[:, 6] = -0.0, float("nan"), float("inf")
+    out = ck.lora_add(x, ck.LoraAdapters(a, b), index, base=y)
+    assert torch.equal(bits(out)[index < 0], bits(y)[index < 0])
+    assert out[index == 1][:, [5, 7]].float().isfinite().sum() == 0
+    keep = [c for c in range(80) if c not in (3, 4, 5, 6, 7)]
+    ref, tol = ref_lora(x, a, b, None, None, index, y)
+    assert_within(out[:, keep], ref[:, keep], tol[:, keep])
+
+
 @pytest.mark.parametrize("M,R", [(37, 40), (290, 40), (5, 200), (280, 200), (1100, 40)])
 def test_lora_ignores_what_lies_beyond_a_rank(M, R):
     x, a, b, sc, _, index, y = lora_case(M, 192, 144, R, 4, seed=M)
