@@ -345,9 +345,10 @@ ck_status ck_moe_route(const void *logits, int32_t logit_kind, int64_t T, int64_
                        int32_t renormalize, int32_t *ids, float *weights, void *stream);
 
 /* Bytes of workspace ck_moe_w4a16 / ck_moe_experts_w4a16 need for T tokens, inner
- * width I, E experts and k slots a token: the routing plan and the hidden
- * activations of one pass (1024 (token, slot) pairs; more tokens run as several
- * passes over the same workspace).  0 for sizes the entry points refuse. */
+ * width I, E experts and k slots a token: the hidden activations and the fp32
+ * results of one pass (up to 1024 (token, slot) pairs; more tokens, or more than
+ * 8192 result columns a pair, run as several passes over the same workspace).
+ * 0 for sizes the entry points refuse. */
 size_t ck_moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int32_t k);
 
 /*
@@ -368,7 +369,7 @@ size_t ck_moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int32_t k);
  *   ws      device workspace of at least ck_moe_workspace_bytes(T, I, E, k)
  *           bytes, 256-byte aligned (CK_ERR_WORKSPACE otherwise); scratch
  * H % 64 == 0, I % 64 == 0 (CK_ERR_INVALID_ARG); H, I <= 32768, E <= 1024,
- * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0; every pass of 1024 / k
+ * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0; every pass of up to 1024 / k
  * tokens reads its experts' weights anew.  A non-finite x or h reaches only its own token's
  * row (as NaN where the weights' offsets cancel).
  */
