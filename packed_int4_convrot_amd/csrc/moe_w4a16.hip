@@ -152,7 +152,8 @@ struct Shared {
     int expert[kMaxSets], count[kMaxSets];
     uint16_t pairs[kMaxSets][kSetPairs], tokens[kMaxSets][kSetPairs];
 };
-static_assert(sizeof(int) * kRouteMaxExperts <= kChunkOperands, "the experts' counts lie in the operands' place");
+static_assert(sizeof(int) * kRouteMaxExperts + sizeof(uint16_t) * kMoePairs <= kChunkOperands,
+              "the experts' counts and the ids lie in the operands' place");
 static_assert(sizeof(Shared) <= 160 * 1024, "LDS");
 
 struct Run {
@@ -162,62 +163,69 @@ struct Run {
     int units;       // of a set
 };
 
-__device__ __forceinline__ int wave_sum_int(int v)
-{
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
-// whole: A lies in LDS whole, so that waves can have unlike columns.
+// whole: A lies in LDS whole, so that waves can have unlike columns.  Everything
+// here precedes the first weight, so dependent steps are kept few: the ids are
+// read once, and what is divided is divided in lanes side by side.
 __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int k, int E, int tiles, int stages, bool whole, Shared &s)
 {
+    constexpr int kThreads = kWaves * kWave, kEach = kMoePairs / kThreads;
+    static_assert(kWaves == 8, "slices");
     int *cnt = reinterpret_cast<int *>(s.operands);
+    uint16_t *chosen = reinterpret_cast<uint16_t *>(cnt + kRouteMaxExperts);
     const int t = threadIdx.x, lane = t % kWave, wave = t / kWave;
-    for (int e = t; e < E; e += kWaves * kWave)
+    int mine[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        mine[i] = i * kThreads + t < P ? ids[i * kThreads + t] : -1;
+    for (int e = t; e < E; e += kThreads)
         cnt[e] = 0;
     __syncthreads();
-    for (int p = t; p < P; p += kWaves * kWave) {
-        const int e = ids[p];
-        if (e >= 0 && e < E)
-            atomicAdd(&cnt[e], 1);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const bool live = mine[i] >= 0 && mine[i] < E;
+        chosen[i * kThreads + t] = live ? (uint16_t)mine[i] : (uint16_t)0xffff;
+        if (live)
+            atomicAdd(&cnt[mine[i]], 1);
     }
     __syncthreads();
     int sets = 0;
     for (int c = 0; c < E; c += kWave)
         sets += c + lane < E ? (cnt[c + lane] + kSetPairs - 1) / kSetPairs : 0;
-    sets = wave_sum_int(sets);
-    // The longest run of units, in stages (doubled; joining slices costs about half a stage).
+    sets = __builtin_amdgcn_readlane(wave_scan(sets), kWave - 1);
+    // The longest run of units, in stages (doubled; joining slices costs about half
+    // a stage): lane i has S = 2^i.
+    const unsigned grid = gridDim.x;
     Run r;
-    int best = 0x7fffffff;
-    for (int S = 1; S <= kWaves; S *= 2) {
+    {
+        const int log = lane % 4, S = 1 << log, units = (tiles * S + kWaves - 1) / kWaves;
+        const int rounds = (int)(((unsigned)(sets * units) + grid - 1) / grid);
+        int cost = rounds * (2 * ((stages + S - 1) >> log) + (S > 1 ? 1 : 0));
         if (S > 1 && (!whole || S > stages))
-            break;
-        const int units = (tiles * S + kWaves - 1) / kWaves;
-        const int rounds = (sets * units + (int)gridDim.x - 1) / (int)gridDim.x;
-        const int cost = rounds * (2 * ((stages + S - 1) / S) + (S > 1 ? 1 : 0));
-        if (cost < best)
-            best = cost, r.slices = S, r.units = units;
+            cost = 0x7fffffff;
+        int best = __builtin_amdgcn_readlane(cost, 0);
+        r.slices = 1;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            const int c = __builtin_amdgcn_readlane(cost, i);
+            if (c < best)
+                best = c, r.slices = 1 << i;
+        }
     }
-    const int total = sets * r.units;
-    r.q0 = (int)((int64_t)total * blockIdx.x / gridDim.x);
-    r.q1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-    r.first_set = r.q0 / r.units;
+    r.units = (tiles * r.slices + kWaves - 1) / kWaves;
+    // At most 1152 sets of 2048 units, times 256 workgroups.
+    const unsigned bound = (unsigned)(sets * r.units) * (blockIdx.x + (lane & 1)) / grid;
+    r.q0 = __builtin_amdgcn_readlane((int)bound, 0);
+    r.q1 = __builtin_amdgcn_readlane((int)bound, 1);
+    const unsigned in_set = (unsigned)(lane & 1 ? r.q1 - 1 : r.q0) / (unsigned)r.units;
+    r.first_set = __builtin_amdgcn_readlane((int)in_set, 0);
+    const int last_set = __builtin_amdgcn_readlane((int)in_set, 1);
     // Wave i finds the run's i-th set: its expert, and its pairs in ascending order.
     const int set = r.first_set + wave;
-    if (r.q0 < r.q1 && set <= (r.q1 - 1) / r.units) {
+    if (r.q0 < r.q1 && set <= last_set) {
         int before = 0, expert = 0, first = 0, count = 0;
         for (int c = 0; c < E; c += kWave) {
-            const int n = c + lane < E ? cnt[c + lane] : 0;
-            int v = (n + kSetPairs - 1) / kSetPairs;
-            const int own = v;
-#pragma unroll
-            for (int d = 1; d < kWave; d <<= 1) {
-                const int u = __shfl_up(v, d);
-                if (lane >= d)
-                    v += u;
-            }
+            const int n = c + lane < E ? cnt[c + lane] : 0, own = (n + kSetPairs - 1) / kSetPairs;
+            const int v = wave_scan(own);
             const uint64_t here = __ballot(before + v - own <= set && set < before + v);
             if (here) {
                 const int l = __builtin_ctzll(here);
@@ -230,7 +238,7 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int k, int E,
         }
         int seen = -first;
         for (int c = 0; c < P && seen < kSetPairs; c += kWave) {
-            const uint64_t mask = __ballot(c + lane < P && ids[c + lane] == expert);
+            const uint64_t mask = __ballot(chosen[c + lane] == expert);
             const int at = seen + __builtin_popcountll(mask & ((uint64_t(1) << lane) - 1));
             if ((mask >> lane & 1) && at >= 0 && at < kSetPairs)
                 s.pairs[wave][at] = (uint16_t)(c + lane), s.tokens[wave][at] = (uint16_t)((c + lane) / k);
@@ -246,39 +254,50 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int k, int E,
 // Cursor over a wave's tiles of a run: one in each unit, where there is one.
 struct RunCursor {
     const int *expert;
-    int q, q1, first_set, units, per_unit, tiles, rows, mine, st, st0, st1;
+    int q, q1, set, at;  // the next unit: of the run, its set, its place in the set
+    int units, per_unit, tiles, rows, mine, st, st0, st1;
     __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int tiles_, int rows_, int stages)
-        : expert(s.expert), q(r.q0), q1(r.q1), first_set(r.first_set), units(r.units), per_unit(kWaves / r.slices),
+        : expert(s.expert), q(r.q0), q1(r.q1), set(0), at(r.q0 - r.first_set * r.units), units(r.units),
           tiles(tiles_), rows(rows_)
     {
-        const int wave = threadIdx.x / kWave, slice = wave % r.slices;
-        mine = wave / r.slices;
-        st0 = slice * stages / r.slices, st1 = (slice + 1) * stages / r.slices;
+        // 1, 2, 4 or 8 slices.
+        const int wave = threadIdx.x / kWave, log = __builtin_ctz(r.slices), slice = wave & (r.slices - 1);
+        per_unit = kWaves >> log;
+        mine = wave >> log;
+        st0 = slice * stages >> log, st1 = (slice + 1) * stages >> log;
         st = st0;
     }
-    __device__ __forceinline__ int tile(int unit) const { return unit % units * per_unit + mine; }
+    __device__ __forceinline__ int tile(int place) const { return place * per_unit + mine; }
+    __device__ __forceinline__ void step()
+    {
+        ++q;
+        if (++at == units)
+            at = 0, ++set;
+    }
     __device__ __forceinline__ bool next(WeightStream<> &ws, int &stage)
     {
         if (st == st0) {
-            while (q < q1 && tile(q) >= tiles)
-                ++q;
+            while (q < q1 && tile(at) >= tiles)
+                step();
             if (q >= q1)
                 return false;
-            ws.tile(__builtin_amdgcn_readfirstlane(expert[q / units - first_set]), tile(q) * rows);
+            ws.tile(__builtin_amdgcn_readfirstlane(expert[set]), tile(at) * rows);
         }
         stage = st;
-        if (++st == st1)
-            st = st0, ++q;
+        if (++st == st1) {
+            st = st0;
+            step();
+        }
         return true;
     }
 };
 
-// Units [q0, q1) of one set against kRows rows of A.  With 16 rows, rows 8-15 are
+// Units [q0, q1) of the run's set `set` against kRows rows of A.  With 16 rows, rows 8-15 are
 // added to rows 0-7.  done(tile, sum) stores a tile's results and returns how many
 // vector stores that is at least.
 template <int kRows, class Load, class Done>
 __device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor, const Run &r, bool zeros, int q0,
-                                           int q1, Shared &s, Load &&load, Done &&done)
+                                           int q1, int set, Shared &s, Load &&load, Done &&done)
 {
     constexpr int kGroups = kChunkElems / 64 / kRows, kRegs = ARows<kRows>::kRegs;
     const int G = ws.G, wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
@@ -292,7 +311,7 @@ __device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor
         return stores;
     };
     for (int q = q0; q < q1; ++q) {
-        const int tile = cursor.tile(q);
+        const int tile = cursor.tile(q - (r.first_set + set) * r.units);
 #pragma unroll
         for (int i = 0; i < kRegs; ++i)
             tot[i] = 0.f;
@@ -318,13 +337,13 @@ __device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor
             for (int i = 0; i < 4; ++i)
                 part[wave][i][lane] = tot[i];
             __syncthreads();
-            if (wave % r.slices == 0)
+            if ((wave & (r.slices - 1)) == 0)
                 for (int w = 1; w < r.slices; ++w)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tot[i] += part[wave + w][i][lane];
         }
-        if (tile < cursor.tiles && wave % r.slices == 0) {
+        if (tile < cursor.tiles && (wave & (r.slices - 1)) == 0) {
             held_tile = tile;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -338,9 +357,8 @@ __device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor
 // rows); A's rows are the set's tokens.
 template <int kRows>
 __device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
-                                       int q1, Shared &s)
+                                       int q1, int set, Shared &s)
 {
-    const int set = q0 / r.units - r.first_set;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
         const int t = s.tokens[set][min(row, count - 1)];
@@ -357,7 +375,7 @@ __device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunC
         }
         return 2 * min(4, count);  // of the lower half's rows at least
     };
-    stream_set<kRows>(ws, cursor, r, p.z1 != nullptr, q0, q1, s, load, done);
+    stream_set<kRows>(ws, cursor, r, p.z1 != nullptr, q0, q1, set, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs p)
@@ -368,12 +386,13 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs 
     WeightStream<> ws(p.w1, p.s1, p.z1, 2 * p.I, p.H / 64, p.I, s.ring[threadIdx.x / kWave]);
     const Run r = plan_run(p.r.ids, p.P, p.k, p.E, tiles, ws.stages(), p.H * kSetPairs <= kChunkElems, s);
     RunCursor cursor(r, s, tiles, 16, ws.stages());
-    for (int q = r.q0; q < r.q1;) {
-        const int end = min(r.q1, (q / r.units + 1) * r.units);
-        if (s.count[q / r.units - r.first_set] <= 4)
-            up_set<4>(p, ws, cursor, r, q, end, s);
+    int q = r.q0;
+    for (int set = 0; q < r.q1; ++set) {
+        const int end = min(r.q1, (r.first_set + set + 1) * r.units);
+        if (s.count[set] <= 4)
+            up_set<4>(p, ws, cursor, r, q, end, set, s);
         else
-            up_set<8>(p, ws, cursor, r, q, end, s);
+            up_set<8>(p, ws, cursor, r, q, end, set, s);
         q = end;
     }
 }
@@ -488,10 +507,9 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
 // to moe_combine_kernel.
 template <int kPairs>
 __device__ __forceinline__ void down_set(const DownArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
-                                         int q1, Shared &s)
+                                         int q1, int set, Shared &s)
 {
     constexpr int kRows = 2 * kPairs;
-    const int set = q0 / r.units - r.first_set;
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
     const auto load = [&](int row, int ch) {
         const int pr = s.pairs[set][min(row % kPairs, count - 1)];
@@ -509,7 +527,7 @@ __device__ __forceinline__ void down_set(const DownArgs &p, WeightStream<> &ws, 
         }
         return min(4, count);
     };
-    stream_set<kRows>(ws, cursor, r, p.z2 != nullptr, q0, q1, s, load, done);
+    stream_set<kRows>(ws, cursor, r, p.z2 != nullptr, q0, q1, set, s, load, done);
 }
 
 __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownArgs p)
@@ -520,18 +538,20 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownA
     WeightStream<> ws(p.w2, p.s2, p.z2, p.H, p.I / 64, 16, s.ring[threadIdx.x / kWave]);
     const Run r = plan_run(p.ids, p.T * p.k, p.k, p.E, tiles, ws.stages(), p.I * 2 * kSetPairs <= kChunkElems, s);
     RunCursor cursor(r, s, tiles, 32, ws.stages());
-    for (int q = r.q0; q < r.q1;) {
-        const int end = min(r.q1, (q / r.units + 1) * r.units);
-        if (s.count[q / r.units - r.first_set] <= 4)
-            down_set<4>(p, ws, cursor, r, q, end, s);
+    int q = r.q0;
+    for (int set = 0; q < r.q1; ++set) {
+        const int end = min(r.q1, (r.first_set + set + 1) * r.units);
+        if (s.count[set] <= 4)
+            down_set<4>(p, ws, cursor, r, q, end, set, s);
         else
-            down_set<8>(p, ws, cursor, r, q, end, s);
+            down_set<8>(p, ws, cursor, r, q, end, set, s);
         q = end;
     }
 }
 
 // out[t] = sum over the slots, in order; four columns a thread, a token a grid row.
-// Eight slots' loads are in flight at a time.
+// Eight slots' loads are in flight at a time, and wait for no id: an empty slot's
+// results are in the workspace too, and not used.
 __global__ __launch_bounds__(64) void moe_combine_kernel(const DownArgs p)
 {
     const int t = blockIdx.y, n = (blockIdx.x * 64 + threadIdx.x) * 4;
@@ -547,9 +567,7 @@ __global__ __launch_bounds__(64) void moe_combine_kernel(const DownArgs p)
             const int pr = t * p.k + min(j0 + j, p.k - 1), e = p.ids[pr];
             live[j] = j0 + j < p.k && e >= 0 && e < p.E;
             w[j] = p.weights[pr];
-            v[j] = v4f{0.f, 0.f, 0.f, 0.f};
-            if (live[j])
-                v[j] = *reinterpret_cast<const v4f *>(p.y + (int64_t)pr * p.H + n);
+            v[j] = *reinterpret_cast<const v4f *>(p.y + (int64_t)pr * p.H + n);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)

@@ -40,10 +40,6 @@ __device__ __forceinline__ v4f mfma16(v8bf a, v8bf b, v4f c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ v8bf bf16_ones()
-{
-    return __builtin_bit_cast(v8bf, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
-}
 
 // fp32 as the sum of two bf16: 16 significant bits.  The second part of a
 // value whose first is not finite is 0, so that infinities stay infinities.
@@ -69,6 +65,21 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     v = max(v, dpp_or_zero<0x142, 0xa>(v));  // row_bcast:15
     v = max(v, dpp_or_zero<0x143, 0xc>(v));  // row_bcast:31
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Sums over the lanes up to each, the same way; lane 63 has the wave's.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_add(int v)
+{
+    return v + (int)dpp_or_zero<kCtrl, kRows>((uint32_t)v);
+}
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);
+    return dpp_add<0x143, 0xc>(v);
 }
 // Sum over the wave, in a fixed order.
 __device__ __forceinline__ float wave_sum(float v)

@@ -259,8 +259,8 @@ __device__ __forceinline__ void put_chunk(uint8_t *operands, float *sums, int ro
 
 // A for a workgroup of kWaves waves, in LDS: whole where it fits, else in chunks
 // of 32768 / kRows columns.  load(row, chunk of 8 columns) gives columns in operand
-// order.  started() runs between A's loads and the barrier: loads retire in
-// order, so weights issued there arrive behind A.
+// order.  started() runs first: weights issued there arrive before A, whose
+// loads' wait covers them.
 constexpr int kChunkElems = 32768;
 constexpr int kChunkOperands = kChunkElems * 2, kChunkSums = kChunkElems / 64;
 
@@ -275,6 +275,8 @@ __device__ __forceinline__ void fill_rows(int G, int g0, uint8_t *operands, floa
     // kept in registers through the streaming loops.
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
+    started();
+    __builtin_amdgcn_sched_barrier(0);
     u32x4 v[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -284,8 +286,6 @@ __device__ __forceinline__ void fill_rows(int G, int g0, uint8_t *operands, floa
         if (o / 8 < rows_groups && g < G)
             v[i] = load(o / 8 % kRows, g * 8 + o % 8);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    started();
     __syncthreads();  // what was there has been read
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
