@@ -5,7 +5,9 @@
 // of the k rounds the wave's maximum key, and among the lanes that hold it the
 // lowest, give the largest logit at its lowest index.  The rounds depend on one
 // another; a round is six shift-and-maximum steps, a ballot and the winner's scan
-// of its own keys.
+// of its own keys.  (Up to 64 experts, counting for each key the keys before it
+// finds all slots at once, but measured no faster: 2.9 against 2.4 us for 5 tokens
+// of 60, k = 4, and the same 4.5 us in front of the experts at k = 8.)
 #pragma once
 
 #include "rows_device.h"
