@@ -447,7 +447,7 @@ _LOGIT_KIND = {torch.float32: CK_LOGITS_F32, torch.bfloat16: CK_LOGITS_BF16}
 
 def _rows(t, name, dtype, device, shape):
     """Row stride of a matrix of exactly this shape, dtype and device with unit column stride."""
-    if t.dtype is not dtype or t.device != device or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
         raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)"
                          % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
     ld, col = t.stride()
@@ -463,7 +463,7 @@ def _rows(t, name, dtype, device, shape):
 
 def _flat(t, name, dtype, device, shape):
     """Pointer of a contiguous tensor of exactly this shape, dtype and device."""
-    if t.dtype is not dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
     return t.data_ptr()
 
@@ -473,7 +473,7 @@ def _logits(logits):
     kind = _LOGIT_KIND.get(logits.dtype)
     if kind is None or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a 2-D fp32 or bf16 GPU tensor")
-    return kind, _rows(logits, "logits", logits.dtype, logits.device, tuple(logits.shape))
+    return kind, _rows(logits, "logits", logits.dtype, logits.device, logits.shape)
 
 
 def _space(workspace, need, device):

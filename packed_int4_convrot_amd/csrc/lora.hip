@@ -11,9 +11,9 @@
 // goes through the sets of its window.
 // The work is bound by memory: x, base and out once, the used adapters once; few
 // rows by the two kernels' latency (one row, K = N = 3840, rank 16: 4.0 + 4.9 us).
-// Measured: 32 rows of as many adapters, N 10240, rank 16: 5.2 + 8.5 us (11 MB);
-// 301 rows of 7, K 10240, N 3840, rank 40: 13 + 8 us (17 MB); 8192 rows of 8 in
-// runs, K 3840, N 10240, rank 64: 37 + 117 us (63 MB of x, 336 MB of base and out).
+// Measured: 32 rows of as many adapters, N 10240, rank 16: 5.2 + 7.0 us (6 MB);
+// 301 rows of 7, K 10240, N 3840, rank 40: 13 + 8 us (15 MB); 8192 rows of 8 in
+// runs, K 3840, N 10240, rank 64: 37 + 116 us (63 MB of x, 336 MB of base and out).
 #include <type_traits>
 
 #include "rows_device.h"
@@ -326,18 +326,18 @@ __device__ __forceinline__ u32x4 mask_ranks(u32x4 w, int r, int rank)
 // sums of 16 rows go through LDS so that base and out are moved in 128-byte
 // runs of a row (8192 rows of rank 64: 250 us without, 132 with).  Four tiles of
 // base are on their way at a time (two: 133 us against 124); with base requested
-// ahead of v too the registers leave one wave a SIMD (170 us).  Now 117 us: two waves
+// ahead of v too the registers leave one wave a SIMD (170 us).  Now 116 us: two waves
 // a SIMD fit beside B_a's operands, so latency shows, 2.9 TB/s of base and out where
 // a copy reaches 5.4.
-template <bool kSlots, int kWaves, int kCols, int kSteps>
-__global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
+template <bool kSlots, int kWaves, int kCols, int kSteps, bool kWide>
+__global__ __launch_bounds__(kWaves * kWave, kSlots ? 1 : 2) void lora_expand_kernel(
     const float *__restrict__ v, int parts, int64_t M, const int32_t *__restrict__ index, int64_t L, int slots, int R,
     const uint16_t *__restrict__ b_w, const float *__restrict__ scaling, const int32_t *__restrict__ ranks, int N,
     const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo)
 {
     constexpr int kPitch = 64 * 4 + 16;      // sums: 16 bytes on from row to row
     constexpr int kVRows = kSlots ? 1 : 4;  // rows of v a thread has on their way
-    constexpr int kAhead = kSlots ? 1 : 4;   // row tiles whose base is on its way
+    constexpr int kAhead = kSlots || kWide ? 1 : 4;   // row tiles whose base is on its way
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ __attribute__((aligned(16))) uint8_t s_out[kWaves][16 * kPitch];
     __shared__ int s_rows[kWave];
@@ -364,18 +364,21 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
         // Few rows: every rank of the slot is loaded, so that no load waits for the
         // adapter's own rank; what lies beyond it meets zeros, and is masked.
         const int upto = kSlots ? (rows.adapter < 0 ? 0 : R) : rank;
-        const int passes = max(1, (upto + kRankBlock - 1) / kRankBlock);
+        const int passes = kWide ? max(1, (upto + kRankBlock - 1) / kRankBlock) : 1;
         u32x4 bf[kSteps][4];
         const auto load_b = [&](int n0, int pass) {
+            int ranks_here = upto;  // opaque, as below
+            if constexpr (!kWide)
+                asm volatile("" : "+s"(ranks_here));
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
                 const int r = pass * kRankBlock + 16 * st + 8 * (quarter % 2);
-                if (pass * kRankBlock + 16 * st < upto)
+                if (pass * kRankBlock + 16 * st < ranks_here)
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const int n = min(n0 + 16 * h + l16, N - 1);
                         bf[st][h] = u32x4{0u, 0u, 0u, 0u};
-                        if (r < upto)
+                        if (r < ranks_here)
                             bf[st][h] = *reinterpret_cast<const u32x4 *>(
                                 b_w + ((int64_t)rows.adapter * N + n) * R + r);
                     }
@@ -398,10 +401,11 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
         const auto load_base = [&](int n0, int p0, u32x4(&to)[2]) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int p = p0 + 8 * i + lane / 8, n = n0 + lane % 8 * 8;
-                const int row = __shfl(rows.order, p & 63);  // by every lane
+                // Past the set or the columns: the last ones again, which are not stored.
+                const int p = min(p0 + 8 * i + lane / 8, last - 1), n = min(n0 + lane % 8 * 8, N - 8);
+                const int row = __shfl(rows.order, p);
                 to[i] = u32x4{0u, 0u, 0u, 0u};
-                if (base && p < last && n < N)
+                if (base)
                     to[i] = *reinterpret_cast<const u32x4 *>(base + (row0 + row) * ldb + n);
             }
         };
@@ -432,6 +436,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                         t[i] += *reinterpret_cast<const v4f *>(from[i] + s * M * R);
 #pragma unroll
                 for (int i = 0; i < kVRows; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);  // one row's masks at a time
                     const int p = pb + kWaves * 4 * i;
                     if (p >= last)
                         break;
@@ -456,6 +461,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
             }
         }
         __syncthreads();
+#pragma unroll 1
         for (int ct = 0; ct < kCols; ++ct) {
             const int n0 = c0 + 64 * kWaves * ct, n = n0 + lane % 8 * 8;
             if (n0 >= N)
@@ -476,6 +482,9 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
                     if (p0 >= last)
                         break;
                     __builtin_amdgcn_sched_barrier(0);
+                    int ranks_here = upto;  // opaque: compared here, not once for all tiles
+                    if constexpr (!kWide)
+                        asm volatile("" : "+s"(ranks_here));
                     v4f acc[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
@@ -488,7 +497,7 @@ __global__ __launch_bounds__(kWaves * kWave) void lora_expand_kernel(
 #pragma unroll
                         for (int st = 0; st < kSteps; ++st) {
                             const int r = pass * kRankBlock + 16 * st;
-                            if (r < upto) {
+                            if (r < ranks_here) {
                                 // Rows past the set repeat its last one and are not stored.
                                 const v8bf vf = *reinterpret_cast<const v8bf *>(
                                     smem + (min(p0 + l16, last - 1) - begin) * vpitch + r * 4 + quarter * 16);
@@ -546,10 +555,10 @@ struct ExpandArgs {
     int64_t ldo;
 };
 
-template <bool kSlots, int kWaves, int kCols, int kSteps>
+template <bool kSlots, int kWaves, int kCols, int kSteps, bool kWide = false>
 hipError_t launch_expand(const ExpandArgs &a, hipStream_t s)
 {
-    const auto kernel = lora_expand_kernel<kSlots, kWaves, kCols, kSteps>;
+    const auto kernel = lora_expand_kernel<kSlots, kWaves, kCols, kSteps, kWide>;
     const int lds = (kSlots ? 16 : kLoraWindow) * ((a.R + 15) / 16 * 64 + 16);  // at most 65 KiB
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
@@ -567,10 +576,12 @@ hipError_t launch_expand(const ExpandArgs &a, hipStream_t s)
 template <bool kSlots, int kWaves, int kCols>
 hipError_t launch_expand_steps(const ExpandArgs &a, hipStream_t s)
 {
-    // As many of B_a's operands in registers as R needs: fewer leave room for more waves.
+    // As many of B_a's operands in registers as R needs: fewer leave room for more
+    // waves.  Beyond 64 ranks they are loaded for every row tile, 64 ranks at a time.
     return a.R <= 16   ? launch_expand<kSlots, kWaves, kCols, 1>(a, s)
            : a.R <= 32 ? launch_expand<kSlots, kWaves, kCols, 2>(a, s)
-                       : launch_expand<kSlots, kWaves, kCols, 4>(a, s);
+           : a.R <= kRankBlock ? launch_expand<kSlots, kWaves, kCols, 4>(a, s)
+                               : launch_expand<kSlots, kWaves, kCols, 4, true>(a, s);
 }
 
 }  // namespace

@@ -263,13 +263,14 @@ __device__ __forceinline__ Run plan_run(const int32_t *ids, int P, int k, int E,
 }
 
 // Cursor over a wave's tiles of a run: one in each unit, where there is one.
+// A tile is kTileRows weight rows (of each kind).
+template <int kTileRows>
 struct RunCursor {
     const int *expert;
-    int q, q1, set, at;  // the next unit: of the run, its set, its place in the set
-    int units, per_unit, tiles, rows, mine, st, st0, st1;
-    __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int tiles_, int rows_, int stages)
-        : expert(s.expert), q(r.q0), q1(r.q1), set(0), at(r.q0 - r.first_set * r.units), units(r.units),
-          tiles(tiles_), rows(rows_)
+    int left, at;  // units to come, and the next one's place in its set, which is expert's first
+    int units, per_unit, tiles, mine, st, st0, st1;
+    __device__ __forceinline__ RunCursor(const Run &r, const Shared &s, int tiles_, int stages)
+        : expert(s.expert), left(r.q1 - r.q0), at(r.q0 - r.first_set * r.units), units(r.units), tiles(tiles_)
     {
         // 1, 2, 4 or 8 slices.
         const int wave = threadIdx.x / kWave, log = __builtin_ctz(r.slices), slice = wave & (r.slices - 1);
@@ -281,18 +282,18 @@ struct RunCursor {
     __device__ __forceinline__ int tile(int place) const { return place * per_unit + mine; }
     __device__ __forceinline__ void step()
     {
-        ++q;
+        --left;
         if (++at == units)
-            at = 0, ++set;
+            at = 0, ++expert;
     }
     __device__ __forceinline__ bool next(WeightStream<> &ws, int &stage)
     {
         if (st == st0) {
-            while (q < q1 && tile(at) >= tiles)
+            while (left > 0 && tile(at) >= tiles)
                 step();
-            if (q >= q1)
+            if (left <= 0)
                 return false;
-            ws.tile(__builtin_amdgcn_readfirstlane(expert[set]), tile(at) * rows);
+            ws.tile(__builtin_amdgcn_readfirstlane(*expert), tile(at) * kTileRows);
         }
         stage = st;
         if (++st == st1) {
@@ -306,8 +307,8 @@ struct RunCursor {
 // Units [q0, q1) of the run's set `set` against kRows rows of A.  With 16 rows, rows 8-15 are
 // added to rows 0-7.  done(tile, sum) stores a tile's results and returns how many
 // vector stores that is at least.
-template <int kRows, class Load, class Done>
-__device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor, const Run &r, bool zeros, int q0,
+template <int kRows, class Cursor, class Load, class Done>
+__device__ __forceinline__ void stream_set(WeightStream<> &ws, Cursor &cursor, const Run &r, bool zeros, int q0,
                                            int q1, int set, Shared &s, Load &&load, Done &&done)
 {
     constexpr int kGroups = kChunkElems / 64 / kRows, kRegs = ARows<kRows>::kRegs;
@@ -367,7 +368,7 @@ __device__ __forceinline__ void stream_set(WeightStream<> &ws, RunCursor &cursor
 // The first product of many pairs: a tile is 16 hidden columns (their gate and up
 // rows); A's rows are the set's tokens.
 template <int kRows>
-__device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
+__device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunCursor<16> &cursor, const Run &r, int q0,
                                        int q1, int set, Shared &s)
 {
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32, count = s.count[set];
@@ -377,11 +378,13 @@ __device__ __forceinline__ void up_set(const UpArgs &p, WeightStream<> &ws, RunC
             u32x4, act_order8(*reinterpret_cast<const u32x4 *>(p.x + (int64_t)t * p.ldx + ch * 8)));
     };
     const auto done = [&](int tile, const float(&tot)[4]) {
+        int rows = count, column = l32;  // opaque: compared here, no masks kept through the stream
+        asm volatile("" : "+v"(rows), "+v"(column));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float u = __shfl_xor(tot[i], 16);
             const int row = (kRows > 4 ? 4 * half : 0) + i;
-            if (l32 < 16 && (kRows > 4 || half == 0) && row < count)
+            if (column < 16 && (kRows > 4 || half == 0) && row < rows)
                 put_hidden(p.hidden, s.pairs[set][row], p.I, tile * 16 + l32, tot[i], u);
         }
         return 2 * min(4, count);  // of the lower half's rows at least
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void moe_up_kernel(const UpArgs 
     const int tiles = p.I / 16;
     WeightStream<> ws(p.w1, p.s1, p.z1, 2 * p.I, p.H / 64, p.I, s.ring[threadIdx.x / kWave]);
     const Run r = plan_run(p.r.ids, p.P, p.k, p.E, tiles, ws.stages(), p.H * kSetPairs <= kChunkElems, s);
-    RunCursor cursor(r, s, tiles, 16, ws.stages());
+    RunCursor<16> cursor(r, s, tiles, ws.stages());
     int q = r.q0;
     for (int set = 0; q < r.q1; ++set) {
         const int end = min(r.q1, (r.first_set + set + 1) * r.units);
@@ -517,7 +520,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void moe_down_few_kernel(const D
 // first parts of the set's pairs, then the second parts; the sums of each pair go
 // to moe_combine_kernel.
 template <int kPairs>
-__device__ __forceinline__ void down_set(const DownArgs &p, WeightStream<> &ws, RunCursor &cursor, const Run &r, int q0,
+__device__ __forceinline__ void down_set(const DownArgs &p, WeightStream<> &ws, RunCursor<32> &cursor, const Run &r, int q0,
                                          int q1, int set, Shared &s)
 {
     constexpr int kRows = 2 * kPairs;
@@ -548,7 +551,7 @@ __global__ __launch_bounds__(kWaves * kWave, 2) void moe_down_kernel(const DownA
     const int tiles = p.H / 32;
     WeightStream<> ws(p.w2, p.s2, p.z2, p.H, p.I / 64, 16, s.ring[threadIdx.x / kWave]);
     const Run r = plan_run(p.ids, p.T * p.k, p.k, p.E, tiles, ws.stages(), p.I * 2 * kSetPairs <= kChunkElems, s);
-    RunCursor cursor(r, s, tiles, 32, ws.stages());
+    RunCursor<32> cursor(r, s, tiles, ws.stages());
     int q = r.q0;
     for (int set = 0; q < r.q1; ++set) {
         const int end = min(r.q1, (r.first_set + set + 1) * r.units);
