@@ -511,11 +511,21 @@ def moe_workspace_bytes(T: int, I: int, E: int, k: int) -> int:
     return int(lib.ck_moe_workspace_bytes(T, I, E, k))
 
 
+def _addresses(tensors, name):
+    """Their addresses as of now (None for a tensor that was not given).  Read for each call:
+    an address of last time may be freed memory."""
+    at = [None if t is None else t.data_ptr() for t in tensors]
+    if 0 in at:
+        raise ValueError("%s: a tensor has no storage any more" % name)
+    return at
+
+
 class MoeExperts:
     """The packed uint4 weights of a mixture-of-experts layer (AWQ W4A16, group 64):
     w1 uint8 [E, 2I, H/2] (I gate rows, then I up rows), s1 and z1 bf16 [E, H/64, 2I],
     w2 uint8 [E, H, I/2], s2 and z2 bf16 [E, I/64, H]; the zero points may be None.
-    The tensors are kept, not copied."""
+    The tensors' storages are kept, not copied: values written into the tensors later count, a
+    storage that is put in a tensor's place (t.data = ...) does not."""
 
     def __init__(self, w1, s1, z1, w2, s2, z2):
         if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or not isinstance(w2, torch.Tensor) or w2.dim() != 3:
@@ -533,9 +543,11 @@ class MoeExperts:
                 continue
             _dense(t, name, torch.bfloat16, shape)
         _same_device(w1, ("s1", s1), ("z1", z1), ("w2", w2), ("s2", s2), ("z2", z2))
-        self.tensors = (w1, s1, z1, w2, s2, z2)
+        self.tensors = tuple(None if t is None else t.detach() for t in (w1, s1, z1, w2, s2, z2))
         self.E, self.H, self.I, self.device = E, H, I, w1.device
-        self._args = (E, I, 64) + tuple(None if t is None else t.data_ptr() for t in self.tensors)
+
+    def _args(self):
+        return (self.E, self.I, 64, *_addresses(self.tensors, "experts"))
 
 
 def _moe_buffers(x, experts, k, out, workspace):
@@ -560,7 +572,7 @@ def moe(x, logits, experts: MoeExperts, k: int, renormalize: bool = True, out=No
         raise ValueError("logits must have shape (%d, %d) on %s" % (T, experts.E, dev))
     ids, weights = _slots(ids, weights, T, k, dev)
     _check(lib.ck_moe_w4a16(x.data_ptr(), T, experts.H, ldx, logits.data_ptr(), kind, ldl, k, 1 if renormalize else 0,
-                            *experts._args, out.data_ptr(), ldo, _flat(ids, "ids", torch.int32, dev, (T, k)),
+                            *experts._args(), out.data_ptr(), ldo, _flat(ids, "ids", torch.int32, dev, (T, k)),
                             _flat(weights, "weights", torch.float32, dev, (T, k)), workspace.data_ptr(),
                             workspace.numel(), _stream(x)))
     return out, ids, weights
@@ -575,7 +587,7 @@ def moe_experts(x, ids, weights, experts: MoeExperts, out=None, workspace=None):
     T, ldx, out, ldo, workspace = _moe_buffers(x, experts, k, out, workspace)
     dev = experts.device
     _check(lib.ck_moe_experts_w4a16(x.data_ptr(), T, experts.H, ldx, _flat(ids, "ids", torch.int32, dev, (T, k)),
-                                    _flat(weights, "weights", torch.float32, dev, (T, k)), k, *experts._args,
+                                    _flat(weights, "weights", torch.float32, dev, (T, k)), k, *experts._args(),
                                     out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _stream(x)))
     return out
 
@@ -583,7 +595,7 @@ def moe_experts(x, ids, weights, experts: MoeExperts, out=None, workspace=None):
 class LoraAdapters:
     """L slots of low-rank adapters of up to R ranks: a bf16 [L, R, K], b bf16 [L, N, R],
     scaling fp32 [L] or None (1), ranks int32 [L] or None (R); what a slot holds beyond its
-    rank is not used.  The tensors are kept, not copied."""
+    rank is not used.  The tensors' storages are kept, not copied, as in MoeExperts."""
 
     def __init__(self, a, b, scaling=None, ranks=None):
         if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
@@ -596,9 +608,11 @@ class LoraAdapters:
         if ranks is not None:
             _dense(ranks, "ranks", torch.int32, (L,))
         _same_device(a, ("b", b), ("scaling", scaling), ("ranks", ranks))
-        self.tensors = (a, b, scaling, ranks)
+        self.tensors = tuple(None if t is None else t.detach() for t in (a, b, scaling, ranks))
         self.L, self.R, self.K, self.N, self.device = L, R, K, N, a.device
-        self._args = (L, R) + tuple(None if t is None else t.data_ptr() for t in self.tensors) + (N,)
+
+    def _args(self):
+        return (self.L, self.R, *_addresses(self.tensors, "adapters"), self.N)
 
 
 def lora_workspace_bytes(M: int, K: int, R: int, L: int) -> int:
@@ -618,6 +632,6 @@ def lora_add(x, adapters: LoraAdapters, index, base=None, out=None, workspace=No
     workspace = _space(workspace, lib.ck_lora_workspace_bytes(M, adapters.K, adapters.R, adapters.L)
                        if workspace is None else 0, dev)
     _check(lib.ck_lora_add(x.data_ptr(), M, adapters.K, ldx, _flat(index, "index", torch.int32, dev, (M,)),
-                           *adapters._args, None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
+                           *adapters._args(), None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
                            workspace.data_ptr(), workspace.numel(), _stream(x)))
     return out
