@@ -445,8 +445,16 @@ def accumulators_i32(codes, packed):
 _LOGIT_KIND = {torch.float32: CK_LOGITS_F32, torch.bfloat16: CK_LOGITS_BF16}
 
 
+def _row_count(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    return t.shape[0]
+
+
 def _rows(t, name, dtype, device, shape):
     """Row stride of a matrix of exactly this shape, dtype and device with unit column stride."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a tensor" % name)
     if t.dtype is not dtype or t.device != device or t.shape != shape:
         raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)"
                          % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
@@ -463,15 +471,17 @@ def _rows(t, name, dtype, device, shape):
 
 def _flat(t, name, dtype, device, shape):
     """Pointer of a contiguous tensor of exactly this shape, dtype and device."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
     return t.data_ptr()
 
 
 def _logits(logits):
     """(kind, row stride) of a [T, E] GPU matrix of router logits."""
+    _row_count(logits, "logits")
     kind = _LOGIT_KIND.get(logits.dtype)
-    if kind is None or logits.dim() != 2 or not logits.is_cuda:
+    if kind is None or not logits.is_cuda:
         raise ValueError("logits must be a 2-D fp32 or bf16 GPU tensor")
     return kind, _rows(logits, "logits", logits.dtype, logits.device, logits.shape)
 
@@ -480,13 +490,15 @@ def _space(workspace, need, device):
     """A workspace tensor of at least `need` bytes."""
     if workspace is None:
         return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
-    if workspace.dtype is not torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
-            or workspace.device != device:
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.dim() != 1 \
+            or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be a contiguous 1-D uint8 tensor on %s" % device)
     return workspace
 
 
 def _slots(ids, weights, T, k, device):
+    if not 1 <= k < 2 ** 31:
+        raise ValueError("k must be positive (got %s)" % k)
     ids = torch.empty((T, k), dtype=torch.int32, device=device) if ids is None else ids
     weights = torch.empty((T, k), dtype=torch.float32, device=device) if weights is None else weights
     return ids, weights
@@ -551,7 +563,7 @@ class MoeExperts:
 
 
 def _moe_buffers(x, experts, k, out, workspace):
-    T = x.shape[0]
+    T = _row_count(x, "x")
     ldx = _rows(x, "x", torch.bfloat16, experts.device, (T, experts.H))
     out = torch.empty((T, experts.H), dtype=torch.bfloat16, device=experts.device) if out is None else out
     ldo = _rows(out, "out", torch.bfloat16, experts.device, (T, experts.H))
@@ -581,8 +593,7 @@ def moe(x, logits, experts: MoeExperts, k: int, renormalize: bool = True, out=No
 def moe_experts(x, ids, weights, experts: MoeExperts, out=None, workspace=None):
     """The experts' part of moe from given int32 ids and fp32 weights [T, k] (an id outside
     [0, E) is an empty slot): out bf16 [T, H]."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be a 2-D tensor")
+    _row_count(ids, "ids")
     k = ids.shape[1]
     T, ldx, out, ldo, workspace = _moe_buffers(x, experts, k, out, workspace)
     dev = experts.device
@@ -623,7 +634,7 @@ def lora_workspace_bytes(M: int, K: int, R: int, L: int) -> int:
 def lora_add(x, adapters: LoraAdapters, index, base=None, out=None, workspace=None):
     """bf16 [M, N]: base[m] + scaling[l] B_l (A_l x[m]) with l = index[m] (int32 [M]), and base[m]
     where l is outside [0, L).  base None: zeros; out may be base (in place)."""
-    M, dev = x.shape[0], adapters.device
+    M, dev = _row_count(x, "x"), adapters.device
     ldx = _rows(x, "x", torch.bfloat16, dev, (M, adapters.K))
     shape = (M, adapters.N)
     out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else out

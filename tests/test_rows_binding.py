@@ -91,3 +91,35 @@ def test_values_written_into_a_handles_tensors_count(kind, tensors, call, at, ca
     for t in mine:
         t.fill_(3)
     assert all((t == 3).all() for t in handle.tensors)
+
+
+NOT_MATRICES = [None, 3.0, [[1.0] * 64] * 3, torch.ones(()), torch.ones((64,), dtype=torch.bfloat16),
+                torch.ones((1, 3, 64), dtype=torch.bfloat16)]
+
+
+@pytest.mark.parametrize("bad", NOT_MATRICES)
+def test_what_is_not_a_matrix_is_refused(calls, monkeypatch, bad):
+    adapters, experts = ck.LoraAdapters(*adapter_tensors()), ck.MoeExperts(*expert_tensors())
+    monkeypatch.setattr(ck, "_LOGIT_KIND", {})
+    x, index = torch.ones((3, 64), dtype=torch.bfloat16), torch.zeros((3,), dtype=torch.int32)
+    ids, weights = torch.zeros((3, 2), dtype=torch.int32), torch.ones((3, 2))
+    for call in (lambda: ck.lora_add(bad, adapters, index), lambda: ck.lora_add(x, adapters, bad),
+                 lambda: ck.moe_experts(bad, ids, weights, experts), lambda: ck.moe_experts(x, bad, weights, experts),
+                 lambda: ck.moe_experts(x, ids, bad, experts), lambda: ck.moe_route(bad, 2),
+                 lambda: ck.moe(x, bad, experts, 2)):
+        with pytest.raises(ValueError):
+            call()
+    if bad is not None:
+        for call in (lambda: ck.lora_add(x, adapters, index, base=bad), lambda: ck.lora_add(x, adapters, index, out=bad),
+                     lambda: ck.lora_add(x, adapters, index, workspace=bad),
+                     lambda: ck.moe_experts(x, ids, weights, experts, out=bad),
+                     lambda: ck.moe_experts(x, ids, weights, experts, workspace=bad)):
+            with pytest.raises(ValueError):
+                call()
+    assert not calls
+
+
+@pytest.mark.parametrize("k", [0, -1, -2 ** 40, 2 ** 31, 2 ** 32 + 2])
+def test_slot_counts_outside_an_int32_are_refused(k):
+    with pytest.raises(ValueError):
+        ck._slots(None, None, 0, k, torch.device("cpu"))
