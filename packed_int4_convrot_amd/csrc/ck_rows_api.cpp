@@ -70,7 +70,7 @@ int64_t moe_room_pairs(int64_t T, int32_t k)
 
 size_t moe_workspace(int64_t T, int64_t I, int64_t E, int32_t k)
 {
-    if (T <= 0 || I <= 0 || E < 1 || E > ck::kRouteMaxExperts || k < 1 || k > ck::kRouteMaxK || I > kMaxK ||
+    if (T <= 0 || I <= 0 || I % 64 != 0 || E < 1 || E > ck::kRouteMaxExperts || k < 1 || k > ck::kRouteMaxK || I > kMaxK ||
         T > kMaxRows)
         return 0;
     const int64_t P = moe_room_pairs(T, k);
@@ -157,7 +157,8 @@ int moe_common(const char *fn, const uint16_t *x, int64_t T, int64_t H, int64_t 
 
 size_t lora_workspace(int64_t M, int64_t K, int64_t R, int64_t L)
 {
-    if (M <= 0 || M > kMaxRows || K < 64 || K > kMaxK || R < 1 || R > ck::kLoraMaxRank || L < 1)
+    if (M <= 0 || M > kMaxRows || K < 64 || K % 64 != 0 || K > kMaxK || R < 1 || R % 8 != 0 ||
+        R > ck::kLoraMaxRank || L < 1 || L > kMaxRows)
         return 0;
     return round_up((size_t)(ck::lora_splits(M, K, R, L) * M * R) * sizeof(float), kWsAlign);
 }
