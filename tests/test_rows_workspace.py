@@ -1,5 +1,6 @@
 """Workspace queries of the mixture-of-experts layer and the adapters (no GPU): 0 for
 whatever the entry points refuse."""
+import pytest
 
 ck = pytest.importorskip("packed_int4_convrot_amd")
 moe, lora = ck.lib.ck_moe_workspace_bytes, ck.lib.ck_lora_workspace_bytes
