@@ -391,8 +391,9 @@ ck_status ck_moe_experts_w4a16(const uint16_t *x, int64_t T, int64_t H, int64_t 
                                const uint16_t *z2, uint16_t *out, int64_t ldo, void *ws, size_t ws_bytes,
                                void *stream);
 
-/* Bytes of workspace ck_lora_add needs (fp32 [parts, M, R], the number of parts
- * chosen by the sizes).  0 for sizes it refuses. */
+/* Bytes of workspace ck_lora_add needs (fp32 [parts, M, R]; the sizes choose the
+ * number of parts, and the bytes allow for the most).  A workspace of some M, K and
+ * R serves every call with no more of each.  0 for sizes it refuses. */
 size_t ck_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
 
 /*

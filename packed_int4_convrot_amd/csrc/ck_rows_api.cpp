@@ -160,7 +160,7 @@ size_t lora_workspace(int64_t M, int64_t K, int64_t R, int64_t L)
     if (M <= 0 || M > kMaxRows || K < 64 || K % 64 != 0 || K > kMaxK || R < 1 || R % 8 != 0 ||
         R > ck::kLoraMaxRank || L < 1 || L > kMaxRows)
         return 0;
-    return round_up((size_t)(ck::lora_splits(M, K, R, L) * M * R) * sizeof(float), kWsAlign);
+    return round_up((size_t)(ck::lora_room_rows(M, K) * R) * sizeof(float), kWsAlign);
 }
 
 int ck_lora_add_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const int32_t *index, int64_t L, int64_t R,

@@ -66,6 +66,8 @@ inline int lora_slots(int64_t M, int64_t L)
     const int64_t rows = M < kLoraWindow ? M : kLoraWindow, sets = rows < L ? rows : L;
     return (int)((rows + 15 * sets) / 16);
 }
+constexpr int64_t kLoraCus = 256;
+inline int64_t lora_most_splits(int64_t K) { return K / 256 < 1 ? 1 : K / 256 < 8 ? K / 256 : 8; }
 // Parts the K columns are split into, so that few rows still fill the chip: about
 // one workgroup for each of the 256 CUs; a wave keeps a 64-column group at least,
 // and the second product adds at most 8 parts.  Of the tiles that a window's sets
@@ -74,10 +76,18 @@ inline int lora_splits(int64_t M, int64_t K, int64_t R, int64_t L)
 {
     const int64_t slots = M > kLoraFewRows ? 1 : lora_slots(M, L);
     const int64_t tiles = lora_ceil(M, kLoraWindow) * (M > kLoraWindow && L < 16 && slots > 6 ? 6 : slots);
-    int64_t s = 256 / (tiles * lora_ceil(R, kLoraRankBlock));
-    const int64_t most = K / 64 / 4 < 8 ? K / 64 / 4 : 8;
+    int64_t s = kLoraCus / (tiles * lora_ceil(R, kLoraRankBlock));
+    const int64_t most = lora_most_splits(K);
     s = s > most ? most : s;
     return (int)(s < 1 ? 1 : s);
+}
+// Rows of v, over all parts, that the workspace has room for: lora_splits() * M at
+// least, and no fewer for more rows or columns, so that a workspace of the largest
+// call serves every smaller one.  (Several parts need parts * windows <= kLoraCus.)
+inline int64_t lora_room_rows(int64_t M, int64_t K)
+{
+    const int64_t split = lora_most_splits(K) * M, most = kLoraCus * kLoraWindow;
+    return M > most ? M : split < most ? split : most;
 }
 // Workgroups of 256 threads of the second product; a launch takes fewer than 2^24.
 inline int64_t lora_blocks(int64_t M, int64_t N, int64_t L)
