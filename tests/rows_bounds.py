@@ -97,6 +97,14 @@ LAYERS = [
     (1, 512, 320, 40, 8, False), (8, 512, 192, 16, 4, False), (40, 1088, 704, 6, 6, False), (33, 256, 128, 8, 2, True),
     (129, 64, 64, 70, 8, False), (8, 3840, 1280, 4, 2, False), (12, 3840, 1280, 4, 2, False),
     (37, 2112, 832, 6, 5, True),
+    # x in chunks: sets of more than four pairs from 4096 columns on, all from 8192 on; passes cut by the results' room
+    (20, 4160, 192, 16, 2, True), (20, 8256, 128, 16, 2, True), (40, 8256, 64, 16, 1, True), (40, 16384, 64, 16, 1, True),
+    (3, 32768, 64, 3, 2, False),
+    # one token and a few whose hidden columns do not fit the few-pair form; h in chunks from 2048 columns on
+    (1, 192, 1600, 40, 8, False), (2, 64, 2112, 9, 2, False), (20, 128, 2112, 8, 2, True), (24, 64, 4160, 6, 2, True),
+    # sixteen logits a lane in front of few pairs; more than eight slots
+    (1, 128, 64, 300, 8, False), (2, 64, 128, 1024, 8, False), (1, 128, 64, 20, 12, False), (5, 128, 192, 40, 20, False),
+    (3, 64, 128, 64, 32, False),
 ]
 
 

@@ -1,4 +1,6 @@
-"""The mixture-of-experts layer against fp64 within rows_bounds' error bounds."""
+"""The mixture-of-experts layer against fp64 within rows_bounds' error bounds: also wide layers
+(activations in chunks, passes cut by the results' room), few pairs in either form, many
+experts and slots."""
 import pytest
 import torch
 
