@@ -1,6 +1,6 @@
 """The mixture-of-experts layer against fp64 within rows_bounds' error bounds: also wide layers
 (activations in chunks, passes cut by the results' room), few pairs in either form, many
-experts and slots."""
+experts and slots, weights beyond 32-bit offsets."""
 import pytest
 import torch
 
@@ -26,3 +26,28 @@ def test_layer(case, kind, renormalize):
     check_route(logits, k, renormalize, ids, w)
     assert refused(out, *layer(x, ids, w, tensors)) is None
     assert torch.equal(bits(out), bits(ck.moe_experts(x, ids, w, experts)))
+
+
+@pytest.mark.parametrize("T,I", [(2, 1280), (12, 2112)])
+def test_weights_beyond_32_bit_offsets(T, I):
+    """Few and many pairs: the last experts of slabs of more than 4 GiB, all of it distinct
+    weights, give the bits that the same experts give by themselves."""
+    E, H, k = 1024, 4096, 2
+    g = torch.Generator(device=DEV).manual_seed(I)
+
+    def one(N, K):
+        p = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+        s = torch.empty((E, K // 64, N), dtype=torch.bfloat16, device=DEV).uniform_(0.002, 0.02, generator=g)
+        z = torch.empty((E, K // 64, N), dtype=torch.bfloat16, device=DEV).normal_(0, 0.01, generator=g)
+        return p, s, z
+    big = one(2 * I, H) + one(H, I)
+    assert big[0].numel() > 2 ** 32 and big[3].numel() > 2 ** 31 and (I < 2112 or big[3].numel() > 2 ** 32)
+    print("offsets T=%d I=%d" % (T, I), flush=True)
+    first = E - 3
+    small = [t[first:].clone() for t in big]
+    x = torch.randn((T, H), device=DEV, generator=g).bfloat16()
+    ids = torch.stack((torch.arange(T, device=DEV) % 3, (torch.arange(T, device=DEV) + 1) % 3), dim=1).int()
+    w = torch.rand((T, k), device=DEV, generator=g)
+    out = ck.moe_experts(x, ids + first, w, ck.MoeExperts(*big))
+    assert torch.equal(bits(out), bits(ck.moe_experts(x, ids, w, ck.MoeExperts(*small))))
+    assert refused(out, *layer(x, ids, w, small)) is None
