@@ -371,7 +371,11 @@ size_t ck_moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int32_t k);
  * H % 64 == 0, I % 64 == 0 (CK_ERR_INVALID_ARG); H, I <= 32768, E <= 1024,
  * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0; every pass of up to 1024 / k
  * tokens reads its experts' weights anew.  A non-finite x or h reaches only its own token's
- * row (as NaN where the weights' offsets cancel).
+ * row.
+ * Range: the sums run over codes offset by 128 and are corrected by x's sum, as in
+ * ck_w4a16_gemv.  They stay finite for |x| and |h| up to 1e34 / max(1, S), S the sum of
+ * |s| + |z| over a weight row's groups; beyond that, and where x, h, a scale or a zero
+ * point is infinite, a result can be NaN where the formula gives a number or an infinity.
  */
 ck_status ck_moe_w4a16(const uint16_t *x, int64_t T, int64_t H, int64_t ldx, const void *logits, int32_t logit_kind,
                        int64_t ldl, int32_t k, int32_t renormalize, int64_t E, int64_t I, int32_t Gw,
@@ -403,6 +407,8 @@ size_t ck_lora_workspace_bytes(int64_t M, int64_t K, int64_t R, int64_t L);
  *   out[m] = base[m] + scaling[l] * B_l[:, :r] (A_l[:r] x[m]),  r = ranks[l],
  * and out[m] = base[m] where l is outside [0, L).  fp32 sums (A x is held to 16
  * significant bits between the products), one rounding to bf16.
+ * An infinite element of b gives NaN where the formula may give an infinity (A x is
+ * two bf16 there, and the second may be 0 or of the other sign).
  *   x       bf16 [M, ldx], K columns; index int32 [M]
  *   a, b    bf16 [L, R, K] and [L, N, R], dense, 16-byte aligned: slots of L
  *           adapters of up to R ranks

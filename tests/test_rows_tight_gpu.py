@@ -1,10 +1,10 @@
-"""The mixture-of-experts layer against fp64 within rows_bounds' error bounds: also wide layers
+"""The mixture-of-experts layer against fp64 within rows_bounds' error bounds: wide layers
 (activations in chunks, passes cut by the results' room), few pairs in either form, many
-experts and slots, weights beyond 32-bit offsets."""
+experts and slots, weights beyond 32-bit offsets, activations near the sums' range."""
 import pytest
 import torch
 
-from rows_bounds import LAYERS, layer, layer_inputs, refused
+from rows_bounds import LAYERS, expert_weights, layer, layer_inputs, refused
 from test_rows_gpu import _need_gpu, bits, check_route  # noqa: F401  (the fixture skips without a GPU)
 
 pytestmark = pytest.mark.gpu
@@ -51,3 +51,20 @@ def test_weights_beyond_32_bit_offsets(T, I):
     out = ck.moe_experts(x, ids + first, w, ck.MoeExperts(*big))
     assert torch.equal(bits(out), bits(ck.moe_experts(x, ids, w, ck.MoeExperts(*small))))
     assert refused(out, *layer(x, ids, w, small)) is None
+
+
+@pytest.mark.parametrize("T", [2, 12])
+def test_activations_near_the_range_of_the_sums(T):
+    """|x| just below 3.7e34, of which 64 products with codes up to 143 stay finite."""
+    H, I, E, k = 256, 128, 4, 2
+    tensors = expert_weights(E, H, I, True, seed=T)
+    for i in (1, 2):
+        tensors[i] = (tensors[i].double() * 2.0 ** -118).bfloat16()
+    g = torch.Generator().manual_seed(T)
+    x = (torch.randn((T, H), generator=g).sign() * torch.empty((T, H)).uniform_(3e34, 3.69e34, generator=g)).bfloat16()
+    x[:, :64] = x[:, :64].abs()  # a group whose sum is as large as can be
+    assert x.abs().max() < 3.7e34
+    tensors = [t.to(DEV) for t in tensors]
+    x, logits = x.to(DEV), torch.randn((T, E), generator=g).to(DEV)
+    out, ids, w = ck.moe(x, logits, ck.MoeExperts(*tensors), k)
+    assert out.isfinite().all() and refused(out, *layer(x, ids, w, tensors)) is None
