@@ -116,3 +116,45 @@ def layer_inputs(T, H, I, E, k, crowded, device="cpu"):
     if crowded:
         logits[:, 0] += 4
     return x, logits.to(device), expert_weights(E, H, I, k % 2 == 0, T + H + I + E, device)
+
+
+# M, K, N, R, L: each form of the second product (one wave and four a workgroup, many rows)
+# at 16, 32, 64 ranks and beyond.
+ADAPTERS = [(1, 3840, 512, 16, 3), (32, 3840, 1024, 16, 32), (40, 256, 272, 24, 5), (301, 1024, 528, 40, 7),
+            (100, 320, 144, 136, 3), (300, 192, 1040, 16, 40), (300, 192, 1040, 24, 40), (300, 192, 1040, 64, 40),
+            (300, 128, 1040, 200, 40), (1030, 3840, 80, 16, 4), (1025, 192, 528, 24, 3), (1300, 1024, 528, 64, 8),
+            (1100, 640, 272, 136, 30)]
+
+
+def adapter_inputs(M, K, N, R, L, device="cpu"):
+    """x, index and (a, b, scaling, ranks), the same on every device."""
+    g = torch.Generator().manual_seed(M + K + N + R + L)
+    x = torch.randn((M, K), generator=g).bfloat16()
+    a = (torch.randn((L, R, K), generator=g) / K ** 0.5).bfloat16()
+    b = (torch.randn((L, N, R), generator=g) * 0.3).bfloat16()
+    scaling = torch.empty((L,)).uniform_(0.5, 2, generator=g)
+    ranks = torch.randint(R // 2, R + 1, (L,), dtype=torch.int32, generator=g)
+    index = torch.randint(-1, L, (M,), dtype=torch.int32, generator=g)
+    index[0] = 0
+    return x.to(device), index.to(device), tuple(t.to(device) for t in (a, b, scaling, ranks))
+
+
+def adapters(x, index, tensors, between=lambda v: v, pick=lambda l: l):
+    """out fp64 [M, N] without base and its error's bound before the last rounding, as `layer`:
+    sums of K and R terms, scaling A x held to 16 significant bits."""
+    a, b, scaling, ranks = tensors
+    K, R = a.shape[2], a.shape[1]
+    out = torch.zeros((x.shape[0], b.shape[1]), dtype=torch.float64, device=x.device)
+    err = torch.zeros_like(out)
+    for l in range(a.shape[0]):
+        rows = (index == l).nonzero().flatten()
+        if not rows.numel():
+            continue
+        p = pick(l)
+        r = int(ranks[p])
+        xa, aa, ba = x[rows].double(), a[p, :r].double(), b[p, :, :r].double()
+        v = between(float(scaling[p]) * (xa @ aa.t()))
+        dv = abs(float(scaling[p])) * SURE * U * (K + 64) ** 0.5 * (xa.abs() @ aa.abs().t()) + (2.0 ** -16 + 4 * U) * v.abs()
+        out[rows] = v @ ba.t()
+        err[rows] = SURE * (dv.square() @ ba.square().t()).sqrt() + SURE * U * (2 * R + 64) ** 0.5 * (v.abs() @ ba.abs().t())
+    return out, err

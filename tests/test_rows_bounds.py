@@ -1,10 +1,10 @@
-"""The bounds of the mixture-of-experts tests refuse wrong results (no GPU): for every
-case of the GPU tests the fp64 layer with a mistake planted in it, and the correctly rounded
-result taken."""
+"""The bounds of the mixture-of-experts and adapter tests refuse wrong results (no GPU): for
+every case of the GPU tests the fp64 definition with a mistake planted in it, and the
+correctly rounded result taken."""
 import pytest
 import torch
 
-from rows_bounds import LAYERS, layer, layer_inputs, refused
+from rows_bounds import ADAPTERS, LAYERS, adapter_inputs, adapters, layer, layer_inputs, refused
 
 
 @pytest.mark.parametrize("case", LAYERS)
@@ -53,5 +53,34 @@ def test_mistakes_are_refused(case):
     if 2048 < I < 4096 + 64:
         wrong["h's first 2048 columns again"] = layer(
             x, ids, w, tensors, hidden=lambda h: torch.cat((h[:, :2048], h[:, :I - 2048]), dim=1))[0]
+    for name, bad in wrong.items():
+        assert refused(bad.to(torch.bfloat16), ref, err) is not None, name
+
+
+@pytest.mark.parametrize("case", ADAPTERS)
+def test_mistakes_in_adapters_are_refused(case):
+    M, K, N, R, L = case
+    x, index, tensors = adapter_inputs(*case)
+    a, b, scaling, ranks = tensors
+    ref, err = adapters(x, index, tensors)
+    right = ref.to(torch.bfloat16)
+    assert refused(right, ref, err) is None
+    lost = x.clone()
+    lost[:, K - 1] = 0
+    wrong = {
+        "nothing": torch.zeros_like(right),
+        "a tile on": right.roll(16, dims=1),
+        "another adapter": adapters(x, index, tensors, pick=lambda l: (l + 1) % L)[0],
+        "A x as one bf16": adapters(x, index, tensors, between=lambda v: v.bfloat16().double())[0],
+        "one column lost": adapters(lost, index, tensors)[0],
+        "a rank lost": adapters(x, index, (a, b, scaling, ranks - 1))[0],
+        "the whole rank": adapters(x, index, (a, b, scaling, torch.full_like(ranks, R)))[0],
+        "no scaling": adapters(x, index, (a, b, torch.ones_like(scaling), ranks))[0],
+        "every row has one": adapters(x, index.clamp(min=0), tensors)[0],
+    }
+    if (ranks[index.clamp(min=0).long()][index >= 0] == R).all():
+        del wrong["the whole rank"]
+    if (index >= 0).all():
+        del wrong["every row has one"]
     for name, bad in wrong.items():
         assert refused(bad.to(torch.bfloat16), ref, err) is not None, name
