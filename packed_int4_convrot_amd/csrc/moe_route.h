@@ -10,6 +10,8 @@
 // of 60, k = 4, and the same 4.5 us in front of the experts at k = 8.)
 #pragma once
 
+#include <type_traits>
+
 #include "rows_device.h"
 
 namespace ck {
@@ -113,6 +115,23 @@ __device__ __forceinline__ float route_weight(const Routed<kNe> &r, bool renorma
     }
     den = wave_sum(den);
     return den > 0.f ? e / den : 0.f;
+}
+
+// Calls f with the logits a lane holds for E experts.  One rule for the router and for
+// the layer that routes its own tokens: the weights' sums run in an order that depends
+// on it, and a token's weights should not depend on which of the two chose them.  (The
+// fewest that fit: one token of a layer of H 2048, I 768, k 8 takes 15.4, 15.4 and 15.7 us
+// with 32, 64 and 128 experts, against 17.1, 16.9 and 17.0 us with four logits a lane.)
+template <class F>
+auto with_lane_logits(int E, F &&f)
+{
+    if (E <= 64)
+        return f(std::integral_constant<int, 1>());
+    if (E <= 128)
+        return f(std::integral_constant<int, 2>());
+    if (E <= 256)
+        return f(std::integral_constant<int, 4>());
+    return f(std::integral_constant<int, 16>());
 }
 
 }  // namespace ck

@@ -35,17 +35,10 @@ void launch_kind(const void *logits, int64_t T, int E, int64_t ldl, int k, bool 
                  float *weights, hipStream_t s)
 {
     const dim3 grid((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock)), block(kTokensPerBlock * kWave);
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, s, logits, T, E, ldl, k, renormalize, ids, weights);
-    };
-    if (E <= 64)
-        go(moe_route_kernel<1, kBf16>);
-    else if (E <= 128)
-        go(moe_route_kernel<2, kBf16>);
-    else if (E <= 256)
-        go(moe_route_kernel<4, kBf16>);
-    else
-        go(moe_route_kernel<16, kBf16>);
+    with_lane_logits(E, [&](auto ne) {
+        hipLaunchKernelGGL((moe_route_kernel<decltype(ne)::value, kBf16>), grid, block, 0, s, logits, T, E, ldl, k,
+                           renormalize, ids, weights);
+    });
 }
 
 }  // namespace

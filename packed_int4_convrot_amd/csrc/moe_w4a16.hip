@@ -628,9 +628,9 @@ hipError_t launch_up(const UpArgs &a, bool few, int blocks, hipStream_t s)
     }
     if (!a.r.logits)
         return launch_up_few<0, false>(a, s);
-    if (a.E <= 256)
-        return a.r.bf16 ? launch_up_few<4, true>(a, s) : launch_up_few<4, false>(a, s);
-    return a.r.bf16 ? launch_up_few<16, true>(a, s) : launch_up_few<16, false>(a, s);
+    return with_lane_logits(a.E, [&](auto ne) {
+        return a.r.bf16 ? launch_up_few<decltype(ne)::value, true>(a, s) : launch_up_few<decltype(ne)::value, false>(a, s);
+    });
 }
 
 }  // namespace
