@@ -369,9 +369,10 @@ size_t ck_moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int32_t k);
  *   ws      device workspace of at least ck_moe_workspace_bytes(T, I, E, k)
  *           bytes, 256-byte aligned (CK_ERR_WORKSPACE otherwise); scratch
  * H % 64 == 0, I % 64 == 0 (CK_ERR_INVALID_ARG); H, I <= 32768, E <= 1024,
- * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0; every pass of up to 1024 / k
- * tokens reads its experts' weights anew.  A non-finite x or h reaches only its own token's
- * row.
+ * k <= 32, Gw == 64 (CK_ERR_UNSUPPORTED).  Any T >= 0.  Up to 16 (token, slot) pairs
+ * with I <= 1536 take two launches; more, or wider, take passes of up to 1024 / k tokens
+ * of four launches (three with given ids), each of which reads its experts' weights anew.
+ * A non-finite x or h reaches only its own token's row.
  * Range: the sums run over codes offset by 128 and are corrected by x's sum, as in
  * ck_w4a16_gemv.  They stay finite for |x| and |h| up to 1e34 / max(1, S), S the sum of
  * |s| + |z| over a weight row's groups; beyond that, and where x, h, a scale or a zero

@@ -427,7 +427,7 @@ struct DownArgs {
 
 constexpr int kFewWaves = 8, kFewDepth = 3;
 __host__ __device__ constexpr int few_half(int groups) { return stage_groups((groups + 1) / 2); }
-int few_down_lds(int P, int G)
+constexpr int few_down_lds(int P, int G)
 {
     return kFewWaves * (kFewDepth * kStageBytes + few_half(G) * (512 + 16)) + (P > kFewWaves ? P : kFewWaves) * 64;
 }
@@ -646,8 +646,8 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
     uint16_t *hidden = static_cast<uint16_t *>(ws);
     float *y = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + moe_hidden_bytes(P, w.I));
 
-    const int few_lds = few_down_lds(P < kMoeFewPairs ? P : kMoeFewPairs, w.I / 64);
-    const bool few = P <= kMoeFewPairs && few_lds <= kMaxLds - 1024;
+    static_assert(few_down_lds(kMoeFewPairs, kMoeFewInner / 64) <= kMaxLds - 1024, "LDS");
+    const bool few = P <= kMoeFewPairs && w.I <= kMoeFewInner;
     if (r.logits && !few) {
         const int e = launch_moe_route(r.logits, r.bf16, T, w.E, r.ldl, r.k, r.renormalize, r.ids, r.weights, stream);
         if (e != 0)
@@ -666,7 +666,8 @@ int launch_moe(const uint16_t *x, int T, int64_t ldx, const MoeRouting &r, const
         e = allow_lds<moe_down_few_kernel, kMaxLds - 1024>();
         if (e != hipSuccess)
             return (int)e;
-        hipLaunchKernelGGL(moe_down_few_kernel, dim3(w.H / 16), dim3(kFewWaves * kWave), few_lds, s, da);
+        hipLaunchKernelGGL(moe_down_few_kernel, dim3(w.H / 16), dim3(kFewWaves * kWave), few_down_lds(P, w.I / 64), s,
+                           da);
     } else {
         e = allow_lds<moe_down_kernel>();
         if (e != hipSuccess)

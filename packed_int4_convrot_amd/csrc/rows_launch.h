@@ -26,6 +26,10 @@ constexpr int kMoePairs = 1024;
 // that share them; 16 pairs 48 against 53; 24 pairs 63 against 65, and repeated
 // experts are read again for each).
 constexpr int kMoeFewPairs = 16;
+// Inner width up to which they do: the second of the two launches has a ring of three
+// stages and the hidden activations of each of its eight waves in LDS (H 3840, 8 of 64
+// experts, one token: I 1536 30 us, against 41 us for the four launches; I 1600 43 us).
+constexpr int kMoeFewInner = 1536;
 inline int64_t moe_hidden_bytes(int64_t P, int64_t I) { return (P * I * 4 + 255) / 256 * 256; }
 inline int64_t moe_pass_columns(int64_t P) { return P * 8192; }
 
@@ -71,7 +75,12 @@ inline int64_t lora_most_splits(int64_t K) { return K / 256 < 1 ? 1 : K / 256 < 
 // Parts the K columns are split into, so that few rows still fill the chip: about
 // one workgroup for each of the 256 CUs; a wave keeps a 64-column group at least,
 // and the second product adds at most 8 parts.  Of the tiles that a window's sets
-// can have, several requests' rows over few adapters use about six.
+// can have, rows of few adapters use some: six are counted.  Over 66 sizes (70 to 1000
+// rows of 6 to 15 adapters, in runs and mixed, ranks 16 to 64) counting four or five
+// takes 3 or 2 % less time on average, but up to 13 or 9 % more for mixed rows (400 rows
+// of 10, K 10240: 34.4 and 33.0 us against 30.5); counting two as much on average and up
+// to 26 % more, and ten 3 % more on average and up to 54 % (1000 rows of 15 in runs,
+// K 10240: 83.6 against 54.4).
 inline int lora_splits(int64_t M, int64_t K, int64_t R, int64_t L)
 {
     const int64_t slots = M > kLoraFewRows ? 1 : lora_slots(M, L);
