@@ -349,7 +349,7 @@ __global__ __launch_bounds__(kWaves * kWave, kSlots ? 1 : 2) void lora_expand_ke
     const int vpitch = (R + 15) / 16 * 64 + 16;  // bytes of a row of v in LDS
     int mine = window_adapter(index, M, L, row0, kLoraWindow);
     // Rows without an adapter join the window's first set, so that they cost no
-    // pass of their own; -0 is added to their base.
+    // pass of their own; their base is stored as it is.
     const uint64_t without = __ballot(mine == -1), with = __ballot(mine >= 0);
     if (with) {
         const int first = __builtin_amdgcn_readlane(mine, __builtin_ctzll(with));
@@ -515,11 +515,9 @@ __global__ __launch_bounds__(kWaves * kWave, kSlots ? 1 : 2) void lora_expand_ke
                     for (int i = 0; i < 2; ++i) {
                         const int p = p0 + 8 * i + lane / 8;
                         const uint8_t *from = sums + (8 * i + lane / 8) * kPitch + lane % 8 * 32;
-                        v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
+                        const v4f t0 = *reinterpret_cast<const v4f *>(from), t1 = *reinterpret_cast<const v4f *>(from + 16);
                         if (p < last && n < N) {
                             const int row = s_rows[p];
-                            if (row >= 64)
-                                t0 = t1 = v4f{-0.f, -0.f, -0.f, -0.f};
                             const u32x4 y = bv[tile][i];
                             u32x4 o;
 #pragma unroll
@@ -527,6 +525,7 @@ __global__ __launch_bounds__(kWaves * kWave, kSlots ? 1 : 2) void lora_expand_ke
                                 const v4f &t = q < 2 ? t0 : t1;
                                 o[q] = pack_bf16x2(t[2 * q % 4] + bf16_to_f32(y[q] & 0xffffu),
                                                    t[2 * q % 4 + 1] + __uint_as_float(y[q] & 0xffff0000u));
+                                o[q] = row < 64 ? o[q] : y[q];
                             }
                             *reinterpret_cast<u32x4 *>(out + (row0 + row % 64) * ldo + n) = o;
                         }
