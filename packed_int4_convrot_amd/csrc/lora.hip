@@ -609,7 +609,7 @@ int launch_lora(const uint16_t *x, int64_t M, int K, int64_t ldx, const int32_t 
     const ExpandArgs ea{ws, parts, M, index, L, slots, R, b, scaling, ranks, N, base, ldb, out, ldo};
     if (!few)
         e = launch_expand_steps<false, 4, 2>(ea, s);
-    else if (lora_expand_waves(M, L) == 1)
+    else if (lora_expand_waves(M, L, R, N) == 1)
         e = launch_expand_steps<true, 1, 1>(ea, s);
     else
         e = launch_expand_steps<true, 4, 1>(ea, s);

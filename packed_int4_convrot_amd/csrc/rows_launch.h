@@ -99,15 +99,19 @@ inline int64_t lora_room_rows(int64_t M, int64_t K)
     return M > most ? M : split < most ? split : most;
 }
 // Waves of a workgroup of the second product, up to kLoraFewRows rows.  A wave brings
-// four rows of v to LDS at a time, so tiles with more rows take four waves, which share
-// that work; tiles of one or two rows take one, whose workgroups spread over the chip
-// (K = 3840, N = 3840 of rank 64, one against four: 1 row 10.8 against 12.2 us; 16 rows
-// of one adapter 16.0 against 12.7; 32 rows of 32 15.5 against 16.4, of 4 15.2 against
-// 13.1; 301 of 7 22.7 against 18.7; 512 rows of 64 123 against 133.  Of rank 16 one wave
-// loses 2 % with many tiles of one row: 512 of 64 58.8 against 57.6).
-inline int lora_expand_waves(int64_t M, int64_t L)
+// four rows of v to LDS at a time, so tiles of more rows take four waves, which share
+// that work (K = N = 3840, one wave against four: 16 rows of one adapter of rank 16
+// 14.0 against 9.3 us; 32 rows of 4 of rank 64 15.2 against 13.1; 301 of 7 22.7 against
+// 18.7).  Tiles of one or two rows take one wave, whose workgroups spread over the chip
+// (1 row of rank 16 8.0 against 8.4 us, of rank 64 10.8 against 12.2; 512 rows of 64
+// adapters of rank 64 123 against 133), unless the chip is full anyway and the ranks are
+// few (32 rows of 32 with N 10240, rank 16 13.6 against 13.1; 1000 rows of 300, rank 32
+// 175 against 171, rank 48 246 against 247).
+inline int lora_expand_waves(int64_t M, int64_t L, int64_t R, int64_t N)
 {
-    return M <= 4 || M <= 2 * lora_ceil(M, kLoraWindow) * lora_slots(M, L) ? 1 : 4;
+    const int64_t tiles = lora_ceil(M, kLoraWindow) * lora_slots(M, L);
+    const bool spread = R > 32 || tiles * lora_ceil(N, 256) <= kLoraCus;
+    return (M <= 4 || M <= 2 * tiles) && spread ? 1 : 4;
 }
 // Workgroups of 256 threads of the second product; a launch takes fewer than 2^24.
 inline int64_t lora_blocks(int64_t M, int64_t N, int64_t L)

@@ -120,10 +120,10 @@ def layer_inputs(T, H, I, E, k, crowded, device="cpu"):
 
 # M, K, N, R, L: each form of the second product (one wave and four a workgroup, many rows)
 # at 16, 32, 64 ranks and beyond.
-ADAPTERS = [(1, 3840, 512, 16, 3), (32, 3840, 1024, 16, 32), (40, 256, 272, 24, 5), (301, 1024, 528, 40, 7),
-            (100, 320, 144, 136, 3), (200, 192, 272, 16, 3), (300, 192, 1040, 16, 40), (300, 192, 1040, 24, 40),
-            (300, 192, 1040, 64, 40), (300, 128, 1040, 200, 40), (1030, 3840, 80, 16, 4), (1025, 192, 528, 24, 3),
-            (1300, 1024, 528, 64, 8), (1100, 640, 272, 136, 30)]
+ADAPTERS = [(1, 3840, 512, 16, 3), (16, 192, 272, 24, 16), (32, 3840, 1024, 16, 32), (40, 256, 272, 24, 5),
+            (301, 1024, 528, 40, 7), (100, 320, 144, 136, 3), (200, 192, 272, 16, 3), (300, 192, 1040, 16, 40),
+            (300, 192, 1040, 24, 40), (300, 192, 1040, 64, 40), (300, 128, 1040, 200, 40), (1030, 3840, 80, 16, 4),
+            (1025, 192, 528, 24, 3), (1300, 1024, 528, 64, 8), (1100, 640, 272, 136, 30)]
 
 
 def adapter_inputs(M, K, N, R, L, device="cpu"):
