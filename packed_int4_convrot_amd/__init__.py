@@ -445,19 +445,27 @@ def accumulators_i32(codes, packed):
 _LOGIT_KIND = {torch.float32: CK_LOGITS_F32, torch.bfloat16: CK_LOGITS_BF16}
 
 
+# What is not a tensor shows by the attributes it lacks: isinstance() for each argument would
+# cost every call.
+
 def _row_count(t, name):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError("%s must be a 2-D tensor" % name)
-    return t.shape[0]
+    """Rows of a 2-D tensor."""
+    try:
+        rows, _ = t.shape
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError("%s must be a 2-D tensor" % name) from None
+    return rows
 
 
 def _rows(t, name, dtype, device, shape):
     """Row stride of a matrix of exactly this shape, dtype and device with unit column stride."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError("%s must be a tensor" % name)
-    if t.dtype is not dtype or t.device != device or t.shape != shape:
-        raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)"
-                         % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+    try:
+        fits = t.dtype is dtype and t.device == device and t.shape == shape
+        if not fits:
+            raise ValueError("%s must be a %s tensor of shape %s on %s (got %s %s on %s)"
+                             % (name, dtype, shape, device, t.dtype, tuple(t.shape), t.device))
+    except AttributeError:
+        raise ValueError("%s must be a tensor" % name) from None
     ld, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError("%s must have unit column stride" % name)
@@ -471,16 +479,18 @@ def _rows(t, name, dtype, device, shape):
 
 def _flat(t, name, dtype, device, shape):
     """Pointer of a contiguous tensor of exactly this shape, dtype and device."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
-            or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
 
 
 def _logits(logits):
     """(kind, row stride) of a [T, E] GPU matrix of router logits."""
     _row_count(logits, "logits")
-    kind = _LOGIT_KIND.get(logits.dtype)
+    kind = _LOGIT_KIND.get(getattr(logits, "dtype", None))
     if kind is None or not logits.is_cuda:
         raise ValueError("logits must be a 2-D fp32 or bf16 GPU tensor")
     return kind, _rows(logits, "logits", logits.dtype, logits.device, logits.shape)
@@ -490,10 +500,13 @@ def _space(workspace, need, device):
     """A workspace tensor of at least `need` bytes."""
     if workspace is None:
         return torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.dim() != 1 \
-            or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError("workspace must be a contiguous 1-D uint8 tensor on %s" % device)
-    return workspace
+    try:
+        if workspace.dtype is torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous() \
+                and workspace.device == device:
+            return workspace
+    except AttributeError:
+        pass
+    raise ValueError("workspace must be a contiguous 1-D uint8 tensor on %s" % device)
 
 
 def _slots(ids, weights, T, k, device):
@@ -523,13 +536,16 @@ def moe_workspace_bytes(T: int, I: int, E: int, k: int) -> int:
     return int(lib.ck_moe_workspace_bytes(T, I, E, k))
 
 
-def _addresses(tensors, name):
-    """Their addresses as of now (None for a tensor that was not given).  Read for each call:
-    an address of last time may be freed memory."""
-    at = [None if t is None else t.data_ptr() for t in tensors]
-    if 0 in at:
-        raise ValueError("%s: a tensor has no storage any more" % name)
-    return at
+def _absent():
+    """The address of a tensor that was not given."""
+    return None
+
+
+def _held(tensors):
+    """The tensors' storages, and a function of each that tells its address (read for each
+    call: an address of last time may be freed memory)."""
+    held = tuple(None if t is None else t.detach() for t in tensors)
+    return held, tuple(_absent if t is None else t.data_ptr for t in held)
 
 
 class MoeExperts:
@@ -555,11 +571,15 @@ class MoeExperts:
                 continue
             _dense(t, name, torch.bfloat16, shape)
         _same_device(w1, ("s1", s1), ("z1", z1), ("w2", w2), ("s2", s2), ("z2", z2))
-        self.tensors = tuple(None if t is None else t.detach() for t in (w1, s1, z1, w2, s2, z2))
+        self.tensors, self._at = _held((w1, s1, z1, w2, s2, z2))
         self.E, self.H, self.I, self.device = E, H, I, w1.device
 
     def _args(self):
-        return (self.E, self.I, 64, *_addresses(self.tensors, "experts"))
+        w1, s1, z1, w2, s2, z2 = self._at
+        at = (self.E, self.I, 64, w1(), s1(), z1(), w2(), s2(), z2())
+        if 0 in at:
+            raise ValueError("experts: none, or a tensor has no storage any more")
+        return at
 
 
 def _moe_buffers(x, experts, k, out, workspace):
@@ -619,11 +639,15 @@ class LoraAdapters:
         if ranks is not None:
             _dense(ranks, "ranks", torch.int32, (L,))
         _same_device(a, ("b", b), ("scaling", scaling), ("ranks", ranks))
-        self.tensors = tuple(None if t is None else t.detach() for t in (a, b, scaling, ranks))
+        self.tensors, self._at = _held((a, b, scaling, ranks))
         self.L, self.R, self.K, self.N, self.device = L, R, K, N, a.device
 
     def _args(self):
-        return (self.L, self.R, *_addresses(self.tensors, "adapters"), self.N)
+        a, b, scaling, ranks = self._at
+        at = (self.L, self.R, a(), b(), scaling(), ranks(), self.N)
+        if 0 in at:
+            raise ValueError("adapters: no slots, or a tensor has no storage any more")
+        return at
 
 
 def lora_workspace_bytes(M: int, K: int, R: int, L: int) -> int:
