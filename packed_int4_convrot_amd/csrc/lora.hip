@@ -10,10 +10,14 @@
 // by side; many rows (prompts, where neighbours share an adapter): a workgroup
 // goes through the sets of its window.
 // The work is bound by memory: x, base and out once, the used adapters once; few
-// rows by the two kernels' latency (one row, K = N = 3840, rank 16: 4.0 + 4.9 us).
-// Measured: 32 rows of as many adapters, N 10240, rank 16: 5.2 + 7.0 us (6 MB);
-// 301 rows of 7, K 10240, N 3840, rank 40: 13 + 8 us (15 MB); 8192 rows of 8 in
-// runs, K 3840, N 10240, rank 64: 37 + 115 us (63 MB of x, 336 MB of base and out).
+// rows by the two kernels' latency (one row, K = N = 3840, rank 16: 4.0 + 5.2 us).
+// Measured (durations in a kernel trace): 32 rows of as many adapters, N 10240, rank 16:
+// 5.2 + 6.9 us (8 MB); 301 rows of 7, K 10240, N 3840, rank 40: 13 + 8 us (16 MB); 8192
+// rows of 8 in runs, K 3840, N 10240, rank 64: 37 + 112 us (63 MB of x, 336 MB of base and
+// out; the waves of the second wait 61 % of their time, and it reads 227 MB from beyond
+// the L2s where base, v and B are 183).
+// A x goes to the second product as two bf16 (16 significant bits), because one would add as
+// much error as the result's own rounding.
 #include <type_traits>
 
 #include "rows_device.h"
@@ -324,10 +328,10 @@ __device__ __forceinline__ u32x4 mask_ranks(u32x4 w, int r, int rank)
 // 16 first parts, then 16 second parts, the 32 columns of k of one MFMA, whose
 // other operand is B_a's 16 ranks twice.  A wave then owns kCols tiles of 64 columns; the
 // sums of 16 rows go through LDS so that base and out are moved in 128-byte
-// runs of a row (8192 rows of rank 64: 250 us without, 132 with).  Four tiles of
-// base are on their way at a time (three: 123 us against 115); asking for the first of
+// runs of a row (8192 rows of rank 64: 250 us without, 132 with, in earlier forms).  Four tiles of
+// base are on their way at a time (three: 123 us against 115 then); asking for the first of
 // them ahead of v gains nothing (116).  Two waves a SIMD fit beside B_a's operands,
-// so latency shows: 2.9 TB/s of base and out, where a copy reaches 5.4.
+// so latency shows: 3.0 TB/s of base and out, where a copy reaches 5.4.
 template <bool kSlots, int kWaves, int kCols, int kSteps, bool kWide>
 __global__ __launch_bounds__(kWaves * kWave, kSlots ? 1 : 2) void lora_expand_kernel(
     const float *__restrict__ v, int parts, int64_t M, const int32_t *__restrict__ index, int64_t L, int slots, int R,

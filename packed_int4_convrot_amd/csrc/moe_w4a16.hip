@@ -6,7 +6,9 @@
 //
 // Few tokens make this a matter of streaming the chosen experts' weights once
 // (w4_stream.h), whatever the number of tokens each has.  Sums are fp32; h goes
-// to the second product as two bf16 (16 significant bits), as two rows of A.
+// to the second product as two bf16 (16 significant bits), as two rows of A: one bf16
+// would add as much error as the result's own rounding, and a third part (24 bits) a
+// third row of A for what lies 2^8 below that rounding.
 //
 // Launches, for P = tokens * k (token, slot) pairs:
 //   few pairs:  first product (each workgroup routes its token itself), second
@@ -15,10 +17,12 @@
 //               workgroup collects its expert's pairs from the ids with ballots.
 //
 // Measured (H 3840, I 1280, zero points, cold weights), of about 6.1 TB/s that bare
-// reads reach here: one token of 8 experts 26 us (first product 44 MB in 14 us,
-// second 22 MB in 12 us); 64 tokens of 8 in 128 experts 270-285 us (697 MB in
-// 164-173 us, 348 MB in 95-102 us); 8 tokens in 64 experts, no zero points, 105 us
-// (219 MB in 60, 110 MB in 36).
+// reads reach here; a call, and its products' durations in a kernel trace, which keeps
+// the kernels of a call apart (their sum is up to a tenth more than the call): one token
+// of 8 experts 25 us (first product 44 MB in 14 us, second 22 MB in 12); 64 tokens of 8
+// in 128 experts 232-251 us (697 MB in 161-168, 348 MB in 91-97); 8 tokens in 64 experts,
+// no zero points, 96 us (219 MB in 58, 110 MB in 35).  1.00 to 1.05 times those bytes
+// come from beyond the L2s; the waves wait 37 to 48 % of their time.
 #include "moe_route.h"
 #include "rows_launch.h"
 #include "w4_stream.h"
@@ -148,10 +152,10 @@ __global__ __launch_bounds__(kFewUpWaves * kWave) void moe_up_few_kernel(const U
 // has many pairs or because the chosen experts do not divide the chip; S is
 // the one whose runs are shortest.  A workgroup finds its run from the ids itself
 // (1.6 us; a launch of its own takes 4.5); a wave's weights are one stream through
-// all its tiles.  Of the first product of 8 tokens, a workgroup has its activations
-// in LDS 8 us after the start and streams until 50 us (median) to 62 us (those with a
-// unit more).  Dividing only the last, partial turn of units into slices evens the
-// ends out, but measured no faster (64 tokens: 165 + 103 against 164-173 + 95-102 us):
+// all its tiles.  In a build with time stamps a workgroup of the first product of 8 tokens
+// has its activations in LDS 8 us after the start and streams until 50 us (median) to
+// 62 us (those with a unit more).  Dividing only the last, partial turn of units into slices evens the
+// ends out, but measured no faster (64 tokens: 165 + 103 against 161-173 + 91-102 us):
 // the workgroups that are left have the memory to themselves.
 constexpr int kWaves = 8, kSetPairs = 8, kMaxSets = 8;
 

@@ -58,9 +58,10 @@ constexpr int kLoraWindow = 64;     // rows that share one look at the adapter i
 constexpr int kLoraMaxRank = 256;
 constexpr int kLoraRankBlock = 64;
 // Rows up to which a workgroup is started for every tile a window can have (K = N =
-// 3840, rank 64, 6 adapters in runs: 1024 rows 32 us, against 43 us of whole windows;
-// 2048 rows 71 against 46.  Mixed rows would gain beyond, 91 against 121 us at 2048
-// rows of 8 adapters, but batches that large are prompts, whose rows come in runs).
+// 3840, rank 64, 6 adapters in runs: 1024 rows 40 us, against 42 us of whole windows; 1500
+// rows 47 against 43, 2048 54 against 46; rank 16 with N 10240 27 against 43, 37 against 44,
+// 46 against 50).  Mixed rows would gain beyond, 90 against 120 us at 2048 rows of 8
+// adapters, but batches that large are prompts, whose rows come in runs.
 constexpr int64_t kLoraFewRows = 1024;
 inline int64_t lora_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tiles of 16 rows that the sets of a window can have, a set being the rows of one
