@@ -428,6 +428,97 @@ ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, cons
                       int64_t N, const uint16_t *base, int64_t ldb, uint16_t *out, int64_t ldo, void *ws,
                       size_t ws_bytes, void *stream);
 
+/*
+ * ------------------------------------------------------- 8-bit float products
+ * Linears and a gated feed-forward block on e4m3 codes (OCP, as the gfx950 matrix cores
+ * take them) with power-of-two scales, one for each block of 128.  A scale is an e8m0
+ * byte e, worth 2^(e - 127): the matrix cores apply it, so that a scale costs nothing
+ * and scaling never rounds.  Conventions as above, but for the shapes: K (and H) a
+ * multiple of 16 up to 32768, a last block of fewer than 128 columns counting as one.
+ *
+ * Activations: codes uint8 [M, ldq] (ldq % 16 == 0, 16-byte aligned) and scales
+ *   uint8 [M, lds], one for each row and 128 columns; 4-byte aligned, lds % 4 == 0,
+ *   and the bytes of a row up to the next multiple of four belong to it (read, not used).
+ * Weights: codes uint8 [N, ldw] (16-byte aligned, ldw % 16 == 0) and scales
+ *   uint8 [ceil(N / 128), ceil(K / 128)], dense, one for each 128 x 128 block;
+ *   N a multiple of 16.
+ *
+ * Quantised, a block of largest absolute value a has the smallest scale s >= 2^-127
+ * with a <= 448 s (1 for a block of zeros), and a code is e4m3(x / s), nearest even,
+ * ties to even: x / s is exact, so this is the only rounding.  A block that holds a
+ * NaN or an infinity gives NaN in every result of its row (of its columns, in a weight).
+ * Sums are fp32, rounded once to the result's type.  Range: products whose scales add up
+ * beyond fp32's exponents overflow or vanish as fp32 does.
+ */
+
+/* ck_fp8_quant: codes and scales of bf16 x [M, ldx], K columns. */
+ck_status ck_fp8_quant(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *codes, int64_t ldq,
+                       uint8_t *scales, int64_t lds, void *stream);
+
+/* ck_fp8_quantize_weights: codes and scales (128 x 128 blocks) of a bf16 weight [N, ldw_in]. */
+ck_status ck_fp8_quantize_weights(const uint16_t *w, int64_t N, int64_t K, int64_t ldw_in, uint8_t *codes,
+                                  int64_t ldw, uint8_t *scales, void *stream);
+
+/* ck_fp8_transpose_weights: the weight's transpose, codes_t [K, ldt] and scales_t
+ * [ceil(K / 128), ceil(N / 128)], for the products of the backward passes (exact: square
+ * blocks keep their scales).  Must not overlap the weight. */
+ck_status ck_fp8_transpose_weights(const uint8_t *codes, int64_t ldw, const uint8_t *scales, int64_t N, int64_t K,
+                                   uint8_t *codes_t, int64_t ldt, uint8_t *scales_t, void *stream);
+
+/*
+ * ck_fp8_gemm
+ *   out[m, n] = sum_b 2^(sa[m, b] + sw[n / 128, b] - 254) sum_{k in b} a[m, k] w[n, k] (+ bias[n])
+ * for activations that are already quantised, bias bf16 [N] or NULL, out bf16 [M, ldo].
+ * The backward pass of the linear, to its input, is the linear of the transposed weight.
+ */
+ck_status ck_fp8_gemm(const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds, int64_t M, int64_t K,
+                      const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t N, const uint16_t *bias,
+                      uint16_t *out, int64_t ldo, void *stream);
+
+/* Bytes of workspace ck_fp8_linear needs: codes and scales of M rows of K columns.  A
+ * workspace of some M, K and N serves every call with no more of each.  0 for sizes it refuses. */
+size_t ck_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* ck_fp8_linear: ck_fp8_quant into the workspace, then ck_fp8_gemm (x bf16 [M, ldx]). */
+ck_status ck_fp8_linear(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint8_t *w, int64_t ldw,
+                        const uint8_t *w_scales, int64_t N, const uint16_t *bias, uint16_t *out, int64_t ldo,
+                        void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace ck_fp8_ffn and ck_fp8_ffn_backward need; as above. */
+size_t ck_fp8_ffn_workspace_bytes(int64_t M, int64_t H, int64_t I);
+size_t ck_fp8_ffn_backward_workspace_bytes(int64_t M, int64_t H, int64_t I);
+
+/*
+ * ck_fp8_ffn
+ * Gated feed-forward block, x bf16 [M, ldx] with H columns, Q the quantiser above:
+ *   g = W1[0:I] Q(x),  u = W1[I:2I] Q(x),  h = silu(g) u (fp32),  out = W2 Q(h)
+ *   w1   codes [2I, H] (I gate rows, then I up rows), s1 [2I / 128, ceil(H / 128)]
+ *   w2   codes [H, I], s2 [ceil(H / 128), I / 128]; all dense
+ *   out  bf16 [M, ldo], H columns
+ *   gate_up  bf16 [M, ldg], 2 I columns (g, then u, each rounded once), or NULL: what
+ *        the backward pass needs (ldg % 8 == 0, 16-byte aligned)
+ * I % 128 == 0 (CK_ERR_INVALID_ARG), I <= 32768.
+ */
+ck_status ck_fp8_ffn(const uint16_t *x, int64_t M, int64_t H, int64_t ldx, int64_t I, const uint8_t *w1,
+                     const uint8_t *s1, const uint8_t *w2, const uint8_t *s2, uint16_t *out, int64_t ldo,
+                     uint16_t *gate_up, int64_t ldg, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ck_fp8_ffn_backward
+ * The gradient of ck_fp8_ffn's input from its output's, dy bf16 [M, ldy] with H columns,
+ * and the gate_up that the forward pass kept.  The weights are frozen, quantisers are
+ * passed straight through:
+ *   dh = W2^T Q(dy),  dg = dh u s (1 + g (1 - s)),  du = dh g s,  s = 1 / (1 + exp(-g)),
+ *   dx = W1[0:I]^T Q(dg) + W1[I:2I]^T Q(du)
+ *   w1t  codes [H, 2I], s1t [ceil(H / 128), 2I / 128];  w2t codes [I, H], s2t
+ *        [I / 128, ceil(H / 128)]: the transposed weights, dense
+ *   dx   bf16 [M, lddx], H columns
+ */
+ck_status ck_fp8_ffn_backward(const uint16_t *dy, int64_t M, int64_t H, int64_t ldy, const uint16_t *gate_up,
+                              int64_t ldg, int64_t I, const uint8_t *w1t, const uint8_t *s1t, const uint8_t *w2t,
+                              const uint8_t *s2t, uint16_t *dx, int64_t lddx, void *ws, size_t ws_bytes,
+                              void *stream);
+
 /* ---------------------------------------------------------------- test hooks
  * Same device code paths as above with a debug epilogue, so that each stage
  * can be compared exactly with the oracle. */

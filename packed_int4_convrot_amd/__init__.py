@@ -63,6 +63,17 @@ SIGNATURES = {
                       _p, _i64, _p, _p, _p, _sz, _p], ctypes.c_int),
     "ck_moe_experts_w4a16": ([_p, _i64, _i64, _i64, _p, _p, _i32, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p, _p, _i64,
                               _p, _sz, _p], ctypes.c_int),
+    "ck_fp8_quant": ([_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p], ctypes.c_int),
+    "ck_fp8_quantize_weights": ([_p, _i64, _i64, _i64, _p, _i64, _p, _p], ctypes.c_int),
+    "ck_fp8_transpose_weights": ([_p, _i64, _p, _i64, _i64, _p, _i64, _p, _p], ctypes.c_int),
+    "ck_fp8_gemm": ([_p, _i64, _p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p], ctypes.c_int),
+    "ck_fp8_linear_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "ck_fp8_linear": ([_p, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p, _sz, _p], ctypes.c_int),
+    "ck_fp8_ffn_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "ck_fp8_ffn_backward_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "ck_fp8_ffn": ([_p, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _sz, _p], ctypes.c_int),
+    "ck_fp8_ffn_backward": ([_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _p, _sz, _p],
+                            ctypes.c_int),
     "ck_lora_workspace_bytes": ([_i64, _i64, _i64, _i64], _sz),
     "ck_lora_add": ([_p, _i64, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _sz, _p],
                     ctypes.c_int),
@@ -670,3 +681,229 @@ def lora_add(x, adapters: LoraAdapters, index, base=None, out=None, workspace=No
                            *adapters._args(), None if base is None else base.data_ptr(), ldb, out.data_ptr(), ldo,
                            workspace.data_ptr(), workspace.numel(), _stream(x)))
     return out
+
+
+# ------------------------------------------------------ 8-bit float products
+# e4m3 codes with power-of-two (e8m0) scales for each block of 128.  As above, the weights
+# are checked once, when their handle is made.
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def fp8_blocks(n: int) -> int:
+    """Blocks of 128 in n columns or rows."""
+    return -(-n // 128)
+
+
+def fp8_empty(M: int, K: int, device):
+    """Room for quantised activations: codes e4m3 [M, K] and scales e8m0 [M, ceil(K / 128)], whose
+    rows lie a multiple of four bytes apart, as the products read them."""
+    blocks = fp8_blocks(K)
+    return (torch.empty((M, K), dtype=E4M3, device=device),
+            torch.empty((M, -(-blocks // 4) * 4), dtype=E8M0, device=device)[:, :blocks])
+
+
+def _fp8_scales(t, M, K, device):
+    """Row stride of an activation's scales."""
+    lds = _rows(t, "scales", E8M0, device, (M, fp8_blocks(K)))
+    if M <= 1:
+        lds = -(-lds // 4) * 4
+    return lds
+
+
+def fp8_quant(x, codes=None, scales=None):
+    """(codes, scales) of bf16 x [M, K]: e4m3 [M, K] and, for each row and 128 columns, the smallest
+    power of two s with |x| <= 448 s, e8m0 [M, ceil(K / 128)] (1 for zeros)."""
+    M = _row_count(x, "x")
+    K, dev = x.shape[1], x.device
+    ldx = _rows(x, "x", torch.bfloat16, dev, (M, K))
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    if codes is None or scales is None:
+        room = fp8_empty(M, K, dev)
+        codes, scales = room[0] if codes is None else codes, room[1] if scales is None else scales
+    ldq = _rows(codes, "codes", E4M3, dev, (M, K))
+    _check(lib.ck_fp8_quant(x.data_ptr(), M, K, ldx, codes.data_ptr(), ldq, scales.data_ptr(),
+                            _fp8_scales(scales, M, K, dev), _stream(x)))
+    return codes, scales
+
+
+def fp8_quantize_weights(w, codes=None, scales=None):
+    """(codes, scales) of a bf16 weight [N, K]: e4m3 [N, K] and e8m0 [ceil(N / 128), ceil(K / 128)],
+    one scale for each 128 x 128 block."""
+    N = _row_count(w, "w")
+    K, dev = w.shape[1], w.device
+    ldw = _rows(w, "w", torch.bfloat16, dev, (N, K))
+    if not w.is_cuda:
+        raise ValueError("w must be a GPU tensor")
+    shape = (fp8_blocks(N), fp8_blocks(K))
+    codes = torch.empty((N, K), dtype=E4M3, device=dev) if codes is None else codes
+    scales = torch.empty(shape, dtype=E8M0, device=dev) if scales is None else scales
+    ldc = _rows(codes, "codes", E4M3, dev, (N, K))
+    _check(lib.ck_fp8_quantize_weights(w.data_ptr(), N, K, ldw, codes.data_ptr(), ldc,
+                                       _flat(scales, "scales", E8M0, dev, shape), _stream(w)))
+    return codes, scales
+
+
+def _fp8_transpose(codes, scales):
+    N, K = codes.shape
+    codes_t = torch.empty((K, N), dtype=E4M3, device=codes.device)
+    scales_t = torch.empty((fp8_blocks(K), fp8_blocks(N)), dtype=E8M0, device=codes.device)
+    _check(lib.ck_fp8_transpose_weights(codes.data_ptr(), _ld(codes), scales.data_ptr(), N, K, codes_t.data_ptr(),
+                                        _ld(codes_t), scales_t.data_ptr(), _stream(codes)))
+    return codes_t, scales_t
+
+
+class Fp8Weights:
+    """An 8-bit float weight: codes e4m3 [N, K] (rows may be strided), scales e8m0 [ceil(N / 128),
+    ceil(K / 128)].  The tensors' storages are kept, not copied, as in MoeExperts."""
+
+    def __init__(self, codes, scales):
+        _matrix(codes, "codes", (E4M3,))
+        self.N, self.K = codes.shape
+        _dense(scales, "scales", E8M0, (fp8_blocks(self.N), fp8_blocks(self.K)))
+        _same_device(codes, ("scales", scales))
+        self.tensors, self._at = _held((codes, scales))
+        self.device, self._ldw = codes.device, _ld(codes)
+
+    def transposed(self):
+        """The transposed weight, laid out anew: the linear's backward pass to its input is the
+        linear of it."""
+        return Fp8Weights(*_fp8_transpose(*self.tensors))
+
+    def _args(self):
+        codes, scales = self._at
+        at = (codes(), self._ldw, scales(), self.N)
+        if 0 in at:
+            raise ValueError("weights: none, or a tensor has no storage any more")
+        return at
+
+
+def _fp8_result(out, name, M, N, device):
+    out = torch.empty((M, N), dtype=torch.bfloat16, device=device) if out is None else out
+    return out, _rows(out, name, torch.bfloat16, device, (M, N))
+
+
+def fp8_gemm(codes, scales, weights: Fp8Weights, bias=None, out=None):
+    """bf16 [M, N] of quantised activations (fp8_quant, fp8_empty) and a weight, plus bias bf16 [N]."""
+    M, dev = _row_count(codes, "codes"), weights.device
+    ldq = _rows(codes, "codes", E4M3, dev, (M, weights.K))
+    lds = _fp8_scales(scales, M, weights.K, dev)
+    # The last row's bytes up to the next multiple of four are read.
+    end = scales.storage_offset() + max(M - 1, 0) * lds + -(-fp8_blocks(weights.K) // 4) * 4
+    if M and end > scales.untyped_storage().nbytes():
+        raise ValueError("scales: a row of %d blocks needs room up to a multiple of four (fp8_empty)"
+                         % fp8_blocks(weights.K))
+    out, ldo = _fp8_result(out, "out", M, weights.N, dev)
+    _check(lib.ck_fp8_gemm(codes.data_ptr(), ldq, scales.data_ptr(), lds, M, weights.K, *weights._args(),
+                           None if bias is None else _flat(bias, "bias", torch.bfloat16, dev, (weights.N,)),
+                           out.data_ptr(), ldo, _stream(codes)))
+    return out
+
+
+def fp8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    """Workspace bytes of fp8_linear for M rows, K columns and N outputs."""
+    return int(lib.ck_fp8_linear_workspace_bytes(M, K, N))
+
+
+def fp8_linear(x, weights: Fp8Weights, bias=None, out=None, workspace=None):
+    """Whole linear, bf16 [M, N]: quantises bf16 x [M, K] as fp8_quant and multiplies as fp8_gemm."""
+    M, dev = _row_count(x, "x"), weights.device
+    ldx = _rows(x, "x", torch.bfloat16, dev, (M, weights.K))
+    out, ldo = _fp8_result(out, "out", M, weights.N, dev)
+    workspace = _space(workspace, lib.ck_fp8_linear_workspace_bytes(M, weights.K, weights.N)
+                       if workspace is None else 0, dev)
+    _check(lib.ck_fp8_linear(x.data_ptr(), M, weights.K, ldx, *weights._args(),
+                             None if bias is None else _flat(bias, "bias", torch.bfloat16, dev, (weights.N,)),
+                             out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), _stream(x)))
+    return out
+
+
+class _Fp8Pair:
+    """Two dense weights of a feed-forward block, whose shapes are checked."""
+
+    def _keep(self, w1, s1, w2, s2, shape1, shape2):
+        for name, w, s, (rows, columns) in (("1", w1, s1, shape1), ("2", w2, s2, shape2)):
+            _dense(w, "w" + name, E4M3, (rows, columns))
+            _dense(s, "s" + name, E8M0, (fp8_blocks(rows), fp8_blocks(columns)))
+        _same_device(w1, ("s1", s1), ("w2", w2), ("s2", s2))
+        self.tensors, self._at = _held((w1, s1, w2, s2))
+        self.device = w1.device
+
+    def _args(self):
+        at = tuple(address() for address in self._at)
+        if 0 in at:
+            raise ValueError("feed-forward weights: a tensor has no storage any more")
+        return at
+
+
+def _fp8_matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.shape[0] or not t.shape[1]:
+        raise ValueError("%s must be a 2-D tensor" % name)
+    return t.shape
+
+
+class Fp8Ffn(_Fp8Pair):
+    """The weights of a gated feed-forward block: w1 e4m3 [2I, H] (I gate rows, then I up rows),
+    w2 e4m3 [H, I], their e8m0 scales of 128 x 128 blocks; I a multiple of 128.  The tensors'
+    storages are kept, not copied, as in MoeExperts."""
+
+    def __init__(self, w1, s1, w2, s2):
+        rows, self.H = _fp8_matrix(w1, "w1")
+        self.I = rows // 2
+        if rows % 256:
+            raise ValueError("w1 has %d rows: expected 2I, I a multiple of 128" % rows)
+        self._keep(w1, s1, w2, s2, (rows, self.H), (self.H, self.I))
+
+    def transposed(self):
+        """The transposed weights, laid out anew, which fp8_ffn_backward takes."""
+        w1, s1, w2, s2 = self.tensors
+        return Fp8FfnTransposed(*_fp8_transpose(w1, s1), *_fp8_transpose(w2, s2))
+
+
+class Fp8FfnTransposed(_Fp8Pair):
+    """The transposed weights of an Fp8Ffn: w1t e4m3 [H, 2I], w2t e4m3 [I, H] and their scales."""
+
+    def __init__(self, w1t, s1t, w2t, s2t):
+        self.I, self.H = _fp8_matrix(w2t, "w2t")
+        if self.I % 128:
+            raise ValueError("w2t has %d rows: expected a multiple of 128" % self.I)
+        self._keep(w1t, s1t, w2t, s2t, (self.H, 2 * self.I), (self.I, self.H))
+
+
+def fp8_ffn_workspace_bytes(M: int, H: int, I: int) -> int:
+    """Workspace bytes of fp8_ffn for M rows, H columns and inner width I."""
+    return int(lib.ck_fp8_ffn_workspace_bytes(M, H, I))
+
+
+def fp8_ffn_backward_workspace_bytes(M: int, H: int, I: int) -> int:
+    """Workspace bytes of fp8_ffn_backward."""
+    return int(lib.ck_fp8_ffn_backward_workspace_bytes(M, H, I))
+
+
+def fp8_ffn(x, ffn: Fp8Ffn, out=None, gate_up=None, workspace=None):
+    """Gated feed-forward block, bf16 [M, H]: W2 Q(silu(g) u) with [g; u] = W1 Q(x), Q the quantiser
+    of fp8_quant.  gate_up bf16 [M, 2I], if given, receives g and u for fp8_ffn_backward."""
+    M, dev = _row_count(x, "x"), ffn.device
+    ldx = _rows(x, "x", torch.bfloat16, dev, (M, ffn.H))
+    out, ldo = _fp8_result(out, "out", M, ffn.H, dev)
+    ldg = 0 if gate_up is None else _rows(gate_up, "gate_up", torch.bfloat16, dev, (M, 2 * ffn.I))
+    workspace = _space(workspace, lib.ck_fp8_ffn_workspace_bytes(M, ffn.H, ffn.I) if workspace is None else 0, dev)
+    _check(lib.ck_fp8_ffn(x.data_ptr(), M, ffn.H, ldx, ffn.I, *ffn._args(), out.data_ptr(), ldo,
+                          None if gate_up is None else gate_up.data_ptr(), ldg, workspace.data_ptr(),
+                          workspace.numel(), _stream(x)))
+    return out
+
+
+def fp8_ffn_backward(dy, gate_up, ffn: Fp8FfnTransposed, dx=None, workspace=None):
+    """The gradient bf16 [M, H] of fp8_ffn's input from its output's, dy bf16 [M, H], the gate_up
+    that it kept and the transposed weights (the weights are frozen)."""
+    M, dev = _row_count(dy, "dy"), ffn.device
+    ldy = _rows(dy, "dy", torch.bfloat16, dev, (M, ffn.H))
+    ldg = _rows(gate_up, "gate_up", torch.bfloat16, dev, (M, 2 * ffn.I))
+    dx, lddx = _fp8_result(dx, "dx", M, ffn.H, dev)
+    workspace = _space(workspace, lib.ck_fp8_ffn_backward_workspace_bytes(M, ffn.H, ffn.I)
+                       if workspace is None else 0, dev)
+    _check(lib.ck_fp8_ffn_backward(dy.data_ptr(), M, ffn.H, ldy, gate_up.data_ptr(), ldg, ffn.I, *ffn._args(),
+                                   dx.data_ptr(), lddx, workspace.data_ptr(), workspace.numel(), _stream(dy)))
+    return dx

@@ -5,7 +5,7 @@
 Kernels are compiled with hipcc for gfx950 only.  Packed-fp32 VALU forms are
 switched off (-Xclang -target-feature -Xclang -packed-fp32-ops) and
 floating-point contraction is off, so every fp32 rounding step in the kernels
-is the one written in the source.  The C ABI layer (ck_api.cpp, ck_rows_api.cpp) is
+is the one written in the source.  The C ABI layer (ck_api.cpp, ck_rows_api.cpp, ck_fp8_api.cpp) is
 plain host C++ compiled with g++.
 """
 from __future__ import annotations
@@ -23,8 +23,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libck.so")
 
 HIP_SOURCES = ["rotate_quant.hip", "w4_gemv.hip", "w4_gemv_fused.hip", "w4_skinny.hip", "w4_skinny_fused.hip", "w4_gemm.hip", "w4a16_gemv.hip",
-               "awq_gemm.hip", "static_scratch.hip", "moe_route.hip", "moe_w4a16.hip", "lora.hip"]
-CXX_SOURCES = ["ck_api.cpp", "ck_rows_api.cpp"]
+               "awq_gemm.hip", "static_scratch.hip", "moe_route.hip", "moe_w4a16.hip", "lora.hip", "fp8_quant.hip", "fp8_tiled.hip"]
+CXX_SOURCES = ["ck_api.cpp", "ck_rows_api.cpp", "ck_fp8_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIP_FLAGS = [

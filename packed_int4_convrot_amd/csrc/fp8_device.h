@@ -1,0 +1,66 @@
+// Device helpers of the 8-bit float kernels.
+#pragma once
+
+#include "ck_device.h"
+
+namespace ck {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+// 16 x 16 x 128 e4m3 MFMA with a scale for each lane: byte kA of sa and byte kB of sb
+// (e8m0).  Lane l holds 32 k-values of row (a) or column (b) l % 16, the quarter l / 16;
+// the result's lane l holds column l % 16, rows 4 (l / 16) + i.  Which k-values make up a
+// quarter does not matter as long as a and b agree and all share one scale.
+template <int kA, int kB>
+__device__ __forceinline__ v4f mfma_e4m3(v8i a, v8i b, v4f c, uint32_t sa, uint32_t sb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, kA, (int)sa, kB, (int)sb);
+}
+
+// 16 bytes a lane from a buffer's byte offset (zeros beyond its range) to LDS, lane after lane.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t buffer, __attribute__((address_space(3))) uint8_t *to,
+                                           int offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void *)to, 16, offset, 0, 0, 0);
+}
+
+// e8m0 byte of the smallest power of two s >= 2^-127 with amax <= 448 s, 127 (1.0) for
+// amax = 0; 255 (NaN) where amax is infinite.  448 = 1.75 * 2^8: the exponent of
+// amax less 8, one more where its mantissa is above 1.75.
+__device__ __forceinline__ uint32_t e8m0_of(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)((u + 0x1fffffu) >> 23) - 8;
+    return u == 0 ? 127u : u >= 0x7f800000u ? 255u : (uint32_t)(e < 0 ? 0 : e);
+}
+// 1 / s of an e8m0 byte below 254 (0 for 255: codes of such a block are NaN or 0).
+__device__ __forceinline__ float e8m0_inverse(uint32_t byte)
+{
+    return byte >= 254 ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+
+// Four fp32 to four e4m3, nearest even; |v| <= 448 or NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    int r = 0;
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    return (uint32_t)r;
+}
+
+// The logistic function by the hardware's exponential and reciprocal: a relative error
+// of about 1e-7 (1 + |g|), which only moves which of two neighbouring codes a value
+// beside their border takes.
+__device__ __forceinline__ float logistic(float g)
+{
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+// silu(g) u, and its gradient from d = dL/dh.
+__device__ __forceinline__ float gated(float g, float u) { return g * logistic(g) * u; }
+__device__ __forceinline__ float2 gated_gradient(float d, float g, float u)
+{
+    const float s = logistic(g);
+    return float2{d * u * s * (1.f + g * (1.f - s)), d * g * s};  // dg, du
+}
+
+}  // namespace ck

@@ -1,0 +1,57 @@
+// Internal launch interface of the 8-bit float operators (quantisers, products with a
+// scale for each block of 128, the gated feed-forward block), between ck_fp8_api.cpp
+// and their kernels.  Arguments were validated by the caller; each launcher returns
+// the hipError_t of its launches as an int (0 = success).
+//
+// Codes are e4m3 bytes, scales e8m0 bytes (2^(byte - 127)).  Activations: codes
+// [M, lda], scales [M, ldsa], one for each 128 columns, rows 4-byte aligned and ldsa % 4
+// == 0.  Weights: codes [N, ldw], scales dense [ceil(N / 128), ceil(K / 128)].
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ck {
+
+constexpr int kFp8Block = 128;
+inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+// Row stride in bytes of an activation's scales in a workspace.
+inline int64_t fp8_scale_stride(int64_t K) { return (fp8_blocks(K) + 3) / 4 * 4; }
+
+int launch_fp8_quant(const void *x, bool f32, int64_t M, int K, int64_t ldx, uint8_t *codes, int64_t lda,
+                     uint8_t *scales, int64_t ldsa, void *stream);
+int launch_fp8_quantize_weights(const uint16_t *w, int64_t N, int K, int64_t ldw_in, uint8_t *codes, int64_t ldw,
+                                uint8_t *scales, void *stream);
+int launch_fp8_transpose(const uint8_t *codes, int64_t ldw, const uint8_t *scales, int N, int K, uint8_t *codes_t,
+                         int64_t ldt, uint8_t *scales_t, void *stream);
+
+// What a product's sums become.
+enum class Fp8Result {
+    kBf16,   // bf16 (sums + bias)
+    kGated,  // of 2 I weight rows, gate then up: silu(g) u, quantised; g and u in bf16 where gate_up is given
+    kGrad,   // d(gate) and d(up) of silu(g) u from sums dh and given g and u, quantised
+};
+struct Fp8Product {
+    const uint8_t *a, *sa;   // activations
+    int64_t lda, ldsa;
+    int64_t M;
+    int K;
+    const uint8_t *w, *sw;   // weights
+    int64_t ldw;
+    int N;                   // weight rows
+    // kBf16
+    const uint16_t *bias;
+    uint16_t *out;
+    int64_t ldo;
+    // kGated, kGrad: I columns of h, or of dg and of du
+    int I;
+    uint16_t *gate_up;       // bf16 [M, ldg]: g at column 0, u at column I
+    int64_t ldg;
+    uint8_t *q, *sq;         // the quantised result [M, I] or [M, 2 I]
+    int64_t ldsq;
+};
+// Workgroups of the product on the smallest tiles (128 x 128).
+inline int64_t fp8_tiles(int64_t M, int64_t N) { return fp8_blocks(M) * fp8_blocks(N); }
+int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream);
+
+}  // namespace ck
