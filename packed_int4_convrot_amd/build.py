@@ -23,7 +23,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libck.so")
 
 HIP_SOURCES = ["rotate_quant.hip", "w4_gemv.hip", "w4_gemv_fused.hip", "w4_skinny.hip", "w4_skinny_fused.hip", "w4_gemm.hip", "w4a16_gemv.hip",
-               "awq_gemm.hip", "static_scratch.hip", "moe_route.hip", "moe_w4a16.hip", "lora.hip", "fp8_quant.hip", "fp8_tiled.hip"]
+               "awq_gemm.hip", "static_scratch.hip", "moe_route.hip", "moe_w4a16.hip", "lora.hip", "fp8_quant.hip", "fp8_tiled.hip", "fp8_few.hip"]
 CXX_SOURCES = ["ck_api.cpp", "ck_rows_api.cpp", "ck_fp8_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

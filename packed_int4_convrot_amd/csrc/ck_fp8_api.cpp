@@ -135,13 +135,54 @@ size_t linear_bytes(int64_t M, int64_t K, int64_t N)
 {
     return serves(M, K, 16) && N > 0 && N % 16 == 0 && N <= kMaxRows ? quantised_bytes(M, K) : 0;
 }
+// fp32 results of the few-row products, between a block's two.
+size_t sums_bytes(int64_t M, int64_t I)
+{
+    return round_up((size_t)((M < ck::kFp8FewRows ? M : ck::kFp8FewRows) * I) * sizeof(float), kWsAlign);
+}
+// x, what lies between the two products, and its fp32 form.
+size_t pair_bytes(int64_t M, int64_t H, int64_t inner)
+{
+    return quantised_bytes(M, H) + quantised_bytes(M, inner) + sums_bytes(M, inner);
+}
 size_t ffn_bytes(int64_t M, int64_t H, int64_t I)
 {
-    return serves(M, H, 16) && serves(M, I, 128) ? quantised_bytes(M, H) + quantised_bytes(M, I) : 0;
+    return serves(M, H, 16) && serves(M, I, 128) ? pair_bytes(M, H, I) : 0;
 }
 size_t backward_bytes(int64_t M, int64_t H, int64_t I)
 {
-    return serves(M, H, 16) && serves(M, I, 128) ? quantised_bytes(M, H) + quantised_bytes(M, 2 * I) : 0;
+    return serves(M, H, 16) && serves(M, I, 128) ? pair_bytes(M, H, 2 * I) : 0;
+}
+
+// A product of bf16 (or fp32) rows: quantised on the way where that pays, through q otherwise.
+int from_rows(ck::Fp8Result kind, ck::Fp8Product &p, const void *x, bool f32, int64_t ldx, const Quantised &q,
+              float *sums, void *stream)
+{
+    if (ck::fp8_few_raw(p.M, p.K))
+        return ck::launch_fp8_few(kind, p, x, f32, ldx, sums, stream);
+    const int e = ck::launch_fp8_quant(x, f32, p.M, p.K, ldx, q.codes, p.K, q.scales, q.stride, stream);
+    if (e != 0)
+        return e;
+    p.a = q.codes, p.lda = p.K, p.sa = q.scales, p.ldsa = q.stride;
+    return p.M <= ck::kFp8FewRows ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
+                                  : ck::launch_fp8_tiled(kind, p, stream);
+}
+
+// The two products of a feed-forward block, or of its backward pass.
+int two_products(ck::Fp8Result kind, ck::Fp8Product &first, ck::Fp8Product &second, const uint16_t *x, int64_t ldx,
+                 void *ws, void *stream)
+{
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    const Quantised q = take(at, first.M, first.K), h = take(at, first.M, second.K);
+    float *sums = reinterpret_cast<float *>(at);
+    first.q = h.codes, first.sq = h.scales, first.ldsq = h.stride;
+    const int e = from_rows(kind, first, x, false, ldx, q, sums, stream);
+    if (e != 0)
+        return e;
+    if (first.M <= ck::kFp8FewRows)
+        return from_rows(ck::Fp8Result::kBf16, second, sums, true, second.K, h, nullptr, stream);
+    second.a = h.codes, second.lda = second.K, second.sa = h.scales, second.ldsa = h.stride;
+    return ck::launch_fp8_tiled(ck::Fp8Result::kBf16, second, stream);
 }
 
 int quant_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *codes, int64_t ldq, uint8_t *scales,
@@ -206,12 +247,10 @@ int check_linear(const char *fn, int64_t M, int64_t K, const uint8_t *w, int64_t
     return check_tiles(fn, M, N);
 }
 
-ck::Fp8Product product(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t ldsa, int64_t M, int64_t K,
-                       const uint8_t *w, int64_t ldw, const uint8_t *sw, int64_t N)
+ck::Fp8Product product(int64_t M, int64_t K, const uint8_t *w, int64_t ldw, const uint8_t *sw, int64_t N)
 {
     ck::Fp8Product p{};
-    p.a = a, p.lda = lda, p.sa = sa, p.ldsa = ldsa, p.M = M, p.K = (int)K;
-    p.w = w, p.ldw = ldw, p.sw = sw, p.N = (int)N;
+    p.M = M, p.K = (int)K, p.w = w, p.ldw = ldw, p.sw = sw, p.N = (int)N;
     return p;
 }
 
@@ -231,9 +270,13 @@ int gemm_impl(const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t 
     CK_TRY(check_apart(fn, {span(out, M, N, ldo, 2)},
                        {codes_span(codes, M, K, ldq), scales_span(scales, M, K, lds), codes_span(w, N, K, ldw),
                         weight_scales_span(w_scales, N, K), span(bias, 1, N, N, 2)}));
-    ck::Fp8Product p = product(codes, ldq, scales, lds, M, K, w, ldw, w_scales, N);
+    ck::Fp8Product p = product(M, K, w, ldw, w_scales, N);
+    p.a = codes, p.lda = ldq, p.sa = scales, p.ldsa = lds;
     p.bias = bias, p.out = out, p.ldo = ldo;
-    return hip_status(ck::launch_fp8_tiled(ck::Fp8Result::kBf16, p, stream), fn);
+    return hip_status(M <= ck::kFp8FewRows
+                          ? ck::launch_fp8_few(ck::Fp8Result::kBf16, p, nullptr, false, 0, nullptr, stream)
+                          : ck::launch_fp8_tiled(ck::Fp8Result::kBf16, p, stream),
+                      fn);
 }
 
 int linear_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint8_t *w, int64_t ldw,
@@ -255,12 +298,9 @@ int linear_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint
                         span(bias, 1, N, N, 2)}));
     uint8_t *at = static_cast<uint8_t *>(ws);
     const Quantised q = take(at, M, K);
-    const int e = ck::launch_fp8_quant(x, false, M, (int)K, ldx, q.codes, K, q.scales, q.stride, stream);
-    if (e != 0)
-        return hip_status(e, fn);
-    ck::Fp8Product p = product(q.codes, K, q.scales, q.stride, M, K, w, ldw, w_scales, N);
+    ck::Fp8Product p = product(M, K, w, ldw, w_scales, N);
     p.bias = bias, p.out = out, p.ldo = ldo;
-    return hip_status(ck::launch_fp8_tiled(ck::Fp8Result::kBf16, p, stream), fn);
+    return hip_status(from_rows(ck::Fp8Result::kBf16, p, x, false, ldx, q, nullptr, stream), fn);
 }
 
 int check_ffn(const char *fn, int64_t M, int64_t H, int64_t I, const uint8_t *w1, const uint8_t *s1, const uint8_t *w2,
@@ -303,20 +343,10 @@ int ffn_impl(const uint16_t *x, int64_t M, int64_t H, int64_t ldx, int64_t I, co
                         span(ws, 1, (int64_t)need, (int64_t)need, 1)},
                        {span(x, M, H, ldx, 2), codes_span(w1, 2 * I, H, H), weight_scales_span(s1, 2 * I, H),
                         codes_span(w2, H, I, I), weight_scales_span(s2, H, I)}));
-    uint8_t *at = static_cast<uint8_t *>(ws);
-    const Quantised q = take(at, M, H), h = take(at, M, I);
-    int e = ck::launch_fp8_quant(x, false, M, (int)H, ldx, q.codes, H, q.scales, q.stride, stream);
-    if (e != 0)
-        return hip_status(e, fn);
-    ck::Fp8Product first = product(q.codes, H, q.scales, q.stride, M, H, w1, H, s1, 2 * I);
+    ck::Fp8Product first = product(M, H, w1, H, s1, 2 * I), second = product(M, I, w2, I, s2, H);
     first.I = (int)I, first.gate_up = gate_up, first.ldg = ldg;
-    first.q = h.codes, first.sq = h.scales, first.ldsq = h.stride;
-    e = ck::launch_fp8_tiled(ck::Fp8Result::kGated, first, stream);
-    if (e != 0)
-        return hip_status(e, fn);
-    ck::Fp8Product second = product(h.codes, I, h.scales, h.stride, M, I, w2, I, s2, H);
     second.out = out, second.ldo = ldo;
-    return hip_status(ck::launch_fp8_tiled(ck::Fp8Result::kBf16, second, stream), fn);
+    return hip_status(two_products(ck::Fp8Result::kGated, first, second, x, ldx, ws, stream), fn);
 }
 
 int backward_impl(const uint16_t *dy, int64_t M, int64_t H, int64_t ldy, const uint16_t *gate_up, int64_t ldg,
@@ -337,20 +367,10 @@ int backward_impl(const uint16_t *dy, int64_t M, int64_t H, int64_t ldy, const u
     CK_TRY(check_apart(fn, {span(dx, M, H, lddx, 2), span(ws, 1, (int64_t)need, (int64_t)need, 1)},
                        {span(dy, M, H, ldy, 2), span(gate_up, M, 2 * I, ldg, 2), codes_span(w1t, H, 2 * I, 2 * I),
                         weight_scales_span(s1t, H, 2 * I), codes_span(w2t, I, H, H), weight_scales_span(s2t, I, H)}));
-    uint8_t *at = static_cast<uint8_t *>(ws);
-    const Quantised q = take(at, M, H), d = take(at, M, 2 * I);
-    int e = ck::launch_fp8_quant(dy, false, M, (int)H, ldy, q.codes, H, q.scales, q.stride, stream);
-    if (e != 0)
-        return hip_status(e, fn);
-    ck::Fp8Product first = product(q.codes, H, q.scales, q.stride, M, H, w2t, H, s2t, I);
+    ck::Fp8Product first = product(M, H, w2t, H, s2t, I), second = product(M, 2 * I, w1t, 2 * I, s1t, H);
     first.I = (int)I, first.gate_up = const_cast<uint16_t *>(gate_up), first.ldg = ldg;
-    first.q = d.codes, first.sq = d.scales, first.ldsq = d.stride;
-    e = ck::launch_fp8_tiled(ck::Fp8Result::kGrad, first, stream);
-    if (e != 0)
-        return hip_status(e, fn);
-    ck::Fp8Product second = product(d.codes, 2 * I, d.scales, d.stride, M, 2 * I, w1t, 2 * I, s1t, H);
     second.out = dx, second.ldo = lddx;
-    return hip_status(ck::launch_fp8_tiled(ck::Fp8Result::kBf16, second, stream), fn);
+    return hip_status(two_products(ck::Fp8Result::kGrad, first, second, dy, ldy, ws, stream), fn);
 }
 
 }  // namespace

@@ -54,4 +54,13 @@ struct Fp8Product {
 inline int64_t fp8_tiles(int64_t M, int64_t N) { return fp8_blocks(M) * fp8_blocks(N); }
 int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream);
 
+// Few rows.  x given: bf16 or fp32 rows, quantised on the way (fp8_few_raw), a and sa unused;
+// null: the codes and scales.  kGated and kGrad write fp32 [M, I] or [M, 2 I] to sums.
+constexpr int kFp8Cus = 256;
+constexpr int64_t kFp8FewRows = 64;
+constexpr int64_t kFp8RawRows = 8, kFp8RawBytes = 64 * 1024;
+inline bool fp8_few_raw(int64_t M, int64_t K) { return M <= kFp8RawRows && M * (fp8_blocks(K) * 128) <= kFp8RawBytes; }
+int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums,
+                   void *stream);
+
 }  // namespace ck
