@@ -164,8 +164,8 @@ int from_rows(ck::Fp8Result kind, ck::Fp8Product &p, const void *x, bool f32, in
     if (e != 0)
         return e;
     p.a = q.codes, p.lda = p.K, p.sa = q.scales, p.ldsa = q.stride;
-    return p.M <= ck::kFp8FewRows ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
-                                  : ck::launch_fp8_tiled(kind, p, stream);
+    return ck::fp8_few(p.M, p.K) ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
+                                 : ck::launch_fp8_tiled(kind, p, stream);
 }
 
 // The two products of a feed-forward block, or of its backward pass.
@@ -179,7 +179,7 @@ int two_products(ck::Fp8Result kind, ck::Fp8Product &first, ck::Fp8Product &seco
     const int e = from_rows(kind, first, x, false, ldx, q, sums, stream);
     if (e != 0)
         return e;
-    if (first.M <= ck::kFp8FewRows)
+    if (ck::fp8_few(first.M, first.K))
         return from_rows(ck::Fp8Result::kBf16, second, sums, true, second.K, h, nullptr, stream);
     second.a = h.codes, second.lda = second.K, second.sa = h.scales, second.ldsa = h.stride;
     return ck::launch_fp8_tiled(ck::Fp8Result::kBf16, second, stream);
@@ -273,7 +273,7 @@ int gemm_impl(const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t 
     ck::Fp8Product p = product(M, K, w, ldw, w_scales, N);
     p.a = codes, p.lda = ldq, p.sa = scales, p.ldsa = lds;
     p.bias = bias, p.out = out, p.ldo = ldo;
-    return hip_status(M <= ck::kFp8FewRows
+    return hip_status(ck::fp8_few(M, K)
                           ? ck::launch_fp8_few(ck::Fp8Result::kBf16, p, nullptr, false, 0, nullptr, stream)
                           : ck::launch_fp8_tiled(ck::Fp8Result::kBf16, p, stream),
                       fn);

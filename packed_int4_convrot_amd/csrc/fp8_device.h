@@ -6,15 +6,18 @@
 namespace ck {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
-// 16 x 16 x 128 e4m3 MFMA with a scale for each lane: byte kA of sa and byte kB of sb
-// (e8m0).  Lane l holds 32 k-values of row (a) or column (b) l % 16, the quarter l / 16;
-// the result's lane l holds column l % 16, rows 4 (l / 16) + i.  Which k-values make up a
-// quarter does not matter as long as a and b agree and all share one scale.
-template <int kA, int kB>
-__device__ __forceinline__ v4f mfma_e4m3(v8i a, v8i b, v4f c, uint32_t sa, uint32_t sb)
+// 32 x 32 x 64 e4m3 MFMA with a scale for each lane, the low byte of sa and of sb (e8m0).
+// Lane l holds 32 k-values of row (a) or column (b) l % 32, the half l / 32; the result's
+// lane l holds column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4.
+// Its sums are not quite fp32's: the products of eight neighbouring k-values are aligned to
+// the largest's leading bit and cut off 13 bits below it, so that a dot product of random
+// values is off by 1.5e-5 of itself (rms), a hundredth of its rounding to bf16.  Every e4m3
+// MFMA does so.
+__device__ __forceinline__ v16f mfma_e4m3(v8i a, v8i b, v16f c, uint32_t sa, uint32_t sb)
 {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, kA, (int)sa, kB, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, (int)sa, 0, (int)sb);
 }
 
 // 16 bytes a lane from a buffer's byte offset (zeros beyond its range) to LDS, lane after lane.
@@ -22,6 +25,13 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t buffer, __attr
                                            int offset)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void *)to, 16, offset, 0, 0, 0);
+}
+
+// The same of four bytes a lane.
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t buffer, __attribute__((address_space(3))) uint8_t *to,
+                                          int offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer, (__attribute__((address_space(3))) void *)to, 4, offset, 0, 0, 0);
 }
 
 // e8m0 byte of the smallest power of two s >= 2^-127 with amax <= 448 s, 127 (1.0) for
@@ -46,6 +56,23 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
     r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
     return (uint32_t)r;
+}
+
+// The upper half of a and the lower half of b change places: lanes 0 .. 31 hold their own a and
+// the a of lane + 32, lanes 32 .. 63 the b of lane - 32 and their own.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0], b = r[1];
+}
+
+// The workgroup's LDS writes are seen; loads stay under way.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // The logistic function by the hardware's exponential and reciprocal: a relative error

@@ -1,9 +1,12 @@
 // Products of a few rows of activations with 8-bit float weights: decode steps, bound by
 // the weights' way from memory.
 //
-// One workgroup for each CU takes an equal run of weight rows; its waves share the columns,
-// a wave every kWaves-th block of 128, and add their sums up through LDS at the end.  Any
-// number of rows can make up a run: rows past its end read its last row again.
+// One workgroup for each CU takes an equal run of weight rows; its eight waves share the
+// columns, a wave every eighth block of 128, and add their sums up through LDS at the
+// end.  Any number of rows can make up a run: rows past its end read its last row again.
+// A wave's weights go global -> LDS directly into a ring of its own, eight units of 16 rows
+// by 128 columns, so that 128 KB are on their way to a CU without a register or a barrier;
+// the 16-byte slots of a row are XORed with bits of the row, as in the tiled product.
 //
 // The products run on the 16 x 16 x 32 bf16 MFMA: an e4m3 code times its block's power of
 // two is a bf16 value, so both operands are exact and the sums are fp32's.  (The e4m3
@@ -12,6 +15,7 @@
 //
 // kRaw and kRawF32: the rows come as bf16 or fp32 and every workgroup quantises them itself,
 // into LDS, while its first weights are under way, which saves the quantiser's launch.
+// kCodes: the rows' codes come through the ring, before the weights of their block.
 #include <type_traits>
 
 #include "fp8_device.h"
@@ -21,8 +25,24 @@
 namespace ck {
 namespace {
 
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+
 enum class Source { kCodes, kRaw, kRawF32 };
 
+constexpr int kWaves = 8, kThreads = kWaves * kWave;
+constexpr int kUnit = 2048, kRing = 8;                 // bytes of a unit, units of a wave's ring
+constexpr int kRings = kWaves * kRing * kUnit;
+constexpr int kScaleLoads = 4;                         // bytes of weight scales a thread
+constexpr int kRawChunks = kFp8RawBytes / 8 / kThreads;  // of eight columns a thread
+static_assert(kRawChunks * 8 * kThreads == kFp8RawBytes, "whole chunks");
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
 // Eight codes as bf16 values, times s (a power of two).
 __device__ __forceinline__ v8bf values8(uint32_t lo, uint32_t hi, float s)
 {
@@ -35,193 +55,278 @@ __device__ __forceinline__ v8bf values8(uint32_t lo, uint32_t hi, float s)
 }
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// Division of 0 <= n < 2^16 by 1 <= d < 2^16: n ceil(2^32 / d) / 2^32 is less than 1 / d off.
+struct Divide {
+    uint32_t inverse;
+    __device__ __forceinline__ int operator()(int n) const { return (int)__umulhi((uint32_t)n, inverse); }
+};
+inline Divide divide_by(int64_t d) { return Divide{(uint32_t)((((int64_t)1 << 32) + d - 1) / d)}; }
+
+// 32 values of a row and block: 16 columns from 16 quarter on, and 16 from 64 + 16 quarter on.
+struct Values {
+    v8bf v[4];
+};
+__device__ __forceinline__ Values values32(u32x4 x, u32x4 y, uint32_t scale)
+{
+    const float s = scale_value(scale);
+    return Values{{values8(x[0], x[1], s), values8(x[2], x[3], s), values8(y[0], y[1], s), values8(y[2], y[3], s)}};
+}
+
+// Column tiles that one pass takes at most.
+template <Fp8Result kKind, int kMt>
+constexpr int kMostTiles = (kMt == 1 ? 8 : 4) / (kKind == Fp8Result::kGated ? 2 : 1);
+
 // kMt: 16-row tiles of activations; kT: 16-row tiles of weights a pass (half gate and half
-// up, for kGated); kD: blocks of weights on their way beside the one in use.
-template <Source kSource, Fp8Result kKind, int kMt, int kT, int kD, int kWaves>
-__global__ __launch_bounds__(kWaves *kWave) void fp8_few_kernel(Fp8Product p, const void *__restrict__ x, int64_t ldx,
-                                                                float *__restrict__ sums, int per, int passes)
+// up, for kGated).
+template <Source kSource, Fp8Result kKind, int kMt, int kT>
+__global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const void *__restrict__ x, int64_t ldx,
+                                                           float *__restrict__ sums, int per, int passes,
+                                                           Divide by_steps, Divide by_dwords)
 {
     constexpr bool kGated = kKind == Fp8Result::kGated;
     constexpr bool kRaw = kSource != Source::kCodes;
-    constexpr int kThreads = kWaves * kWave;
-    constexpr int kPass = (kGated ? kT / 2 : kT) * 16;   // result columns of a pass
+    constexpr int kPair = kGated ? 2 : 1, kPass = kT / kPair * 16;   // result columns of a pass
+    constexpr int kBlockRows = (kPass + 127) / 128 + 1;              // rows of weight blocks they can touch
+    constexpr int kUnits = kT + (kRaw ? 0 : kMt);                    // of a block
+    // Equal passes: several are longer than half the most.
+    constexpr bool kPasses = kT / kPair > kMostTiles<kKind, kMt> / 2;
     static_assert(!kRaw || kMt == 1, "raw rows make up one tile");
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    v4f *red = reinterpret_cast<v4f *>(smem);            // [kWaves][kT][kMt][64]
-    float *red1 = reinterpret_cast<float *>(smem);
-    uint8_t *lds_codes = smem + kWaves * kT * kMt * kWave * 16;
+    static_assert(kT * kMt <= 2 * kRing, "a wave's sums fit its ring");
+    static_assert(kPair * kBlockRows * 512 <= kScaleLoads * kThreads, "scales of up to 512 blocks");
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem_generic[];
+    lds_u8 *smem = (lds_u8 *)smem_generic;
 
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
     const int l16 = lane % 16, quarter = lane / 16;
     const int M = (int)p.M, K = p.K, steps = (K + 127) / 128;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int c0 = blockIdx.x * per, c1 = min(c0 + per, cols);
-    if (c0 >= cols)
-        return;
-    const int pitch = steps * 128 + 16;
-    uint8_t *lds_scales = lds_codes + M * pitch;         // [M][steps]
+    lds_u8 *ring = smem + wave * kRing * kUnit;
+    lds_u8 *sw = smem + kRings;                          // [kPair][kBlockRows][steps]
+    const int sa_pitch = (steps + 3) / 4 * 4, pitch = steps * 128 + 16;
+    lds_u8 *sa = sw + kScaleLoads * kThreads;            // [M][sa_pitch]
+    lds_u8 *codes = sa + (M * sa_pitch + 15) / 16 * 16;  // [M][pitch]
 
-    // A lane's share of a block: 16 columns from 16 quarter on, and 16 from 64 + 16 quarter on.
-    struct Piece {
-        u32x4 v[2];
-        uint32_t scale;
+    u32x4 raw[kRaw ? kRawChunks : 1][kSource == Source::kRawF32 ? 2 : 1];
+    const int chunks = M * steps * 16;                   // of eight columns
+    // (m, first column) of a thread's r-th chunk.
+    auto chunk_of = [&](int r) {
+        const int i = min(r * kThreads + t, chunks - 1), m = steps == 1 ? i / 16 : by_steps(i / 16);
+        return int2{m, (i - m * steps * 16) * 8};
     };
-    Piece w[kD][kT];
-    const uint8_t *w_row[kT], *w_scale[kT];
-    auto rows_of = [&](int first) {
+    if constexpr (kRaw) {
+#pragma unroll
+        for (int r = 0; r < kRawChunks; ++r) {
+            const int2 c = chunk_of(r);
+            const int64_t at = c.x * ldx + min(c.y, K - 8);
+            if constexpr (kSource == Source::kRawF32) {
+                const u32x4 *from = reinterpret_cast<const u32x4 *>(static_cast<const float *>(x) + at);
+                raw[r][0] = from[0], raw[r][1] = from[1];
+            } else {
+                raw[r][0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(x) + at);
+            }
+        }
+    }
+
+    // A load fills eight rows of a unit.  Rows are clamped, so only columns past K are out of
+    // a buffer's range; they read as zeros.
+    constexpr int kRange = 0x7ffffff0, kPast = 0x7fffffff;
+    const int chunk = 16 * (lane % 8), eight = lane / 8;
+    const int at0 = chunk ^ (16 * ((eight >> 1) & 7)), at1 = chunk ^ (16 * (((eight + 8) >> 1) & 7));
+    __amdgpu_buffer_rsrc_t w_rsrc, a_rsrc;
+    int w_row[kT][2], a_row[kRaw ? 1 : kMt][2];          // byte offsets of a lane's rows
+    if constexpr (!kRaw) {
+        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, kRange, 0x00020000);
+#pragma unroll
+        for (int j = 0; j < kMt; ++j) {
+            a_row[j][0] = min(j * 16 + eight, M - 1) * (int)p.lda + at0;
+            a_row[j][1] = min(j * 16 + 8 + eight, M - 1) * (int)p.lda + at1;
+        }
+    }
+    auto start_pass = [&](int first) {
+        w_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.w + first * p.ldw), (short)0, kRange, 0x00020000);
 #pragma unroll
         for (int i = 0; i < kT; ++i) {
-            const int tile = kGated ? i % (kT / 2) : i;
-            const int row = min(first + tile * 16 + l16, c1 - 1) + (kGated && i >= kT / 2 ? p.I : 0);
-            w_row[i] = p.w + (int64_t)row * p.ldw + 16 * quarter;
-            w_scale[i] = p.sw + (int64_t)(row / 128) * steps;
+            const int tile = i % (kT / kPair), far = i / (kT / kPair) * p.I;
+            w_row[i][0] = (min(tile * 16 + eight, c1 - 1 - first) + far) * (int)p.ldw + at0;
+            w_row[i][1] = (min(tile * 16 + 8 + eight, c1 - 1 - first) + far) * (int)p.ldw + at1;
         }
     };
-    auto load = [&](Piece &q, int i, int b) {
-        const uint8_t *at = w_row[i] + b * 128;
-        if (b * 128 + 128 <= K) {
-            q.v[0] = load_nt16(at);
-            q.v[1] = load_nt16(at + 64);
-        } else {
-            const int k = b * 128 + 16 * quarter;
-            q.v[0] = k < K ? load_nt16(at) : u32x4{0, 0, 0, 0};
-            q.v[1] = k + 64 < K ? load_nt16(at + 64) : u32x4{0, 0, 0, 0};
-        }
-        q.scale = w_scale[i][b];
+    int place = 0;                                       // ring slot of the next unit
+    // Workgroups start at columns of their own, so that they are spread over the memory.
+    const int shift = (int)((int64_t)blockIdx.x * steps / gridDim.x);
+    auto turned = [&](int b) { return b + shift < steps ? b + shift : b < steps ? b + shift - steps : b; };
+    // Unit u of block b: the rows' codes, then the weights.  A block past the last reads zeros.
+    auto issue = [&](int u, int nth, int slot) {
+        const int b = turned(nth);
+        lds_u8 *to = ring + slot * kUnit;
+        const bool act = u < kUnits - kT;
+        const int r0 = act ? a_row[kRaw ? 0 : u][0] : w_row[u - (kUnits - kT)][0];
+        const int r1 = act ? a_row[kRaw ? 0 : u][1] : w_row[u - (kUnits - kT)][1];
+        load_lds16(act ? a_rsrc : w_rsrc, to, b * 128 + at0 < K ? r0 + b * 128 : kPast);
+        load_lds16(act ? a_rsrc : w_rsrc, to + 1024, b * 128 + at1 < K ? r1 + b * 128 : kPast);
     };
+    // The first kRing units.
     auto fill = [&]() {
 #pragma unroll
-        for (int d = 0; d < kD; ++d)
-            if (wave + d * kWaves < steps)
-#pragma unroll
-                for (int i = 0; i < kT; ++i)
-                    load(w[d][i], i, wave + d * kWaves);
+        for (int n = 0; n < kRing; ++n)
+            issue(n % kUnits, wave + n / kUnits * kWaves, n);
+        place = 0;
     };
-    rows_of(c0);
+    // Loads return in order, so what is waited for first goes ahead of the ring's.
+    uint32_t sw_in[kScaleLoads];
+    const int sw_count = kPair * kBlockRows * steps;
+    auto load_scales = [&](int first) {
+#pragma unroll
+        for (int r = 0; r < kScaleLoads; ++r) {
+            const int i = min(r * kThreads + t, sw_count - 1), block = steps == 1 ? i : by_steps(i);
+            const int row = block / kBlockRows * p.I + min((first / 128 + block % kBlockRows) * 128, c1 - 1);
+            sw_in[r] = p.sw[(int64_t)(row / 128) * steps + i - block * steps];
+        }
+    };
+    auto keep_scales = [&]() {
+#pragma unroll
+        for (int r = 0; r < kScaleLoads; ++r)
+            if (r * kThreads < sw_count)
+                sw[r * kThreads + t] = (uint8_t)sw_in[r];
+    };
+    load_scales(c0);
+    constexpr int kRowScaleLoads = kMt == 1 ? 4 : 8;
+    uint32_t sa_in[kRaw ? 1 : kRowScaleLoads];
+    const int sa_count = M * (sa_pitch / 4);
+    if constexpr (!kRaw) {
+#pragma unroll
+        for (int r = 0; r < kRowScaleLoads; ++r) {
+            const int i = min(r * kThreads + t, sa_count - 1), m = sa_pitch == 4 ? i : by_dwords(i);
+            sa_in[r] = *reinterpret_cast<const uint32_t *>(p.sa + m * p.ldsa + (i * 4 - m * sa_pitch));
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    start_pass(c0);
     fill();
+    __builtin_amdgcn_sched_barrier(0);
 
     if constexpr (kRaw) {
         // 16 threads a block, eight columns each; columns past K are zeros.
-        constexpr bool kF32 = kSource == Source::kRawF32;
-        for (int i = t; i < M * steps * 16; i += kThreads) {
-            const int m = i / (steps * 16), k = (i - m * steps * 16) * 8;
-            float v[8];
-            if (k < K) {
-                if constexpr (kF32) {
-                    const v4f *at = reinterpret_cast<const v4f *>(static_cast<const float *>(x) + m * ldx + k);
-                    const v4f lo = at[0], hi = at[1];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = lo[j], v[4 + j] = hi[j];
-                } else {
-                    const u32x4 q = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(x) + m * ldx + k);
+        for (int r = 0; r < kRawChunks; ++r) {
+            const int i = r * kThreads + t;
+            const int2 c = chunk_of(r);
+            if (r * kThreads < chunks) {
+                float v[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[2 * j] = bf16_to_f32(q[j] & 0xffffu), v[2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (kSource == Source::kRawF32)
+                        v[j] = __uint_as_float(raw[r][j / 4][j % 4]);
+                    else
+                        v[j] = j % 2 ? __uint_as_float(raw[r][0][j / 2] & 0xffff0000u)
+                                     : bf16_to_f32(raw[r][0][j / 2] & 0xffffu);
+                    v[j] = c.y < K ? v[j] : 0.f;
                 }
-            } else {
+                float a = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] = 0.f;
+                    a = fmaxf(a, fabsf(v[j]));
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2)
+                    a = fmaxf(a, __shfl_xor(a, d));
+                const uint32_t s = e8m0_of(a);
+                const float inv = e8m0_inverse(s);
+                if (i < chunks) {
+                    const u32x2 q = {pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                                     pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+                    *(__attribute__((address_space(3))) u32x2 *)(codes + c.x * pitch + c.y) = q;
+                    if (i % 16 == 0)
+                        sa[c.x * sa_pitch + c.y / 128] = (uint8_t)s;
+                }
             }
-            float a = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                a = fmaxf(a, fabsf(v[j]));
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2)
-                a = fmaxf(a, __shfl_xor(a, d));
-            const uint32_t s = e8m0_of(a);
-            const float inv = e8m0_inverse(s);
-            const u32x2 q = {pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                             pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
-            *reinterpret_cast<u32x2 *>(lds_codes + m * pitch + k) = q;
-            if (i % 16 == 0)
-                lds_scales[m * steps + k / 128] = (uint8_t)s;
         }
-        __syncthreads();
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRowScaleLoads; ++r)
+            if (r * kThreads + t < sa_count)
+                *(__attribute__((address_space(3))) uint32_t *)(sa + (r * kThreads + t) * 4) = sa_in[r];
     }
+    keep_scales();
+    lds_barrier();
 
-    auto activation = [&](Piece &q, int j, int b) {
-        const int m = min(j * 16 + l16, M - 1), k = b * 128 + 16 * quarter;
-        if constexpr (kRaw) {
-            const uint8_t *at = lds_codes + m * pitch + k;
-            q.v[0] = *reinterpret_cast<const u32x4 *>(at);
-            q.v[1] = *reinterpret_cast<const u32x4 *>(at + 64);
-            q.scale = lds_scales[m * steps + b];
-        } else {
-            const uint8_t *at = p.a + m * p.lda + k;
-            q.v[0] = k < K ? *reinterpret_cast<const u32x4 *>(at) : u32x4{0, 0, 0, 0};
-            q.v[1] = k + 64 < K ? *reinterpret_cast<const u32x4 *>(at + 64) : u32x4{0, 0, 0, 0};
-            q.scale = p.sa[m * p.ldsa + b];
-        }
-    };
-
-    for (int pass = 0; pass < passes; ++pass) {
+    const int near = l16 * 128 + ((16 * quarter) ^ (16 * ((l16 >> 1) & 7)));
+    const int far = l16 * 128 + ((64 + 16 * quarter) ^ (16 * ((l16 >> 1) & 7)));
+    for (int pass = 0; pass < (kPasses ? passes : 1); ++pass) {
         const int first = c0 + pass * kPass;
         if (first >= c1)
             break;
+        if (kPasses && pass > 0) {
+            lds_barrier();   // the last pass's sums and scales are read
+            load_scales(first);
+            __builtin_amdgcn_sched_barrier(0);
+            start_pass(first);
+            fill();
+            __builtin_amdgcn_sched_barrier(0);
+            keep_scales();
+            lds_barrier();
+        }
+        int sw_at[kT];       // of a lane's weight rows
+#pragma unroll
+        for (int i = 0; i < kT; ++i) {
+            const int row = min(first + i % (kT / kPair) * 16 + l16, c1 - 1);
+            sw_at[i] = (i / (kT / kPair) * kBlockRows + row / 128 - first / 128) * steps;
+        }
         v4f acc[kT][kMt];
 #pragma unroll
         for (int i = 0; i < kT; ++i)
 #pragma unroll
             for (int j = 0; j < kMt; ++j)
                 acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int b0 = wave; b0 < steps; b0 += kD * kWaves) {
+        for (int nth = wave; nth < steps; nth += kWaves) {
+            const int b = turned(nth);
+            Values a[kMt];
+            if constexpr (kRaw) {
+                const int m = min(l16, M - 1);
+                const lds_u8 *at = codes + m * pitch + b * 128 + 16 * quarter;
+                a[0] = values32(*(lds_u32x4 *)at, *(lds_u32x4 *)(at + 64), sa[m * sa_pitch + b]);
+            }
 #pragma unroll
-            for (int d = 0; d < kD; ++d) {
-                const int b = b0 + d * kWaves;
-                if (b < steps) {
-                    Piece a[kMt];
+            for (int u = 0; u < kUnits; ++u) {
+                wait_vmcnt<2 * (kRing - 1)>();
+                asm volatile("" ::: "memory");
+                const lds_u8 *unit = ring + place * kUnit;
+                const u32x4 lo = *(lds_u32x4 *)(unit + near), hi = *(lds_u32x4 *)(unit + far);
+                const int i = u - (kUnits - kT);
+                const uint32_t scale = i < 0 ? sa[min(u * 16 + l16, M - 1) * sa_pitch + b] : sw[sw_at[i < 0 ? 0 : i] + b];
+                const Values v = values32(lo, hi, scale);
+                // The unit is in registers: its slot takes the unit a ring's length on.
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                issue((u + kRing) % kUnits, nth + (u + kRing) / kUnits * kWaves, place);
+                place = place + 1 == kRing ? 0 : place + 1;
+                if (i < 0) {
+                    a[i < 0 ? u : 0] = v;
+                } else {
 #pragma unroll
-                    for (int j = 0; j < kMt; ++j)
-                        activation(a[j], j, b);
-                    v8bf av[kMt][4];
+                    for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int j = 0; j < kMt; ++j)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            av[j][s] = values8(a[j].v[s / 2][s % 2 * 2], a[j].v[s / 2][s % 2 * 2 + 1],
-                                               scale_value(a[j].scale));
-#pragma unroll
-                    for (int i = 0; i < kT; ++i) {
-                        const Piece q = w[d][i];
-                        const float ws = scale_value(q.scale);
-                        v8bf wv[4];
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            wv[s] = values8(q.v[s / 2][s % 2 * 2], q.v[s / 2][s % 2 * 2 + 1], ws);
-                        if (b + kD * kWaves < steps)
-                            load(w[d][i], i, b + kD * kWaves);
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-#pragma unroll
-                            for (int j = 0; j < kMt; ++j)
-                                acc[i][j] = mfma16(wv[s], av[j][s], acc[i][j]);
-                    }
+                        for (int j = 0; j < kMt; ++j)
+                            acc[i < 0 ? 0 : i][j] = mfma16(v.v[s], a[j].v[s], acc[i < 0 ? 0 : i][j]);
                 }
             }
         }
-        if (pass + 1 < passes && first + kPass < c1) {
-            rows_of(first + kPass);
-            fill();
-        }
-        if (pass > 0)
-            __syncthreads();   // the last pass's sums are read
+        // The ring holds nothing more that is used.
+        wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kT; ++i)
 #pragma unroll
             for (int j = 0; j < kMt; ++j)
                 if (j * 16 + l16 < M)
-                    red[((wave * kT + i) * kMt + j) * kWave + lane] = acc[i][j];
-        __syncthreads();
+                    *(__attribute__((address_space(3))) v4f *)(ring + ((i * kMt + j) * kWave + lane) * 16) = acc[i][j];
+        lds_barrier();
         // Element (m, row of the pass's tiles): the waves' sums in order.
         auto total = [&](int m, int row) {
             const int at = ((row / 16 * kMt + m / 16) * kWave + row % 16 / 4 * 16 + m % 16) * 4 + row % 4;
             float s = 0.f;
 #pragma unroll
             for (int o = 0; o < kWaves; ++o)
-                s += red1[o * kT * kMt * kWave * 4 + at];
+                s += *(__attribute__((address_space(3))) const float *)(smem + o * kRing * kUnit + at * 4);
             return s;
         };
         for (int e = t; e < kPass * M; e += kThreads) {
@@ -248,45 +353,44 @@ __global__ __launch_bounds__(kWaves *kWave) void fp8_few_kernel(Fp8Product p, co
     }
 }
 
-template <Source kSource, Fp8Result kKind, int kMt, int kT, int kD, int kWaves>
+template <Source kSource, Fp8Result kKind, int kMt, int kT>
 int launch_one(const Fp8Product &p, const void *x, int64_t ldx, float *sums, int grid, int per, int passes,
                void *stream)
 {
-    auto kern = fp8_few_kernel<kSource, kKind, kMt, kT, kD, kWaves>;
-    const int64_t rows = kSource == Source::kCodes ? 0 : p.M;
-    const size_t lds = (size_t)kWaves * kT * kMt * kWave * 16 +
-                       (size_t)(rows * (fp8_blocks(p.K) * 128 + 16) + rows * fp8_blocks(p.K));
+    auto kern = fp8_few_kernel<kSource, kKind, kMt, kT>;
+    const size_t steps = fp8_blocks(p.K), M = p.M;
+    const size_t lds = kRings + kScaleLoads * kThreads + (M * ((steps + 3) / 4 * 4) + 15) / 16 * 16 +
+                       (kSource == Source::kCodes ? 0 : M * (steps * 128 + 16));
     constexpr int kMostLds = 160 * 1024;
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
     if (attr != hipSuccess)
         return (int)attr;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kWaves * kWave), lds, reinterpret_cast<hipStream_t>(stream), p,
-                       x, ldx, sums, per, passes);
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, reinterpret_cast<hipStream_t>(stream), p, x,
+                       ldx, sums, per, passes, divide_by((int64_t)steps), divide_by((int64_t)(steps + 3) / 4));
     return (int)hipGetLastError();
 }
 
 template <Source kSource, Fp8Result kKind, int kMt>
 int launch_shape(const Fp8Product &p, const void *x, int64_t ldx, float *sums, void *stream)
 {
-    constexpr int kPair = kKind == Fp8Result::kGated ? 2 : 1, kWaves = kMt == 1 ? 16 : 8;
-    constexpr int kMost = 4 / kPair;   // column tiles of a pass
+    constexpr int kPair = kKind == Fp8Result::kGated ? 2 : 1;
+    constexpr int kMost = kMostTiles<kKind, kMt>;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int per = (cols + kFp8Cus - 1) / kFp8Cus, grid = (cols + per - 1) / per;
     const int tiles = (per + 15) / 16, passes = (tiles + kMost - 1) / kMost, each = (tiles + passes - 1) / passes;
-#define CK_FP8_FEW(T)                                                                                            \
-    return launch_one<kSource, kKind, kMt, T * kPair, (T * kPair <= 2 ? 2 : 1), kWaves>(p, x, ldx, sums, grid, per, \
-                                                                                        passes, stream)
-    if (each == 1)
-        CK_FP8_FEW(1);
-    if constexpr (kPair == 1) {
-        if (each == 3)
-            CK_FP8_FEW(3);
-        if (each == 4)
-            CK_FP8_FEW(4);
-    }
+#define CK_FP8_FEW(T)                                                                                  \
+    if constexpr (T <= kMost)                                                                          \
+        if (each <= T)                                                                                 \
+    return launch_one<kSource, kKind, kMt, T * kPair>(p, x, ldx, sums, grid, per, passes, stream)
+    CK_FP8_FEW(1);
     CK_FP8_FEW(2);
+    CK_FP8_FEW(3);
+    CK_FP8_FEW(4);
+    CK_FP8_FEW(6);
+    CK_FP8_FEW(8);
 #undef CK_FP8_FEW
+    return (int)hipErrorInvalidValue;
 }
 
 template <Fp8Result kKind>
@@ -299,6 +403,8 @@ int launch_kind(const Fp8Product &p, const void *x, bool f32, int64_t ldx, float
         return launch_shape<Source::kCodes, kKind, 1>(p, x, ldx, sums, stream);
     if (p.M <= 32)
         return launch_shape<Source::kCodes, kKind, 2>(p, x, ldx, sums, stream);
+    if (p.M <= 48)
+        return launch_shape<Source::kCodes, kKind, 3>(p, x, ldx, sums, stream);
     return launch_shape<Source::kCodes, kKind, 4>(p, x, ldx, sums, stream);
 }
 

@@ -58,8 +58,10 @@ int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream);
 // null: the codes and scales.  kGated and kGrad write fp32 [M, I] or [M, 2 I] to sums.
 constexpr int kFp8Cus = 256;
 constexpr int64_t kFp8FewRows = 64;
-constexpr int64_t kFp8RawRows = 8, kFp8RawBytes = 64 * 1024;
+constexpr int kFp8RawRows = 8, kFp8RawBytes = 16 * 1024;
 inline bool fp8_few_raw(int64_t M, int64_t K) { return M <= kFp8RawRows && M * (fp8_blocks(K) * 128) <= kFp8RawBytes; }
+// The rows' scales lie in LDS beside 128 KB of rings.
+inline bool fp8_few(int64_t M, int64_t K) { return M <= kFp8FewRows && M * fp8_scale_stride(K) <= 16 * 1024; }
 int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums,
                    void *stream);
 

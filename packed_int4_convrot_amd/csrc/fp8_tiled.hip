@@ -3,12 +3,14 @@
 //
 //   sums[m, n] = sum_b 2^(sa[m, b] + sw[n / 128, b]) sum_{k in block b} a[m, k] w[n, k]
 //
-// A block of 128 columns is one 16 x 16 x 128 MFMA, which takes an e8m0 scale for each
-// row of either operand: the scales cost no instruction and the sums of all blocks stay
-// in one fp32 accumulator.  Weights are the rows of the result (operand A), activations
-// its columns: a lane has one row of the output and four neighbouring columns a tile.
+// The 32 x 32 x 64 MFMA takes an e8m0 scale for each row of either operand: the scales
+// cost no instruction and the sums of all blocks stay in one fp32 accumulator.  (On
+// random codes it holds 4.1 PFLOP/s over the chip, the 16 x 16 x 128 one 3.8: both are
+// bound by power.)  Weights are the rows of the result (operand A), activations its
+// columns: a lane has one row of the output and, of a tile, four times four neighbouring
+// columns.
 //
-// A workgroup has kWn x kWm waves, a wave kTn x kTm tiles of 16 x 16.  A stage is one
+// A workgroup has kWn x kWm waves, a wave kTn x kTm tiles of 32 x 32.  A stage is one
 // block of 128 columns of every row of both operands, 128 bytes a row, moved from
 // global memory to LDS directly into two buffers; the 16-byte slots of a row are
 // XORed with bits of the row so that the lanes of a fragment's read meet in no bank.
@@ -30,59 +32,68 @@ typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 // LDS slot of 16-byte chunk c of row r, and the reverse.
 __device__ __forceinline__ int swizzle(int r, int c) { return c ^ ((r >> 1) & 7); }
 
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xc07f); }
-
+// This wave's LDS reads have returned and all but the last N of its loads have landed.
+template <int N>
+__device__ __forceinline__ void wait_reads_and_loads()
+{
+    static_assert(N < 16, "vmcnt");
+    __builtin_amdgcn_s_waitcnt(N | (7 << 4));
+}
 
 template <int kWn_, int kWm_, int kTn_, int kTm_>
 struct Tile {
     static constexpr int kWn = kWn_, kWm = kWm_, kTn = kTn_, kTm = kTm_;
     static constexpr int kWaves = kWn * kWm;
-    static constexpr int kBn = kWn * kTn * 16, kBm = kWm * kTm * 16;
+    static constexpr int kBn = kWn * kTn * 32, kBm = kWm * kTm * 32;
     static constexpr int kStage = (kBn + kBm) * 128;
-    // Scales of 64 steps: a row for each activation row and for two rows of weight blocks.
-    static constexpr int kScaleSteps = 64, kScalePitch = kScaleSteps + 4;
-    static constexpr int kScales = (kBm + 2) * kScalePitch;
-    static constexpr int kPitch = kTn * 32 + 16;      // a staged row of a wave's bf16 tile
-    static constexpr int kOut = kWaves * kTm * 16 * kPitch;
-    static constexpr int kCodePitch = 128 + 16;       // a staged row of a block's codes
-    static constexpr int kCodes = (kBn + 127) / 128 * kBm * kCodePitch;
-    static constexpr int kMost = kOut > kCodes ? kOut : kCodes;
-    static constexpr int kLds = (2 * kStage > kMost ? 2 * kStage : kMost) + kScales + kWaves * kTm * 16 * 4;
+    // Scales of 64 steps: dwords (four steps) [16][kBm] of the activations, then bytes [2][64]
+    // of two rows of weight blocks.
+    static constexpr int kScaleSteps = 64, kRowScales = kScaleSteps * kBm;
+    static constexpr int kScales = kRowScales + 2 * kScaleSteps;
+    static constexpr int kLds = 2 * kStage + kScales + kWaves * 32 * 4;
+    static constexpr int kPerCu = 160 * 1024 / kLds;
 };
 
 template <class T, Fp8Result kKind>
-__global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product p, int tiles_m, int tiles_n)
+__global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product p, int tiles_m, int tiles)
 {
     constexpr bool kGated = kKind == Fp8Result::kGated;
     constexpr int kBn = T::kBn, kBm = T::kBm, kTn = T::kTn, kTm = T::kTm, kWaves = T::kWaves;
     static_assert(!kGated || kBn == 256, "a gated tile covers one block of the result");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem_generic[];
     lds_u8 *smem = (lds_u8 *)smem_generic;
-    lds_u8 *scales = smem + (2 * T::kStage > T::kMost ? 2 * T::kStage : T::kMost);
+    lds_u8 *scales = smem + 2 * T::kStage;
     __attribute__((address_space(3))) float *red = (__attribute__((address_space(3))) float *)(scales + T::kScales);
 
-    // Runs of kGroupM tile rows are walked column by column, a contiguous run on each XCD.
-    constexpr int kGroupM = 4;
-    const int tile = xcd_block(blockIdx.x, tiles_m * tiles_n);
-    const int group = tile / (kGroupM * tiles_n);
-    const int first_m = group * kGroupM;
-    const int group_m = min(kGroupM, tiles_m - first_m);
-    const int in_group = tile - group * kGroupM * tiles_n;
-    const int64_t m0 = (int64_t)(first_m + in_group % group_m) * kBm;
-    const int n0 = (in_group / group_m) * (kGated ? kBn / 2 : kBn);  // first column of the result
-
-    const int t = threadIdx.x, wave = t / kWave, lane = t % kWave;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
     const int wn = wave / T::kWm, wm = wave % T::kWm;
-    const int l16 = lane % 16, quarter = lane / 16;
+    const int l32 = lane % 32, half = lane / 32;
     const int K = p.K, steps = (K + 127) / 128;
-    const int rows = (int)min((int64_t)kBm, p.M - m0);
 
-    // Operand rows past the end and columns past K read as zero (out of the buffer's range).
-    const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(p.a + m0 * p.lda), (short)0, (int)((rows - 1) * p.lda + K), 0x00020000);
-    const int w_rows = kGated ? p.I + kBn / 2 : min(kBn, p.N - n0);
-    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(p.w + n0 * p.ldw), (short)0, (int)((w_rows - 1) * p.ldw + K), 0x00020000);
+    // A workgroup takes tile after tile.  Runs of kGroupM tile rows are walked column by column,
+    // a contiguous run on each XCD.
+    int64_t m0;
+    int n0, rows;                                        // first row and column of the result
+    __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc, sa_rsrc;
+    auto start_tile = [&](int index) {
+        constexpr int kGroupM = 4;
+        const int tiles_n = tiles / tiles_m, tile = xcd_block(index, tiles);
+        const int group = tile / (kGroupM * tiles_n);
+        const int first_m = group * kGroupM;
+        const int group_m = min(kGroupM, tiles_m - first_m);
+        const int in_group = tile - group * kGroupM * tiles_n;
+        m0 = (int64_t)(first_m + in_group % group_m) * kBm;
+        n0 = (in_group / group_m) * (kGated ? kBn / 2 : kBn);
+        rows = (int)min((int64_t)kBm, p.M - m0);
+        // Operand rows past the end and columns past K read as zero (out of the buffer's range).
+        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.a + m0 * p.lda), (short)0,
+                                                   (int)((rows - 1) * p.lda + K), 0x00020000);
+        const int w_rows = kGated ? p.I + kBn / 2 : min(kBn, p.N - n0);
+        w_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.w + n0 * p.ldw), (short)0,
+                                                   (int)((w_rows - 1) * p.ldw + K), 0x00020000);
+        sa_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.sa + m0 * p.ldsa), (short)0, (int)(rows * p.ldsa),
+                                                    0x00020000);
+    };
     constexpr int kPast = 0x7fffffff;
     constexpr int kALoads = kBm * 128 / (kWaves * 1024), kWLoads = kBn * 128 / (kWaves * 1024);
     static_assert(kALoads * kWaves * 1024 == kBm * 128 && kWLoads * kWaves * 1024 == kBn * 128, "whole loads");
@@ -91,266 +102,390 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     auto weight_row = [&](int r) {
         if constexpr (!kGated)
             return r;
-        constexpr int kHalf = kTn * 8;   // a wave's rows: half gate, half up
+        constexpr int kHalf = kTn * 16;   // a wave's rows: half gate, half up
         const int q = r % (2 * kHalf), col = r / (2 * kHalf) * kHalf + q % kHalf;
         return q < kHalf ? col : p.I + col;
     };
-    const int swave = __builtin_amdgcn_readfirstlane(wave);
     const int w_lane = lane / 8 * (int)p.ldw, a_lane = lane / 8 * (int)p.lda;
-    auto issue = [&](int step, int b) {
-        lds_u8 *to = smem + b * T::kStage;
-        auto chunk = [&](int eight) { return step * 128 + 16 * swizzle(eight * 8 + lane / 8, lane % 8); };
-#pragma unroll
-        for (int i = 0; i < kWLoads; ++i) {
-            const int eight = swave * kWLoads + i, c = chunk(eight);
-            load_lds16(w_rsrc, to + eight * 1024, c < K ? w_lane + c + weight_row(eight * 8) * (int)p.ldw : kPast);
-        }
-#pragma unroll
-        for (int i = 0; i < kALoads; ++i) {
-            const int eight = swave * kALoads + i, c = chunk(eight);
-            load_lds16(a_rsrc, to + kBn * 128 + eight * 1024, c < K ? a_lane + c + eight * 8 * (int)p.lda : kPast);
-        }
+    // Load n of a wave's share of a step, into its buffer.  Weight rows are dealt to the waves so
+    // that the first half of a wave's loads are of the first half of every wave's tiles.
+    constexpr int kEarly = kWLoads / 2, kLate = kWLoads - kEarly;
+    static_assert(kWLoads % 2 == 0 && kTn % 2 == 0, "halves");
+    auto issue = [&](int step, bool weights, int n) {
+        constexpr int kRows = kTn * 32, kEights = kRows / 16;     // of a wave's tiles; in a half of them
+        const int w8 = wave * kEarly + n % kEarly;                // of the early or the late eights
+        const int eight = weights ? w8 / kEights * (2 * kEights) + w8 % kEights + n / kEarly * kEights
+                                  : wave * kALoads + n;
+        const int c = step * 128 + 16 * swizzle(eight * 8 + lane / 8, lane % 8);
+        lds_u8 *to = smem + (step & 1) * T::kStage + eight * 1024;
+        if (weights)
+            load_lds16(w_rsrc, to, c < K ? w_lane + c + weight_row(eight * 8) * (int)p.ldw : kPast);
+        else
+            load_lds16(a_rsrc, to + kBn * 128, c < K ? a_lane + c + eight * 8 * (int)p.lda : kPast);
     };
+    // What is read first of a step: activations and the early weights.
+    constexpr int kFirst = kALoads + kEarly, kAll = kFirst + kLate;
+    auto issue_first = [&](int step, int n) { issue(step, n >= kALoads, n < kALoads ? n : n - kALoads); };
+    auto issue_late = [&](int step, int n) { issue(step, true, kEarly + n); };
 
-    // Scales of steps first .. first + 63 to LDS.
-    const uint8_t *sa_tile = p.sa + m0 * p.ldsa;
+    // Scales of steps first .. first + 63 to LDS, a row of the activations in each lane; those of
+    // the weights through a register.
     const int far = kGated ? p.I / 128 : 1, block_rows = (p.N + 127) / 128;
+    uint32_t sw_in = 0;
     auto load_scales = [&](int first) {
-        for (int i = t; i < kBm * 16; i += kWaves * kWave) {
-            const int r = min(i / 16, rows - 1), b = first + i % 16 * 4;
-            if (b < steps)
-                *(__attribute__((address_space(3))) uint32_t *)(scales + i / 16 * T::kScalePitch + i % 16 * 4) =
-                    *reinterpret_cast<const uint32_t *>(sa_tile + (uint32_t)(r * (int)p.ldsa + b));
-        }
-        for (int i = t; i < 2 * 64; i += kWaves * kWave) {
-            const int r = min(n0 / 128 + i / 64 * far, block_rows - 1), b = min(first + i % 64, steps - 1);
-            scales[(kBm + i / 64) * T::kScalePitch + i % 64] = p.sw[(int64_t)r * steps + b];
+        constexpr int kParts = kBm / kWave, kEach = 16 * kParts / kWaves;
+        static_assert(kEach * kWaves == 16 * kParts, "whole loads");
+        const int sw_row = min(n0 / 128 + t / 64 % 2 * far, block_rows - 1);
+        sw_in = p.sw[(int64_t)sw_row * steps + min(first + t % 64, steps - 1)];
+#pragma unroll
+        for (int n = 0; n < kEach; ++n) {
+            const int e = n * kWaves + wave, part = e % kParts, four = e / kParts;
+            if (first + 4 * four < steps)
+                load_lds4(sa_rsrc, scales + e % kParts * 256 + four * kBm * 4,
+                          min(part * kWave + lane, rows - 1) * (int)p.ldsa + first + 4 * four);
         }
     };
-    load_scales(0);
+    auto keep_scales = [&]() {
+        if (t < 128)
+            scales[T::kRowScales + t] = (uint8_t)sw_in;
+    };
 
-    issue(0, 0);
-    issue(1, 1);
-
-    v4f acc[kTn][kTm];
+    // A step has 2 kTn units: the weight tiles in order, two k-halves each.  Two barriers cut it
+    // in halves.  Past the first every wave holds all activations and the first half of the
+    // weight tiles, past the second the rest: so each part of a buffer is filled for the step
+    // after the next as soon as that, and every load has one and a half steps to land.  (With
+    // one barrier and one step it takes 792 us for a feed-forward block of 8192 rows, H 3840,
+    // I 10240.)  Loads go out one or two at a time between products.
+    constexpr int kUnits = 2 * kTn;
+    auto first_loads = [&]() {
+        load_scales(0);
 #pragma unroll
-    for (int i = 0; i < kTn; ++i)
+        for (int n = 0; n < kFirst; ++n)
+            issue_first(0, n);
 #pragma unroll
-        for (int j = 0; j < kTm; ++j)
-            acc[i][j] = v4f{};
+        for (int n = 0; n < kLate; ++n)
+            issue_late(0, n);
+#pragma unroll
+        for (int n = 0; n < kFirst; ++n)
+            issue_first(1, n);
+    };
 
-    // Fragment addresses: the swizzle depends on the row's low four bits only, so a wave's
-    // tiles differ by constants.
-    const int near = 16 * swizzle(l16, quarter), half = 16 * swizzle(l16, quarter + 4);
-    const int w_at = (wn * kTn * 16 + l16) * 128, a_at = kBn * 128 + (wm * kTm * 16 + l16) * 128;
-    auto fragment = [&](const lds_u8 *row) {
-        const u32x4 x = *(lds_u32x4 *)(row + near), y = *(lds_u32x4 *)(row + half);
+    v16f acc[kTn][kTm];
+
+    // A lane's fragment of k-half s: 32 bytes from 64 s + 32 half on, two slots.  The swizzle
+    // depends on the row's low four bits only, so a wave's tiles differ by constants.
+    const int slot0 = 16 * swizzle(l32, 2 * half), slot1 = 16 * swizzle(l32, 2 * half + 1);
+    const int w_at = (wn * kTn * 32 + l32) * 128, a_at = kBn * 128 + (wm * kTm * 32 + l32) * 128;
+    auto fragment = [&](const lds_u8 *row, int s) {   // chunk + 4 is slot ^ 64
+        const u32x4 x = *(lds_u32x4 *)(row + (slot0 ^ (64 * s))), y = *(lds_u32x4 *)(row + (slot1 ^ (64 * s)));
         return v8i{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
     };
     // The block row of a wave's first weight tiles (all of them, unless gated).
-    const lds_u8 *sa_at = scales + (wm * kTm * 16 + l16) * T::kScalePitch;
-    const lds_u8 *sw_at = scales + (kBm + (kGated ? 0 : wn * kTn * 16 / 128)) * T::kScalePitch;
-    uint32_t sa[kTm], sw[2];
+    const lds_u8 *sa_at = scales + (wm * kTm * 32 + l32) * 4;
+    const lds_u8 *sw_at = scales + T::kRowScales + (kGated ? 0 : wn * kTn * 32 / 128) * T::kScaleSteps;
+    uint32_t sa[kTm], sw[2], sa_next[kTm], sw_next[2];
     auto read_scales = [&](int kt) {
         const int b = kt % T::kScaleSteps;
-        sw[0] = sw_at[b];
+        sw_next[0] = sw_at[b];
         if constexpr (kGated)
-            sw[1] = sw_at[T::kScalePitch + b];
+            sw_next[1] = sw_at[T::kScaleSteps + b];
 #pragma unroll
         for (int j = 0; j < kTm; ++j)
-            sa[j] = sa_at[j * 16 * T::kScalePitch + b];
+            sa_next[j] = sa_at[j * 32 * 4 + b / 4 * kBm * 4 + b % 4];
+    };
+    auto take_scales = [&]() {
+        sw[0] = sw_next[0];
+        if constexpr (kGated)
+            sw[1] = sw_next[1];
+#pragma unroll
+        for (int j = 0; j < kTm; ++j)
+            sa[j] = sa_next[j];
     };
 
-    // One step: a weight tile's fragment is read while the tile before it is multiplied.  The
-    // barrier stands before the last tile's products: under them this buffer is filled
-    // anew, and the other one's first fragments take the place of those just used.
-    v8i a[kTm], w[2];
-    auto read_activation = [&](const lds_u8 *stage, int j) { a[j] = fragment(stage + a_at + j * 2048); };
-    auto multiply = [&](int i, int j) {
-        acc[i][j] = mfma_e4m3<0, 0>(w[i & 1], a[j], acc[i][j], sw[kGated && i >= kTn / 2], sa[j]);
+    // A unit's weight fragment is read while the unit before it is multiplied; the barriers stand
+    // before the last unit's products of either half, under which the next half's first
+    // fragments are read.
+    v8i a[2][kTm], w[2];
+    auto multiply = [&](int u, int j) {
+        const int i = u / 2, s = u % 2;
+        acc[i][j] = mfma_e4m3(w[u & 1], a[s][j], acc[i][j], sw[kGated && i >= kTn / 2], sa[j]);
     };
-    static_assert(kTn % 2 == 0, "two fragments alternate across steps");
-    auto all_but_last = [&](const lds_u8 *stage) {
+    auto all_but_last = [&](int kt) {
+        const lds_u8 *stage = smem + (kt & 1) * T::kStage;
 #pragma unroll
-        for (int i = 0; i + 1 < kTn; ++i) {
-            w[(i + 1) & 1] = fragment(stage + w_at + (i + 1) * 2048);
+        for (int u = 0; u + 1 < kUnits; ++u) {
+            if (u == kTn - 1) {
+                wait_reads_and_loads<kAll>();
+                __builtin_amdgcn_s_barrier();
+            }
+            w[(u + 1) & 1] = fragment(stage + w_at + (u + 1) / 2 * 4096, (u + 1) % 2);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < kTm; ++j)
-                multiply(i, j);
+                multiply(u, j);
+            if (u < kLate)
+                issue_late(kt + 1, u);
+            if (u >= kTn - 1)
+#pragma unroll
+                for (int n = (u - kTn + 1) * kFirst / kTn; n < (u - kTn + 2) * kFirst / kTn; ++n)
+                    issue_first(kt + 2, n);
+            if (u == kUnits - 2)
+                read_scales(kt + 1);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    static_assert(kLate <= kTn - 1, "loads of the first half");
 
-    wait_vmcnt0();
-    __syncthreads();
-    w[0] = fragment(smem + w_at);
+    // Results.  A lane has row 32 j + l32 of the wave's and, in registers 4 q .. 4 q + 3 of tile i,
+    // its columns from 32 i + 8 q + 4 half on.  The two lanes of a row exchange halves, so that
+    // each has 16 bytes that lie together.
+    // Columns 32 i + 16 h .. of a tile's codes, h = half.
+    auto codes16 = [&](const float(&v)[16], float inv) {
+        uint32_t c[4];
 #pragma unroll
-    for (int j = 0; j < kTm; ++j)
-        read_activation(smem, j);
-    for (int first = 0;; first += T::kScaleSteps) {
-        const int end = min(first + T::kScaleSteps, steps - 1);   // of the steps that have a successor here
-        read_scales(first);
-        // One straight run: a load past the last step's columns reads zeros.
-        for (int kt = first; kt < end; ++kt) {
-            all_but_last(smem + (kt & 1) * T::kStage);
-            wait_lgkm0();
-            wait_vmcnt0();
-            __builtin_amdgcn_s_barrier();
-            const lds_u8 *other = smem + (~kt & 1) * T::kStage;
-            w[0] = fragment(other + w_at);
-            issue(kt + 2, kt & 1);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int q = 0; q < 4; ++q)
+            c[q] = pack_e4m3x4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+        swap_halves(c[0], c[2]);
+        swap_halves(c[1], c[3]);
+        return u32x4{c[0], c[2], c[1], c[3]};
+    };
+    // Columns 32 i + 16 g + 8 half .. of a tile in bf16, g = 0 and 1.
+    auto bf16x8 = [&](const float *v) {   // registers 8 g .. 8 g + 7
+        uint32_t x0 = pack_bf16x2(v[0], v[1]), x1 = pack_bf16x2(v[2], v[3]);
+        uint32_t y0 = pack_bf16x2(v[4], v[5]), y1 = pack_bf16x2(v[6], v[7]);
+        swap_halves(x0, y0);
+        swap_halves(x1, y1);
+        return u32x4{x0, x1, y0, y1};
+    };
+    // The reverse, to fp32.
+    auto floats8 = [&](u32x4 x, float *v) {
+        uint32_t d[4] = {x[0], x[1], x[2], x[3]};
+        swap_halves(d[0], d[2]);
+        swap_halves(d[1], d[3]);
 #pragma unroll
-            for (int j = 0; j < kTm; ++j) {
-                multiply(kTn - 1, j);
-                read_activation(other, j);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            read_scales(kt + 1);
-        }
-        if (end < first + T::kScaleSteps)
-            break;
-        __syncthreads();
-        load_scales(end);
-        __syncthreads();
-    }
-    all_but_last(smem + (~steps & 1) * T::kStage);
-#pragma unroll
-    for (int j = 0; j < kTm; ++j)
-        multiply(kTn - 1, j);
-    wait_vmcnt0();
-    __syncthreads();
-
-    const int64_t mw = m0 + wm * kTm * 16;   // the wave's rows and columns
-    // Write the wave's staged bf16 tile: kTm * 16 rows of `cols` columns to dst at column n.
-    lds_u8 *mine = smem + wave * kTm * 16 * T::kPitch;
-    auto write_bf16 = [&](uint16_t *dst, int64_t ld, int n, int N, int cols_, int from) {
-        const int chunks = cols_ / 8, rows_each = kWave / chunks;
-        for (int r = lane / chunks; r < kTm * 16; r += rows_each) {
-            const int c = lane % chunks;
-            const u32x4 v = *(lds_u32x4 *)(mine + r * T::kPitch + from + 16 * c);
-            if (mw + r < p.M && n + 8 * c < N)
-                *reinterpret_cast<u32x4 *>(dst + (mw + r) * ld + n + 8 * c) = v;
+        for (int r = 0; r < 4; ++r) {
+            v[r] = r % 2 ? __uint_as_float(d[r / 2] & 0xffff0000u) : bf16_to_f32(d[r / 2] & 0xffffu);
+            v[4 + r] = r % 2 ? __uint_as_float(d[2 + r / 2] & 0xffff0000u) : bf16_to_f32(d[2 + r / 2] & 0xffffu);
         }
     };
-    auto stage_bf16 = [&](int i, int j, const v4f &v) {
-        const u32x2 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        *(__attribute__((address_space(3))) u32x2 *)(mine + (j * 16 + l16) * T::kPitch + (i * 16 + 4 * quarter) * 2) = q;
-    };
-    // Quantise blocks of 128 columns, each held by kPer waves side by side with kTiles tiles
-    // each, and write block i's codes at column n + 128 i, its scales at scale[.. + i].
-    auto quantise = [&](const auto &v, auto tiles_c, int n, uint8_t *dst, int64_t ld, uint8_t *scale) {
-        constexpr int kTiles = decltype(tiles_c)::value, kPer = 8 / kTiles;
-        static_assert(kPer * kTiles == 8 && T::kWn % kPer == 0, "whole blocks");
-        constexpr int kBlocks = T::kWn / kPer;
-        const int block = wn / kPer, col = wn % kPer * kTiles * 16;
-        __syncthreads();  // what the stages or the last blocks held is done with
-#pragma unroll
-        for (int j = 0; j < kTm; ++j) {
-            float a = 0.f;
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a = fmaxf(a, fabsf(v[i][j][r]));
-            a = fmaxf(a, __shfl_xor(a, 16));
-            a = fmaxf(a, __shfl_xor(a, 32));
-            if (quarter == 0)
-                red[(wn * T::kWm + wm) * kTm * 16 + j * 16 + l16] = a;
-        }
-        __syncthreads();
-        lds_u8 *to = smem + block * kBm * T::kCodePitch;
-#pragma unroll
-        for (int j = 0; j < kTm; ++j) {
-            float a = 0.f;
+    // Quantise a row's kTiles tiles, the largest of which is a, with the waves that hold the other
+    // columns of its block of 128: the scale, and the codes of tile(i) at column n + 32 i.
+    auto quantise = [&](auto tiles, float a, auto tile, int m, int n, uint8_t *dst, uint8_t *scale) {
+        constexpr int kTiles = decltype(tiles)::value, kPer = 4 / kTiles;   // waves of a block
+        static_assert(kPer * kTiles == 4 && T::kWn % kPer == 0, "whole blocks");
+        a = fmaxf(a, __shfl_xor(a, 32));
+        if constexpr (kPer > 1) {
+            if (half == 0)
+                red[wave * 32 + l32] = a;
+            lds_barrier();
 #pragma unroll
             for (int o = 0; o < kPer; ++o)
-                a = fmaxf(a, red[((block * kPer + o) * T::kWm + wm) * kTm * 16 + j * 16 + l16]);
-            const uint32_t s = e8m0_of(a);
-            const float inv = e8m0_inverse(s);
-            const int row = wm * kTm * 16 + j * 16 + l16;
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-                *(__attribute__((address_space(3))) uint32_t *)(to + row * T::kCodePitch + col + i * 16 + 4 * quarter) =
-                    pack_e4m3x4(v[i][j][0] * inv, v[i][j][1] * inv, v[i][j][2] * inv, v[i][j][3] * inv);
-            if (wn % kPer == 0 && quarter == 0 && row < rows && n + 128 * block < p.I)
-                scale[(m0 + row) * p.ldsq + block] = (uint8_t)s;
+                a = fmaxf(a, red[((wn / kPer * kPer + o) * T::kWm + wm) * 32 + l32]);
+            lds_barrier();   // read before the next row's is written
         }
-        __syncthreads();
-        for (int i = t; i < kBlocks * kBm * 8; i += kWaves * kWave) {
-            const int row = i / 8 % kBm, b = i / 8 / kBm;
-            if (row < rows && n + 128 * b < p.I)
-                *reinterpret_cast<u32x4 *>(dst + (m0 + row) * ld + n + 128 * b + i % 8 * 16) =
-                    *(lds_u32x4 *)(smem + (b * kBm + row) * T::kCodePitch + i % 8 * 16);
+        const uint32_t s = e8m0_of(a);
+        const float inv = e8m0_inverse(s);
+        const bool inside = m < rows && n < p.I;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            float v[16];
+            tile(i, v);
+            const u32x4 c = codes16(v, inv);
+            if (inside)
+                *reinterpret_cast<u32x4 *>(dst + 32 * i + 16 * half) = c;
+        }
+        if (wn % kPer == 0 && half == 0 && inside)
+            *scale = (uint8_t)s;
+    };
+    // bf16 rows go through the wave's part of the stages, whose 16-byte slots are XORed with the
+    // row, so that a store writes four whole rows of the wave's columns.
+    constexpr int kRowBytes = kTn * 64, kSlots = kRowBytes / 16;
+    lds_u8 *mine = smem + wave * kTm * 32 * kRowBytes;
+    auto stage_bf16 = [&](int i, int j, int g, const float *v) {
+        const int r = j * 32 + l32, slot = 4 * i + 2 * g + half;
+        *(__attribute__((address_space(3))) u32x4 *)(mine + r * kRowBytes + 16 * (slot ^ (r % kSlots))) = bf16x8(v);
+    };
+    // Slots `from` .. `from` + `width` - 1 of the staged rows to dst, column n.
+    auto write_bf16 = [&](uint16_t *dst, int64_t ld, int n, int N, auto width, int from) {
+        constexpr int kWidth = decltype(width)::value, kRows = kWave / kWidth;
+#pragma unroll
+        for (int r0 = 0; r0 < kTm * 32; r0 += kRows) {
+            const int r = r0 + lane / kWidth, c = lane % kWidth, m = wm * kTm * 32 + r;
+            const u32x4 v = *(lds_u32x4 *)(mine + r * kRowBytes + 16 * ((from + c) ^ (r % kSlots)));
+            if (m < rows && n + 8 * c < N)
+                *reinterpret_cast<u32x4 *>(dst + (m0 + m) * ld + n + 8 * c) = v;
         }
     };
-
-    if constexpr (kKind == Fp8Result::kBf16) {
-        const int nw = n0 + wn * kTn * 16;
-#pragma unroll
-        for (int i = 0; i < kTn; ++i) {
-            float b[4] = {0.f, 0.f, 0.f, 0.f};
-            if (p.bias)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    b[r] = bf16_to_f32(p.bias[min(nw + i * 16 + 4 * quarter + r, p.N - 1)]);
-#pragma unroll
-            for (int j = 0; j < kTm; ++j) {
-                v4f v = acc[i][j];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    v[r] += b[r];
-                stage_bf16(i, j, v);
-            }
-        }
-        write_bf16(p.out, p.ldo, nw, p.N, kTn * 16, 0);
-    } else if constexpr (kGated) {
-        constexpr int kHalf = kTn / 2;
-        const int col = wn * kHalf * 16;
-        if (p.gate_up) {
+    auto write_tile = [&]() {
+        const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
+        if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
 #pragma unroll
             for (int i = 0; i < kTn; ++i)
 #pragma unroll
-                for (int j = 0; j < kTm; ++j)
-                    stage_bf16(i, j, acc[i][j]);
-            write_bf16(p.gate_up, p.ldg, n0 + col, p.I, kHalf * 16, 0);
-            write_bf16(p.gate_up + p.I, p.ldg, n0 + col, p.I, kHalf * 16, kHalf * 32);
+                for (int g = 0; g < 2; ++g) {
+                    float b[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        b[r] = 0.f;
+                    if (kKind == Fp8Result::kBf16 && p.bias)
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            b[r] = bf16_to_f32(
+                                p.bias[min(nw + i * 32 + 16 * g + r / 4 * 8 + 4 * half + r % 4, p.N - 1)]);
+#pragma unroll
+                    for (int j = 0; j < kTm; ++j) {
+                        float v[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            v[r] = acc[i][j][8 * g + r] + b[r];
+                        stage_bf16(i, j, g, v);
+                    }
+                }
+            if constexpr (kKind == Fp8Result::kBf16) {
+                write_bf16(p.out, p.ldo, nw, p.N, std::integral_constant<int, kSlots>{}, 0);
+            } else {
+                const std::integral_constant<int, kSlots / 2> width;
+                write_bf16(p.gate_up, p.ldg, nw, p.I, width, 0);
+                write_bf16(p.gate_up + p.I, p.ldg, nw, p.I, width, kSlots / 2);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i)
+        for (int j = 0; j < (kKind == Fp8Result::kBf16 ? 0 : kTm); ++j) {
+            const int m = wm * kTm * 32 + j * 32 + l32;
+            const int64_t row = m0 + m;
+            if constexpr (kGated) {
+                constexpr int kHalf = kTn / 2;
+                float h[kHalf][16], largest = 0.f;
 #pragma unroll
-            for (int j = 0; j < kTm; ++j)
+                for (int i = 0; i < kHalf; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[i][j][r] = gated(acc[i][j][r], acc[i + kHalf][j][r]);
-        quantise(acc, std::integral_constant<int, kHalf>{}, n0, p.q, p.I, p.sq + n0 / 128);
-    } else {
-        auto gradient = [&](int i, int j, v4f &dg) {   // acc[i][j] becomes du
-            const int64_t m = m0 + min(wm * kTm * 16 + j * 16 + l16, rows - 1);
-            const int n = min(n0 + wn * kTn * 16 + i * 16, p.I - 16) + 4 * quarter;
-            const u32x2 gv = *reinterpret_cast<const u32x2 *>(p.gate_up + m * p.ldg + n);
-            const u32x2 uv = *reinterpret_cast<const u32x2 *>(p.gate_up + m * p.ldg + p.I + n);
+                    for (int r = 0; r < 16; ++r) {
+                        h[i][r] = gated(acc[i][j][r], acc[i + kHalf][j][r]);
+                        largest = fmaxf(largest, fabsf(h[i][r]));
+                    }
+                quantise(std::integral_constant<int, kHalf>{}, largest,
+                         [&](int i, float *v) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float g = bf16_to_f32(r % 2 ? gv[r / 2] >> 16 : gv[r / 2] & 0xffffu);
-                const float u = bf16_to_f32(r % 2 ? uv[r / 2] >> 16 : uv[r / 2] & 0xffffu);
-                const float2 d = gated_gradient(acc[i][j][r], g, u);
-                dg[r] = d.x, acc[i][j][r] = d.y;
+                             for (int r = 0; r < 16; ++r)
+                                 v[r] = h[i][r];
+                         },
+                         m, nw, p.q + row * p.I + nw, p.sq + row * p.ldsq + nw / 128);
+            } else {
+                // dg stays in registers, du waits in the wave's part of the stages.
+                const uint16_t *gu = p.gate_up + (m0 + min(m, rows - 1)) * p.ldg +
+                                     (nw < p.I ? nw : p.I - kTn * 32) + 8 * half;
+                lds_u8 *wait = smem + (wave * kTn * 4 * kWave + lane) * 16;
+                float dg[kTn][16], largest_g = 0.f, largest_u = 0.f;
+#pragma unroll
+                for (int i = 0; i < kTn; ++i) {
+#pragma unroll
+                    for (int g2 = 0; g2 < 2; ++g2) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        float g[8], u[8];
+                        floats8(*reinterpret_cast<const u32x4 *>(gu + i * 32 + 16 * g2), g);
+                        floats8(*reinterpret_cast<const u32x4 *>(gu + p.I + i * 32 + 16 * g2), u);
+                        v4f du[2];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float2 d = gated_gradient(acc[i][j][8 * g2 + r], g[r], u[r]);
+                            dg[i][8 * g2 + r] = d.x, du[r / 4][r % 4] = d.y;
+                            largest_g = fmaxf(largest_g, fabsf(d.x)), largest_u = fmaxf(largest_u, fabsf(d.y));
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + 2 * g2 + q) * kWave * 16) = du[q];
+                    }
+                }
+                uint8_t *to = p.q + row * 2 * p.I + nw, *scale = p.sq + row * p.ldsq + nw / 128;
+                const std::integral_constant<int, kTn> tiles_c;
+                quantise(tiles_c, largest_g,
+                         [&](int i, float *v) {
+#pragma unroll
+                             for (int r = 0; r < 16; ++r)
+                                 v[r] = dg[i][r];
+                         },
+                         m, nw, to, scale);
+                quantise(tiles_c, largest_u,
+                         [&](int i, float *v) {
+#pragma unroll
+                             for (int q = 0; q < 4; ++q) {
+                                 const v4f d = *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + q) * kWave * 16);
+#pragma unroll
+                                 for (int r = 0; r < 4; ++r)
+                                     v[4 * q + r] = d[r];
+                             }
+                         },
+                         m, nw, to + p.I, scale + p.I / 128);
             }
-        };
-        v4f dg[kTn][kTm];
-#pragma unroll
-        for (int i = 0; i < kTn; ++i) {
-#pragma unroll
-            for (int j = 0; j < kTm; ++j)
-                gradient(i, j, dg[i][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        quantise(dg, std::integral_constant<int, kTn>{}, n0, p.q, 2 * (int64_t)p.I, p.sq + n0 / 128);
-        quantise(acc, std::integral_constant<int, kTn>{}, n0, p.q + p.I, 2 * (int64_t)p.I,
-                 p.sq + (p.I + n0) / 128);
-    }
+    };
+
+    static_assert(kKind != Fp8Result::kGrad || kWaves * kTn * 4 * kWave * 16 <= 2 * T::kStage, "du fits the stages");
+    start_tile(blockIdx.x);
+    first_loads();
+#pragma unroll
+        for (int i = 0; i < kTn; ++i)
+#pragma unroll
+            for (int j = 0; j < kTm; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[i][j][r] = 0.f;
+        keep_scales();
+        wait_vmcnt0();
+        lds_barrier();
+        w[0] = fragment(smem + w_at, 0);
+#pragma unroll
+        for (int j = 0; j < kTm; ++j)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                a[s][j] = fragment(smem + a_at + j * 4096, s);
+        for (int first = 0;; first += T::kScaleSteps) {
+            const int end = __builtin_amdgcn_readfirstlane(min(first + T::kScaleSteps, steps - 1));
+            read_scales(first);
+            take_scales();
+            // One straight run: a load past the last step's columns reads zeros.
+            for (int kt = first; kt < end; ++kt) {
+                all_but_last(kt);
+                wait_reads_and_loads<kAll>();
+                __builtin_amdgcn_s_barrier();
+                const lds_u8 *other = smem + (~kt & 1) * T::kStage;
+                w[0] = fragment(other + w_at, 0);
+#pragma unroll
+                for (int j = 0; j < kTm; ++j)
+                    a[0][j] = fragment(other + a_at + j * 4096, 0);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < kTm; ++j) {
+                    multiply(kUnits - 1, j);
+                    a[1][j] = fragment(other + a_at + j * 4096, 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                take_scales();
+            }
+            if (end < first + T::kScaleSteps)
+                break;
+            lds_barrier();
+            load_scales(end);
+            keep_scales();
+            wait_vmcnt0();
+            lds_barrier();
+        }
+        all_but_last(steps - 1);
+#pragma unroll
+        for (int j = 0; j < kTm; ++j)
+            multiply(kUnits - 1, j);
+        // All products are done here: left to itself the compiler takes some of the last step's, and
+        // the fragments that they need, into the writing of the results.
+#pragma unroll
+        for (int i = 0; i < kTn; ++i)
+#pragma unroll
+            for (int j = 0; j < kTm; ++j)
+                asm volatile("" : "+v"(acc[i][j]));
+        wait_vmcnt0();   // loads past the last step
+        lds_barrier();
+
+        write_tile();
 }
 
 template <class T, Fp8Result kKind>
@@ -362,17 +497,17 @@ int launch_tile(const Fp8Product &p, void *stream)
     static_assert(T::kLds <= 160 * 1024, "LDS");
     if (attr != hipSuccess)
         return (int)attr;
-    const int tiles_m = (int)((p.M + T::kBm - 1) / T::kBm);
+    const int64_t tiles_m = (p.M + T::kBm - 1) / T::kBm;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int width = kKind == Fp8Result::kGated ? T::kBn / 2 : T::kBn;
-    const int tiles_n = (cols + width - 1) / width;
-    hipLaunchKernelGGL(kern, dim3((unsigned)tiles_m * (unsigned)tiles_n), dim3(T::kWaves * kWave), T::kLds,
-                       reinterpret_cast<hipStream_t>(stream), p, tiles_m, tiles_n);
+    const int64_t tiles = tiles_m * ((cols + width - 1) / width);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(T::kWaves * kWave), T::kLds,
+                       reinterpret_cast<hipStream_t>(stream), p, (int)tiles_m, (int)tiles);
     return (int)hipGetLastError();
 }
 
-using Large = Tile<2, 4, 8, 4>;   // 256 weight rows x 256 activation rows
-using Small = Tile<2, 4, 4, 2>;   // 128 x 128
+using Large = Tile<2, 4, 4, 2>;   // 256 weight rows x 256 activation rows
+using Small = Tile<2, 4, 2, 1>;   // 128 x 128
 
 }  // namespace
 
@@ -384,7 +519,7 @@ int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream)
     case Fp8Result::kGated:
         return launch_tile<Large, Fp8Result::kGated>(p, stream);
     default:
-        return launch_tile<Small, Fp8Result::kGrad>(p, stream);
+        return launch_tile<Large, Fp8Result::kGrad>(p, stream);
     }
 }
 
