@@ -761,6 +761,8 @@ class Fp8Weights:
     def __init__(self, codes, scales):
         _matrix(codes, "codes", (E4M3,))
         self.N, self.K = codes.shape
+        if not self.N or not self.K or self.N % 16 or self.K % 16:
+            raise ValueError("codes has shape %s: expected multiples of 16" % (tuple(codes.shape),))
         _dense(scales, "scales", E8M0, (fp8_blocks(self.N), fp8_blocks(self.K)))
         _same_device(codes, ("scales", scales))
         self.tensors, self._at = _held((codes, scales))
@@ -851,8 +853,9 @@ class Fp8Ffn(_Fp8Pair):
     def __init__(self, w1, s1, w2, s2):
         rows, self.H = _fp8_matrix(w1, "w1")
         self.I = rows // 2
-        if rows % 256:
-            raise ValueError("w1 has %d rows: expected 2I, I a multiple of 128" % rows)
+        if rows % 256 or self.H % 16:
+            raise ValueError("w1 has shape (%d, %d): expected 2I, I a multiple of 128, by H, a multiple of 16"
+                             % (rows, self.H))
         self._keep(w1, s1, w2, s2, (rows, self.H), (self.H, self.I))
 
     def transposed(self):
@@ -866,8 +869,8 @@ class Fp8FfnTransposed(_Fp8Pair):
 
     def __init__(self, w1t, s1t, w2t, s2t):
         self.I, self.H = _fp8_matrix(w2t, "w2t")
-        if self.I % 128:
-            raise ValueError("w2t has %d rows: expected a multiple of 128" % self.I)
+        if self.I % 128 or self.H % 16:
+            raise ValueError("w2t has shape (%d, %d): expected multiples of 128 and of 16" % (self.I, self.H))
         self._keep(w1t, s1t, w2t, s2t, (self.H, 2 * self.I), (self.I, self.H))
 
 

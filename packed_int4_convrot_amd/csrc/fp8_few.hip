@@ -98,7 +98,10 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
 
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
     const int l16 = lane % 16, quarter = lane / 16;
-    const int M = (int)p.M, K = p.K, steps = (K + 127) / 128;
+    // Rows of this workgroup: one of the runs of 16 kMt.
+    const int64_t m0 = (int64_t)blockIdx.y * kMt * 16;
+    const int M = (int)min((int64_t)kMt * 16, p.M - m0), K = p.K, steps = (K + 127) / 128;
+    const uint8_t *rows_a = p.a + m0 * p.lda, *rows_sa = p.sa + m0 * p.ldsa;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int c0 = blockIdx.x * per, c1 = min(c0 + per, cols);
     lds_u8 *ring = smem + wave * kRing * kUnit;
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
     __amdgpu_buffer_rsrc_t w_rsrc, a_rsrc;
     int w_row[kT][2], a_row[kRaw ? 1 : kMt][2];          // byte offsets of a lane's rows
     if constexpr (!kRaw) {
-        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, kRange, 0x00020000);
+        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)rows_a, (short)0, kRange, 0x00020000);
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
             a_row[j][0] = min(j * 16 + eight, M - 1) * (int)p.lda + at0;
@@ -198,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
 #pragma unroll
         for (int r = 0; r < kRowScaleLoads; ++r) {
             const int i = min(r * kThreads + t, sa_count - 1), m = sa_pitch == 4 ? i : by_dwords(i);
-            sa_in[r] = *reinterpret_cast<const uint32_t *>(p.sa + m * p.ldsa + (i * 4 - m * sa_pitch));
+            sa_in[r] = *reinterpret_cast<const uint32_t *>(rows_sa + m * p.ldsa + (i * 4 - m * sa_pitch));
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -333,21 +336,22 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
             const int m = e / kPass, r = e % kPass, c = first + r;
             if (c >= c1)
                 continue;
+            const int64_t row = m0 + m;
             if constexpr (kKind == Fp8Result::kBf16) {
                 const float s = total(m, r) + (p.bias ? bf16_to_f32(p.bias[c]) : 0.f);
-                p.out[m * p.ldo + c] = f32_to_bf16(s);
+                p.out[row * p.ldo + c] = f32_to_bf16(s);
             } else if constexpr (kGated) {
                 const float g = total(m, r), u = total(m, kPass + r);
                 if (p.gate_up) {
-                    p.gate_up[m * p.ldg + c] = f32_to_bf16(g);
-                    p.gate_up[m * p.ldg + p.I + c] = f32_to_bf16(u);
+                    p.gate_up[row * p.ldg + c] = f32_to_bf16(g);
+                    p.gate_up[row * p.ldg + p.I + c] = f32_to_bf16(u);
                 }
-                sums[(int64_t)m * p.I + c] = gated(g, u);
+                sums[row * p.I + c] = gated(g, u);
             } else {
-                const float g = bf16_to_f32(p.gate_up[m * p.ldg + c]), u = bf16_to_f32(p.gate_up[m * p.ldg + p.I + c]);
+                const float g = bf16_to_f32(p.gate_up[row * p.ldg + c]), u = bf16_to_f32(p.gate_up[row * p.ldg + p.I + c]);
                 const float2 d = gated_gradient(total(m, r), g, u);
-                sums[(int64_t)m * 2 * p.I + c] = d.x;
-                sums[(int64_t)m * 2 * p.I + p.I + c] = d.y;
+                sums[row * 2 * p.I + c] = d.x;
+                sums[row * 2 * p.I + p.I + c] = d.y;
             }
         }
     }
@@ -358,7 +362,7 @@ int launch_one(const Fp8Product &p, const void *x, int64_t ldx, float *sums, int
                void *stream)
 {
     auto kern = fp8_few_kernel<kSource, kKind, kMt, kT>;
-    const size_t steps = fp8_blocks(p.K), M = p.M;
+    const size_t steps = fp8_blocks(p.K), M = p.M < kMt * 16 ? p.M : kMt * 16;
     const size_t lds = kRings + kScaleLoads * kThreads + (M * ((steps + 3) / 4 * 4) + 15) / 16 * 16 +
                        (kSource == Source::kCodes ? 0 : M * (steps * 128 + 16));
     constexpr int kMostLds = 160 * 1024;
@@ -366,7 +370,7 @@ int launch_one(const Fp8Product &p, const void *x, int64_t ldx, float *sums, int
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
     if (attr != hipSuccess)
         return (int)attr;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, reinterpret_cast<hipStream_t>(stream), p, x,
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid, (unsigned)((p.M + kMt * 16 - 1) / (kMt * 16))), dim3(kThreads), lds, reinterpret_cast<hipStream_t>(stream), p, x,
                        ldx, sums, per, passes, divide_by((int64_t)steps), divide_by((int64_t)(steps + 3) / 4));
     return (int)hipGetLastError();
 }

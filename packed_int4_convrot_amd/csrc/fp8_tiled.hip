@@ -223,8 +223,10 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
 #pragma unroll
             for (int j = 0; j < kTm; ++j)
                 multiply(u, j);
-            if (u < kLate)
-                issue_late(kt + 1, u);
+            if (u < kTn - 1)
+#pragma unroll
+                for (int n = u * kLate / (kTn - 1); n < (u + 1) * kLate / (kTn - 1); ++n)
+                    issue_late(kt + 1, n);
             if (u >= kTn - 1)
 #pragma unroll
                 for (int n = (u - kTn + 1) * kFirst / kTn; n < (u - kTn + 2) * kFirst / kTn; ++n)
@@ -234,8 +236,6 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    static_assert(kLate <= kTn - 1, "loads of the first half");
-
     // Results.  A lane has row 32 j + l32 of the wave's and, in registers 4 q .. 4 q + 3 of tile i,
     // its columns from 32 i + 8 q + 4 half on.  The two lanes of a row exchange halves, so that
     // each has 16 bytes that lie together.
@@ -507,19 +507,26 @@ int launch_tile(const Fp8Product &p, void *stream)
 }
 
 using Large = Tile<2, 4, 4, 2>;   // 256 weight rows x 256 activation rows
+using Middle = Tile<4, 2, 2, 2>;  // 256 x 128
 using Small = Tile<2, 4, 2, 1>;   // 128 x 128
 
 }  // namespace
 
 int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream)
 {
+    const Fp8Tile tile = fp8_tile(kind, p.M, kind == Fp8Result::kBf16 ? p.N : p.I);
     switch (kind) {
     case Fp8Result::kBf16:
-        return launch_tile<Large, Fp8Result::kBf16>(p, stream);
+        return tile == Fp8Tile::kLarge    ? launch_tile<Large, Fp8Result::kBf16>(p, stream)
+               : tile == Fp8Tile::kMiddle ? launch_tile<Middle, Fp8Result::kBf16>(p, stream)
+                                          : launch_tile<Small, Fp8Result::kBf16>(p, stream);
     case Fp8Result::kGated:
-        return launch_tile<Large, Fp8Result::kGated>(p, stream);
+        return tile == Fp8Tile::kLarge ? launch_tile<Large, Fp8Result::kGated>(p, stream)
+                                       : launch_tile<Middle, Fp8Result::kGated>(p, stream);
     default:
-        return launch_tile<Large, Fp8Result::kGrad>(p, stream);
+        return tile == Fp8Tile::kLarge    ? launch_tile<Large, Fp8Result::kGrad>(p, stream)
+               : tile == Fp8Tile::kMiddle ? launch_tile<Middle, Fp8Result::kGrad>(p, stream)
+                                          : launch_tile<Small, Fp8Result::kGrad>(p, stream);
     }
 }
 

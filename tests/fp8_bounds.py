@@ -184,7 +184,8 @@ def random_rows(M, K, seed, device="cpu"):
     x = torch.randn((M, K), generator=g)
     x[:, torch.randperm(K, generator=g)[:max(1, K // 200)]] *= 20
     x *= torch.exp2(torch.randint(-3, 4, (M, blocks(K)), generator=g).float()).repeat_interleave(B, 1)[:, :K]
-    x[M // 2, :B] = 0
+    if M > 1:
+        x[M // 2, :B] = 0
     if M > 4:
         x[M - 2] = 0
     return x.bfloat16().to(device)
