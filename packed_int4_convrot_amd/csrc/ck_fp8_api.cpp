@@ -14,7 +14,6 @@ using namespace ck::api;
 // Row strides in bytes: a tile's 256 rows are addressed with 32-bit buffer offsets.
 constexpr int64_t kMaxLd = int64_t(1) << 23;
 // Workgroups of up to 512 threads of one launch.
-constexpr int64_t kMaxTiles = (int64_t(1) << 32) / 512 - 1;
 
 int check_columns(const char *fn, const char *name, int64_t K, int64_t of = 16)
 {
@@ -71,7 +70,7 @@ int check_weight_scales(const char *fn, const char *name, const uint8_t *scales)
 
 int check_tiles(const char *fn, int64_t M, int64_t N)
 {
-    if (ck::fp8_tiles(M, N) > kMaxTiles)
+    if (ck::fp8_tiles(M, N) > ck::kFp8MaxTiles)
         return fail(CK_ERR_UNSUPPORTED, "%s: M * N too large for one launch (M=%lld, N=%lld)", fn, (long long)M,
                     (long long)N);
     return CK_OK;
@@ -154,6 +153,16 @@ size_t backward_bytes(int64_t M, int64_t H, int64_t I)
     return serves(M, H, 16) && serves(M, I, 128) ? pair_bytes(M, H, 2 * I) : 0;
 }
 
+bool few(ck::Fp8Result kind, const ck::Fp8Product &p)
+{
+    return ck::fp8_few(kind, p.M, p.K, kind == ck::Fp8Result::kBf16 ? p.N : p.I);
+}
+int from_codes(ck::Fp8Result kind, const ck::Fp8Product &p, float *sums, void *stream)
+{
+    return few(kind, p) ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
+                        : ck::launch_fp8_tiled(kind, p, stream);
+}
+
 // A product of bf16 (or fp32) rows: quantised on the way where that pays, through q otherwise.
 int from_rows(ck::Fp8Result kind, ck::Fp8Product &p, const void *x, bool f32, int64_t ldx, const Quantised &q,
               float *sums, void *stream)
@@ -164,8 +173,7 @@ int from_rows(ck::Fp8Result kind, ck::Fp8Product &p, const void *x, bool f32, in
     if (e != 0)
         return e;
     p.a = q.codes, p.lda = p.K, p.sa = q.scales, p.ldsa = q.stride;
-    return ck::fp8_few(p.M, p.K) ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
-                                 : ck::launch_fp8_tiled(kind, p, stream);
+    return from_codes(kind, p, sums, stream);
 }
 
 // The two products of a feed-forward block, or of its backward pass.
@@ -179,10 +187,10 @@ int two_products(ck::Fp8Result kind, ck::Fp8Product &first, ck::Fp8Product &seco
     const int e = from_rows(kind, first, x, false, ldx, q, sums, stream);
     if (e != 0)
         return e;
-    if (ck::fp8_few(first.M, first.K))
+    if (ck::fp8_few_raw(first.M, first.K) || few(kind, first))
         return from_rows(ck::Fp8Result::kBf16, second, sums, true, second.K, h, nullptr, stream);
     second.a = h.codes, second.lda = second.K, second.sa = h.scales, second.ldsa = h.stride;
-    return ck::launch_fp8_tiled(ck::Fp8Result::kBf16, second, stream);
+    return from_codes(ck::Fp8Result::kBf16, second, nullptr, stream);
 }
 
 int quant_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *codes, int64_t ldq, uint8_t *scales,
@@ -273,10 +281,7 @@ int gemm_impl(const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t 
     ck::Fp8Product p = product(M, K, w, ldw, w_scales, N);
     p.a = codes, p.lda = ldq, p.sa = scales, p.ldsa = lds;
     p.bias = bias, p.out = out, p.ldo = ldo;
-    return hip_status(ck::fp8_few(M, K)
-                          ? ck::launch_fp8_few(ck::Fp8Result::kBf16, p, nullptr, false, 0, nullptr, stream)
-                          : ck::launch_fp8_tiled(ck::Fp8Result::kBf16, p, stream),
-                      fn);
+    return hip_status(from_codes(ck::Fp8Result::kBf16, p, nullptr, stream), fn);
 }
 
 int linear_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint8_t *w, int64_t ldw,

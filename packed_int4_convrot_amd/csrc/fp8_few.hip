@@ -72,9 +72,11 @@ __device__ __forceinline__ Values values32(u32x4 x, u32x4 y, uint32_t scale)
     return Values{{values8(x[0], x[1], s), values8(x[2], x[3], s), values8(y[0], y[1], s), values8(y[2], y[3], s)}};
 }
 
-// Column tiles that one pass takes at most.
-template <Fp8Result kKind, int kMt>
-constexpr int kMostTiles = (kMt == 1 ? 8 : 4) / (kKind == Fp8Result::kGated ? 2 : 1);
+// Column tiles that one pass takes at most.  Codes take one pass: wider results are the tiled
+// product's (fp8_few).
+template <Source kSource, Fp8Result kKind, int kMt>
+constexpr int kMostTiles = kSource == Source::kCodes ? (int)(fp8_few_columns(kKind, kMt) / kFp8Cus / 16)
+                                                     : 8 / (kKind == Fp8Result::kGated ? 2 : 1);
 
 // kMt: 16-row tiles of activations; kT: 16-row tiles of weights a pass (half gate and half
 // up, for kGated).
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
     constexpr int kBlockRows = (kPass + 127) / 128 + 1;              // rows of weight blocks they can touch
     constexpr int kUnits = kT + (kRaw ? 0 : kMt);                    // of a block
     // Equal passes: several are longer than half the most.
-    constexpr bool kPasses = kT / kPair > kMostTiles<kKind, kMt> / 2;
+    constexpr bool kPasses = kRaw && kT / kPair > kMostTiles<kSource, kKind, kMt> / 2;
     static_assert(!kRaw || kMt == 1, "raw rows make up one tile");
     static_assert(kT * kMt <= 2 * kRing, "a wave's sums fit its ring");
     static_assert(kPair * kBlockRows * 512 <= kScaleLoads * kThreads, "scales of up to 512 blocks");
@@ -98,10 +100,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
 
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
     const int l16 = lane % 16, quarter = lane / 16;
-    // Rows of this workgroup: one of the runs of 16 kMt.
-    const int64_t m0 = (int64_t)blockIdx.y * kMt * 16;
-    const int M = (int)min((int64_t)kMt * 16, p.M - m0), K = p.K, steps = (K + 127) / 128;
-    const uint8_t *rows_a = p.a + m0 * p.lda, *rows_sa = p.sa + m0 * p.ldsa;
+    const int M = (int)p.M, K = p.K, steps = (K + 127) / 128;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int c0 = blockIdx.x * per, c1 = min(c0 + per, cols);
     lds_u8 *ring = smem + wave * kRing * kUnit;
@@ -139,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
     __amdgpu_buffer_rsrc_t w_rsrc, a_rsrc;
     int w_row[kT][2], a_row[kRaw ? 1 : kMt][2];          // byte offsets of a lane's rows
     if constexpr (!kRaw) {
-        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)rows_a, (short)0, kRange, 0x00020000);
+        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p.a, (short)0, kRange, 0x00020000);
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
             a_row[j][0] = min(j * 16 + eight, M - 1) * (int)p.lda + at0;
@@ -156,12 +155,8 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
         }
     };
     int place = 0;                                       // ring slot of the next unit
-    // Workgroups start at columns of their own, so that they are spread over the memory.
-    const int shift = (int)((int64_t)blockIdx.x * steps / gridDim.x);
-    auto turned = [&](int b) { return b + shift < steps ? b + shift : b < steps ? b + shift - steps : b; };
     // Unit u of block b: the rows' codes, then the weights.  A block past the last reads zeros.
-    auto issue = [&](int u, int nth, int slot) {
-        const int b = turned(nth);
+    auto issue = [&](int u, int b, int slot) {
         lds_u8 *to = ring + slot * kUnit;
         const bool act = u < kUnits - kT;
         const int r0 = act ? a_row[kRaw ? 0 : u][0] : w_row[u - (kUnits - kT)][0];
@@ -201,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
 #pragma unroll
         for (int r = 0; r < kRowScaleLoads; ++r) {
             const int i = min(r * kThreads + t, sa_count - 1), m = sa_pitch == 4 ? i : by_dwords(i);
-            sa_in[r] = *reinterpret_cast<const uint32_t *>(rows_sa + m * p.ldsa + (i * 4 - m * sa_pitch));
+            sa_in[r] = *reinterpret_cast<const uint32_t *>(p.sa + m * p.ldsa + (i * 4 - m * sa_pitch));
         }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -281,8 +276,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
 #pragma unroll
             for (int j = 0; j < kMt; ++j)
                 acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int nth = wave; nth < steps; nth += kWaves) {
-            const int b = turned(nth);
+        for (int b = wave; b < steps; b += kWaves) {
             Values a[kMt];
             if constexpr (kRaw) {
                 const int m = min(l16, M - 1);
@@ -300,7 +294,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
                 const Values v = values32(lo, hi, scale);
                 // The unit is in registers: its slot takes the unit a ring's length on.
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                issue((u + kRing) % kUnits, nth + (u + kRing) / kUnits * kWaves, place);
+                issue((u + kRing) % kUnits, b + (u + kRing) / kUnits * kWaves, place);
                 place = place + 1 == kRing ? 0 : place + 1;
                 if (i < 0) {
                     a[i < 0 ? u : 0] = v;
@@ -336,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
             const int m = e / kPass, r = e % kPass, c = first + r;
             if (c >= c1)
                 continue;
-            const int64_t row = m0 + m;
+            const int64_t row = m;
             if constexpr (kKind == Fp8Result::kBf16) {
                 const float s = total(m, r) + (p.bias ? bf16_to_f32(p.bias[c]) : 0.f);
                 p.out[row * p.ldo + c] = f32_to_bf16(s);
@@ -362,7 +356,7 @@ int launch_one(const Fp8Product &p, const void *x, int64_t ldx, float *sums, int
                void *stream)
 {
     auto kern = fp8_few_kernel<kSource, kKind, kMt, kT>;
-    const size_t steps = fp8_blocks(p.K), M = p.M < kMt * 16 ? p.M : kMt * 16;
+    const size_t steps = fp8_blocks(p.K), M = p.M;
     const size_t lds = kRings + kScaleLoads * kThreads + (M * ((steps + 3) / 4 * 4) + 15) / 16 * 16 +
                        (kSource == Source::kCodes ? 0 : M * (steps * 128 + 16));
     constexpr int kMostLds = 160 * 1024;
@@ -370,8 +364,8 @@ int launch_one(const Fp8Product &p, const void *x, int64_t ldx, float *sums, int
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
     if (attr != hipSuccess)
         return (int)attr;
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid, (unsigned)((p.M + kMt * 16 - 1) / (kMt * 16))), dim3(kThreads), lds, reinterpret_cast<hipStream_t>(stream), p, x,
-                       ldx, sums, per, passes, divide_by((int64_t)steps), divide_by((int64_t)(steps + 3) / 4));
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, reinterpret_cast<hipStream_t>(stream), p, x, ldx, sums, per,
+                       passes, divide_by((int64_t)steps), divide_by((int64_t)(steps + 3) / 4));
     return (int)hipGetLastError();
 }
 
@@ -379,7 +373,7 @@ template <Source kSource, Fp8Result kKind, int kMt>
 int launch_shape(const Fp8Product &p, const void *x, int64_t ldx, float *sums, void *stream)
 {
     constexpr int kPair = kKind == Fp8Result::kGated ? 2 : 1;
-    constexpr int kMost = kMostTiles<kKind, kMt>;
+    constexpr int kMost = kMostTiles<kSource, kKind, kMt>;
     const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
     const int per = (cols + kFp8Cus - 1) / kFp8Cus, grid = (cols + per - 1) / per;
     const int tiles = (per + 15) / 16, passes = (tiles + kMost - 1) / kMost, each = (tiles + passes - 1) / passes;

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLaneColumns = 16;
+constexpr int kRowsEach = kThreads / kWave;     // of a workgroup
 constexpr int kSegment = kWave * kLaneColumns;  // columns of a wave: eight blocks
 
 __device__ __forceinline__ float abs_max16(const float (&v)[16])
@@ -57,18 +58,16 @@ __device__ __forceinline__ void load16(const void *x, int64_t at, float (&v)[16]
     }
 }
 
-// A wave quantises 1024 columns of a row, a lane 16 of them; eight lanes share a block.
+// A wave quantises 1024 columns of a row, a lane 16 of them; eight lanes share a block.  (x, the
+// segments of a row, by y, rows: a division would take a third of the time of a few rows.)
 template <bool kF32>
-__global__ __launch_bounds__(kThreads) void fp8_quant_kernel(const void *__restrict__ x, int64_t units, int segments,
-                                                             int K, int64_t ldx, uint8_t *__restrict__ codes,
-                                                             int64_t lda, uint8_t *__restrict__ scales, int64_t ldsa)
+__global__ __launch_bounds__(kThreads) void fp8_quant_kernel(const void *__restrict__ x, int64_t M, int K, int64_t ldx,
+                                                             uint8_t *__restrict__ codes, int64_t lda,
+                                                             uint8_t *__restrict__ scales, int64_t ldsa)
 {
     const int lane = threadIdx.x % kWave;
-    constexpr int kUnits = kThreads / kWave;
-    for (int64_t unit = (int64_t)blockIdx.x * kUnits + threadIdx.x / kWave; unit < units;
-         unit += (int64_t)gridDim.x * kUnits) {
-        const int64_t m = unit / segments;
-        const int k = (int)(unit - m * segments) * kSegment + lane * kLaneColumns;
+    const int k = blockIdx.x * kSegment + lane * kLaneColumns;
+    for (int64_t m = blockIdx.y * kRowsEach + threadIdx.x / kWave; m < M; m += (int64_t)gridDim.y * kRowsEach) {
         float v[16];
         if (k < K) {
             load16<kF32>(x, m * ldx + k, v);
@@ -179,13 +178,11 @@ int launch_fp8_quant(const void *x, bool f32, int64_t M, int K, int64_t ldx, uin
     if (M <= 0)
         return 0;
     const int segments = (K + kSegment - 1) / kSegment;
-    const int64_t units = M * segments;
     auto kern = f32 ? fp8_quant_kernel<true> : fp8_quant_kernel<false>;
-    constexpr int kUnits = kThreads / kWave;
-    constexpr int64_t kMostBlocks = int64_t(1) << 23;  // of 256 threads: below 2^32 work-items
-    const int64_t blocks = (units + kUnits - 1) / kUnits;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks)), dim3(kThreads), 0,
-                       reinterpret_cast<hipStream_t>(stream), x, units, segments, K, ldx, codes, lda, scales, ldsa);
+    constexpr int64_t kMostRuns = 65535;
+    const int64_t runs = (M + kRowsEach - 1) / kRowsEach;
+    hipLaunchKernelGGL(kern, dim3((unsigned)segments, (unsigned)(runs < kMostRuns ? runs : kMostRuns)), dim3(kThreads),
+                       0, reinterpret_cast<hipStream_t>(stream), x, M, K, ldx, codes, lda, scales, ldsa);
     return (int)hipGetLastError();
 }
 

@@ -36,13 +36,14 @@ __device__ __forceinline__ int swizzle(int r, int c) { return c ^ ((r >> 1) & 7)
 template <int N>
 __device__ __forceinline__ void wait_reads_and_loads()
 {
-    static_assert(N < 16, "vmcnt");
-    __builtin_amdgcn_s_waitcnt(N | (7 << 4));
+    static_assert(N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
 }
 
-template <int kWn_, int kWm_, int kTn_, int kTm_>
+template <int kWn_, int kWm_, int kTn_, int kTm_, int kStages_ = 2>
 struct Tile {
-    static constexpr int kWn = kWn_, kWm = kWm_, kTn = kTn_, kTm = kTm_;
+    static constexpr int kWn = kWn_, kWm = kWm_, kTn = kTn_, kTm = kTm_, kStages = kStages_;
+    static_assert((kStages & (kStages - 1)) == 0, "a power of two");
     static constexpr int kWaves = kWn * kWm;
     static constexpr int kBn = kWn * kTn * 32, kBm = kWm * kTm * 32;
     static constexpr int kStage = (kBn + kBm) * 128;
@@ -50,7 +51,7 @@ struct Tile {
     // of two rows of weight blocks.
     static constexpr int kScaleSteps = 64, kRowScales = kScaleSteps * kBm;
     static constexpr int kScales = kRowScales + 2 * kScaleSteps;
-    static constexpr int kLds = 2 * kStage + kScales + kWaves * 32 * 4;
+    static constexpr int kLds = kStages * kStage + kScales + kWaves * 32 * 4;
     static constexpr int kPerCu = 160 * 1024 / kLds;
 };
 
@@ -62,7 +63,7 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     static_assert(!kGated || kBn == 256, "a gated tile covers one block of the result");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem_generic[];
     lds_u8 *smem = (lds_u8 *)smem_generic;
-    lds_u8 *scales = smem + 2 * T::kStage;
+    lds_u8 *scales = smem + T::kStages * T::kStage;
     __attribute__((address_space(3))) float *red = (__attribute__((address_space(3))) float *)(scales + T::kScales);
 
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
@@ -70,30 +71,24 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     const int l32 = lane % 32, half = lane / 32;
     const int K = p.K, steps = (K + 127) / 128;
 
-    // A workgroup takes tile after tile.  Runs of kGroupM tile rows are walked column by column,
-    // a contiguous run on each XCD.
-    int64_t m0;
-    int n0, rows;                                        // first row and column of the result
-    __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc, sa_rsrc;
-    auto start_tile = [&](int index) {
-        constexpr int kGroupM = 4;
-        const int tiles_n = tiles / tiles_m, tile = xcd_block(index, tiles);
-        const int group = tile / (kGroupM * tiles_n);
-        const int first_m = group * kGroupM;
-        const int group_m = min(kGroupM, tiles_m - first_m);
-        const int in_group = tile - group * kGroupM * tiles_n;
-        m0 = (int64_t)(first_m + in_group % group_m) * kBm;
-        n0 = (in_group / group_m) * (kGated ? kBn / 2 : kBn);
-        rows = (int)min((int64_t)kBm, p.M - m0);
-        // Operand rows past the end and columns past K read as zero (out of the buffer's range).
-        a_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.a + m0 * p.lda), (short)0,
-                                                   (int)((rows - 1) * p.lda + K), 0x00020000);
-        const int w_rows = kGated ? p.I + kBn / 2 : min(kBn, p.N - n0);
-        w_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.w + n0 * p.ldw), (short)0,
-                                                   (int)((w_rows - 1) * p.ldw + K), 0x00020000);
-        sa_rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)(p.sa + m0 * p.ldsa), (short)0, (int)(rows * p.ldsa),
-                                                    0x00020000);
-    };
+    // Runs of kGroupM tile rows are walked column by column, a contiguous run on each XCD.
+    constexpr int kGroupM = 4;
+    const int tiles_n = tiles / tiles_m, tile = xcd_block(blockIdx.x, tiles);
+    const int group = tile / (kGroupM * tiles_n);
+    const int first_m = group * kGroupM;
+    const int group_m = min(kGroupM, tiles_m - first_m);
+    const int in_group = tile - group * kGroupM * tiles_n;
+    const int64_t m0 = (int64_t)(first_m + in_group % group_m) * kBm;     // first row and
+    const int n0 = (in_group / group_m) * (kGated ? kBn / 2 : kBn);       // column of the result
+    const int rows = (int)min((int64_t)kBm, p.M - m0);
+    // Operand rows past the end and columns past K read as zero (out of the buffer's range).
+    const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(p.a + m0 * p.lda), (short)0, (int)((rows - 1) * p.lda + K), 0x00020000);
+    const int w_rows = kGated ? p.I + kBn / 2 : min(kBn, p.N - n0);
+    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(p.w + n0 * p.ldw), (short)0, (int)((w_rows - 1) * p.ldw + K), 0x00020000);
+    const __amdgpu_buffer_rsrc_t sa_rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.sa + m0 * p.ldsa), (short)0, (int)(rows * p.ldsa), 0x00020000);
     constexpr int kPast = 0x7fffffff;
     constexpr int kALoads = kBm * 128 / (kWaves * 1024), kWLoads = kBn * 128 / (kWaves * 1024);
     static_assert(kALoads * kWaves * 1024 == kBm * 128 && kWLoads * kWaves * 1024 == kBn * 128, "whole loads");
@@ -110,14 +105,16 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     // Load n of a wave's share of a step, into its buffer.  Weight rows are dealt to the waves so
     // that the first half of a wave's loads are of the first half of every wave's tiles.
     constexpr int kEarly = kWLoads / 2, kLate = kWLoads - kEarly;
-    static_assert(kWLoads % 2 == 0 && kTn % 2 == 0, "halves");
+    static_assert(kWLoads % 2 == 0 && kTn * 2 % kEarly == 0, "halves");
+    constexpr int kStages = T::kStages;
+    auto buffer = [&](int step) { return smem + (step & (kStages - 1)) * T::kStage; };
     auto issue = [&](int step, bool weights, int n) {
         constexpr int kRows = kTn * 32, kEights = kRows / 16;     // of a wave's tiles; in a half of them
         const int w8 = wave * kEarly + n % kEarly;                // of the early or the late eights
         const int eight = weights ? w8 / kEights * (2 * kEights) + w8 % kEights + n / kEarly * kEights
                                   : wave * kALoads + n;
         const int c = step * 128 + 16 * swizzle(eight * 8 + lane / 8, lane % 8);
-        lds_u8 *to = smem + (step & 1) * T::kStage + eight * 1024;
+        lds_u8 *to = buffer(step) + eight * 1024;
         if (weights)
             load_lds16(w_rsrc, to, c < K ? w_lane + c + weight_row(eight * 8) * (int)p.ldw : kPast);
         else
@@ -156,18 +153,41 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     // after the next as soon as that, and every load has one and a half steps to land.  (With
     // one barrier and one step it takes 792 us for a feed-forward block of 8192 rows, H 3840,
     // I 10240.)  Loads go out one or two at a time between products.
+    // Small tiles have more than two buffers: one barrier a step, and loads kStages - 1 steps ahead.
     constexpr int kUnits = 2 * kTn;
+    constexpr int kUnderWay = kStages == 2 ? kAll : (kStages - 2) * kAll;   // at a barrier
     auto first_loads = [&]() {
         load_scales(0);
 #pragma unroll
-        for (int n = 0; n < kFirst; ++n)
-            issue_first(0, n);
+        for (int step = 0; step < kStages - 1; ++step) {
 #pragma unroll
-        for (int n = 0; n < kLate; ++n)
-            issue_late(0, n);
+            for (int n = 0; n < kFirst; ++n)
+                issue_first(step, n);
 #pragma unroll
-        for (int n = 0; n < kFirst; ++n)
-            issue_first(1, n);
+            for (int n = 0; n < kLate; ++n)
+                issue_late(step, n);
+        }
+        if constexpr (kStages == 2)
+#pragma unroll
+            for (int n = 0; n < kFirst; ++n)
+                issue_first(1, n);
+    };
+    // Loads under unit u of a step.
+    auto issue_under = [&](int kt, int u) {
+        if constexpr (kStages > 2) {
+            constexpr int kSlots = kUnits - 1;
+#pragma unroll
+            for (int n = u * kAll / kSlots; n < (u + 1) * kAll / kSlots; ++n)
+                n < kFirst ? issue_first(kt + kStages - 1, n) : issue_late(kt + kStages - 1, n - kFirst);
+        } else if (u < kTn - 1) {
+#pragma unroll
+            for (int n = u * kLate / (kTn - 1); n < (u + 1) * kLate / (kTn - 1); ++n)
+                issue_late(kt + 1, n);
+        } else {
+#pragma unroll
+            for (int n = (u - kTn + 1) * kFirst / kTn; n < (u - kTn + 2) * kFirst / kTn; ++n)
+                issue_first(kt + 2, n);
+        }
     };
 
     v16f acc[kTn][kTm];
@@ -211,11 +231,11 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
         acc[i][j] = mfma_e4m3(w[u & 1], a[s][j], acc[i][j], sw[kGated && i >= kTn / 2], sa[j]);
     };
     auto all_but_last = [&](int kt) {
-        const lds_u8 *stage = smem + (kt & 1) * T::kStage;
+        const lds_u8 *stage = buffer(kt);
 #pragma unroll
         for (int u = 0; u + 1 < kUnits; ++u) {
-            if (u == kTn - 1) {
-                wait_reads_and_loads<kAll>();
+            if (kStages == 2 && u == kTn - 1) {
+                wait_reads_and_loads<kUnderWay>();
                 __builtin_amdgcn_s_barrier();
             }
             w[(u + 1) & 1] = fragment(stage + w_at + (u + 1) / 2 * 4096, (u + 1) % 2);
@@ -223,14 +243,7 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
 #pragma unroll
             for (int j = 0; j < kTm; ++j)
                 multiply(u, j);
-            if (u < kTn - 1)
-#pragma unroll
-                for (int n = u * kLate / (kTn - 1); n < (u + 1) * kLate / (kTn - 1); ++n)
-                    issue_late(kt + 1, n);
-            if (u >= kTn - 1)
-#pragma unroll
-                for (int n = (u - kTn + 1) * kFirst / kTn; n < (u - kTn + 2) * kFirst / kTn; ++n)
-                    issue_first(kt + 2, n);
+            issue_under(kt, u);
             if (u == kUnits - 2)
                 read_scales(kt + 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -316,176 +329,172 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
                 *reinterpret_cast<u32x4 *>(dst + (m0 + m) * ld + n + 8 * c) = v;
         }
     };
-    auto write_tile = [&]() {
-        const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
-        if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
-#pragma unroll
-            for (int i = 0; i < kTn; ++i)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float b[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        b[r] = 0.f;
-                    if (kKind == Fp8Result::kBf16 && p.bias)
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            b[r] = bf16_to_f32(
-                                p.bias[min(nw + i * 32 + 16 * g + r / 4 * 8 + 4 * half + r % 4, p.N - 1)]);
-#pragma unroll
-                    for (int j = 0; j < kTm; ++j) {
-                        float v[8];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            v[r] = acc[i][j][8 * g + r] + b[r];
-                        stage_bf16(i, j, g, v);
-                    }
-                }
-            if constexpr (kKind == Fp8Result::kBf16) {
-                write_bf16(p.out, p.ldo, nw, p.N, std::integral_constant<int, kSlots>{}, 0);
-            } else {
-                const std::integral_constant<int, kSlots / 2> width;
-                write_bf16(p.gate_up, p.ldg, nw, p.I, width, 0);
-                write_bf16(p.gate_up + p.I, p.ldg, nw, p.I, width, kSlots / 2);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < (kKind == Fp8Result::kBf16 ? 0 : kTm); ++j) {
-            const int m = wm * kTm * 32 + j * 32 + l32;
-            const int64_t row = m0 + m;
-            if constexpr (kGated) {
-                constexpr int kHalf = kTn / 2;
-                float h[kHalf][16], largest = 0.f;
-#pragma unroll
-                for (int i = 0; i < kHalf; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        h[i][r] = gated(acc[i][j][r], acc[i + kHalf][j][r]);
-                        largest = fmaxf(largest, fabsf(h[i][r]));
-                    }
-                quantise(std::integral_constant<int, kHalf>{}, largest,
-                         [&](int i, float *v) {
-#pragma unroll
-                             for (int r = 0; r < 16; ++r)
-                                 v[r] = h[i][r];
-                         },
-                         m, nw, p.q + row * p.I + nw, p.sq + row * p.ldsq + nw / 128);
-            } else {
-                // dg stays in registers, du waits in the wave's part of the stages.
-                const uint16_t *gu = p.gate_up + (m0 + min(m, rows - 1)) * p.ldg +
-                                     (nw < p.I ? nw : p.I - kTn * 32) + 8 * half;
-                lds_u8 *wait = smem + (wave * kTn * 4 * kWave + lane) * 16;
-                float dg[kTn][16], largest_g = 0.f, largest_u = 0.f;
-#pragma unroll
-                for (int i = 0; i < kTn; ++i) {
-#pragma unroll
-                    for (int g2 = 0; g2 < 2; ++g2) {
-                        __builtin_amdgcn_sched_barrier(0);
-                        float g[8], u[8];
-                        floats8(*reinterpret_cast<const u32x4 *>(gu + i * 32 + 16 * g2), g);
-                        floats8(*reinterpret_cast<const u32x4 *>(gu + p.I + i * 32 + 16 * g2), u);
-                        v4f du[2];
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const float2 d = gated_gradient(acc[i][j][8 * g2 + r], g[r], u[r]);
-                            dg[i][8 * g2 + r] = d.x, du[r / 4][r % 4] = d.y;
-                            largest_g = fmaxf(largest_g, fabsf(d.x)), largest_u = fmaxf(largest_u, fabsf(d.y));
-                        }
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + 2 * g2 + q) * kWave * 16) = du[q];
-                    }
-                }
-                uint8_t *to = p.q + row * 2 * p.I + nw, *scale = p.sq + row * p.ldsq + nw / 128;
-                const std::integral_constant<int, kTn> tiles_c;
-                quantise(tiles_c, largest_g,
-                         [&](int i, float *v) {
-#pragma unroll
-                             for (int r = 0; r < 16; ++r)
-                                 v[r] = dg[i][r];
-                         },
-                         m, nw, to, scale);
-                quantise(tiles_c, largest_u,
-                         [&](int i, float *v) {
-#pragma unroll
-                             for (int q = 0; q < 4; ++q) {
-                                 const v4f d = *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + q) * kWave * 16);
-#pragma unroll
-                                 for (int r = 0; r < 4; ++r)
-                                     v[4 * q + r] = d[r];
-                             }
-                         },
-                         m, nw, to + p.I, scale + p.I / 128);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
+    static_assert(kKind != Fp8Result::kGrad || kWaves * kTn * 4 * kWave * 16 <= kStages * T::kStage, "du fits the stages");
 
-    static_assert(kKind != Fp8Result::kGrad || kWaves * kTn * 4 * kWave * 16 <= 2 * T::kStage, "du fits the stages");
-    start_tile(blockIdx.x);
     first_loads();
 #pragma unroll
-        for (int i = 0; i < kTn; ++i)
+    for (int i = 0; i < kTn; ++i)
+#pragma unroll
+        for (int j = 0; j < kTm; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[i][j][r] = 0.f;
+    keep_scales();
+    wait_reads_and_loads<kStages == 2 ? kFirst : (kStages - 2) * kAll>();   // the first step is there
+    lds_barrier();
+    w[0] = fragment(smem + w_at, 0);
+#pragma unroll
+    for (int j = 0; j < kTm; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            a[s][j] = fragment(smem + a_at + j * 4096, s);
+    for (int first = 0;; first += T::kScaleSteps) {
+        const int end = __builtin_amdgcn_readfirstlane(min(first + T::kScaleSteps, steps - 1));
+        read_scales(first);
+        take_scales();
+        // One straight run: a load past the last step's columns reads zeros.
+        for (int kt = first; kt < end; ++kt) {
+            all_but_last(kt);
+            wait_reads_and_loads<kUnderWay>();
+            __builtin_amdgcn_s_barrier();
+            const lds_u8 *other = buffer(kt + 1);
+            w[0] = fragment(other + w_at, 0);
 #pragma unroll
             for (int j = 0; j < kTm; ++j)
+                a[0][j] = fragment(other + a_at + j * 4096, 0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[i][j][r] = 0.f;
+            for (int j = 0; j < kTm; ++j) {
+                multiply(kUnits - 1, j);
+                a[1][j] = fragment(other + a_at + j * 4096, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            take_scales();
+        }
+        if (end < first + T::kScaleSteps)
+            break;
+        lds_barrier();
+        load_scales(end);
         keep_scales();
         wait_vmcnt0();
         lds_barrier();
-        w[0] = fragment(smem + w_at, 0);
+    }
+    all_but_last(steps - 1);
+#pragma unroll
+    for (int j = 0; j < kTm; ++j)
+        multiply(kUnits - 1, j);
+    // All products are done here: left to itself the compiler takes some of the last step's, and
+    // the fragments that they need, into the writing of the results.
+#pragma unroll
+    for (int i = 0; i < kTn; ++i)
 #pragma unroll
         for (int j = 0; j < kTm; ++j)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                a[s][j] = fragment(smem + a_at + j * 4096, s);
-        for (int first = 0;; first += T::kScaleSteps) {
-            const int end = __builtin_amdgcn_readfirstlane(min(first + T::kScaleSteps, steps - 1));
-            read_scales(first);
-            take_scales();
-            // One straight run: a load past the last step's columns reads zeros.
-            for (int kt = first; kt < end; ++kt) {
-                all_but_last(kt);
-                wait_reads_and_loads<kAll>();
-                __builtin_amdgcn_s_barrier();
-                const lds_u8 *other = smem + (~kt & 1) * T::kStage;
-                w[0] = fragment(other + w_at, 0);
-#pragma unroll
-                for (int j = 0; j < kTm; ++j)
-                    a[0][j] = fragment(other + a_at + j * 4096, 0);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int j = 0; j < kTm; ++j) {
-                    multiply(kUnits - 1, j);
-                    a[1][j] = fragment(other + a_at + j * 4096, 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                take_scales();
-            }
-            if (end < first + T::kScaleSteps)
-                break;
-            lds_barrier();
-            load_scales(end);
-            keep_scales();
-            wait_vmcnt0();
-            lds_barrier();
-        }
-        all_but_last(steps - 1);
-#pragma unroll
-        for (int j = 0; j < kTm; ++j)
-            multiply(kUnits - 1, j);
-        // All products are done here: left to itself the compiler takes some of the last step's, and
-        // the fragments that they need, into the writing of the results.
+            asm volatile("" : "+v"(acc[i][j]));
+    wait_vmcnt0();   // loads past the last step
+    lds_barrier();
+
+    const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
+    if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
 #pragma unroll
         for (int i = 0; i < kTn; ++i)
 #pragma unroll
-            for (int j = 0; j < kTm; ++j)
-                asm volatile("" : "+v"(acc[i][j]));
-        wait_vmcnt0();   // loads past the last step
-        lds_barrier();
-
-        write_tile();
+            for (int g = 0; g < 2; ++g) {
+                float b[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    b[r] = 0.f;
+                if (kKind == Fp8Result::kBf16 && p.bias)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        b[r] = bf16_to_f32(
+                            p.bias[min(nw + i * 32 + 16 * g + r / 4 * 8 + 4 * half + r % 4, p.N - 1)]);
+#pragma unroll
+                for (int j = 0; j < kTm; ++j) {
+                    float v[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        v[r] = acc[i][j][8 * g + r] + b[r];
+                    stage_bf16(i, j, g, v);
+                }
+            }
+        if constexpr (kKind == Fp8Result::kBf16) {
+            write_bf16(p.out, p.ldo, nw, p.N, std::integral_constant<int, kSlots>{}, 0);
+        } else {
+            const std::integral_constant<int, kSlots / 2> width;
+            write_bf16(p.gate_up, p.ldg, nw, p.I, width, 0);
+            write_bf16(p.gate_up + p.I, p.ldg, nw, p.I, width, kSlots / 2);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < (kKind == Fp8Result::kBf16 ? 0 : kTm); ++j) {
+        const int m = wm * kTm * 32 + j * 32 + l32;
+        const int64_t row = m0 + m;
+        if constexpr (kGated) {
+            constexpr int kHalf = kTn / 2;
+            float h[kHalf][16], largest = 0.f;
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    h[i][r] = gated(acc[i][j][r], acc[i + kHalf][j][r]);
+                    largest = fmaxf(largest, fabsf(h[i][r]));
+                }
+            quantise(std::integral_constant<int, kHalf>{}, largest,
+                     [&](int i, float *v) {
+#pragma unroll
+                         for (int r = 0; r < 16; ++r)
+                             v[r] = h[i][r];
+                     },
+                     m, nw, p.q + row * p.I + nw, p.sq + row * p.ldsq + nw / 128);
+        } else if constexpr (kKind == Fp8Result::kGrad) {
+            // dg stays in registers, du waits in the wave's part of the stages.
+            const uint16_t *gu = p.gate_up + (m0 + min(m, rows - 1)) * p.ldg +
+                                 (nw < p.I ? nw : p.I - kTn * 32) + 8 * half;
+            lds_u8 *wait = smem + (wave * kTn * 4 * kWave + lane) * 16;
+            float dg[kTn][16], largest_g = 0.f, largest_u = 0.f;
+#pragma unroll
+            for (int i = 0; i < kTn; ++i) {
+#pragma unroll
+                for (int g2 = 0; g2 < 2; ++g2) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    float g[8], u[8];
+                    floats8(*reinterpret_cast<const u32x4 *>(gu + i * 32 + 16 * g2), g);
+                    floats8(*reinterpret_cast<const u32x4 *>(gu + p.I + i * 32 + 16 * g2), u);
+                    v4f du[2];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float2 d = gated_gradient(acc[i][j][8 * g2 + r], g[r], u[r]);
+                        dg[i][8 * g2 + r] = d.x, du[r / 4][r % 4] = d.y;
+                        largest_g = fmaxf(largest_g, fabsf(d.x)), largest_u = fmaxf(largest_u, fabsf(d.y));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + 2 * g2 + q) * kWave * 16) = du[q];
+                }
+            }
+            uint8_t *to = p.q + row * 2 * p.I + nw, *scale = p.sq + row * p.ldsq + nw / 128;
+            const std::integral_constant<int, kTn> tiles_c;
+            quantise(tiles_c, largest_g,
+                     [&](int i, float *v) {
+#pragma unroll
+                         for (int r = 0; r < 16; ++r)
+                             v[r] = dg[i][r];
+                     },
+                     m, nw, to, scale);
+            quantise(tiles_c, largest_u,
+                     [&](int i, float *v) {
+#pragma unroll
+                         for (int q = 0; q < 4; ++q) {
+                             const v4f d = *(__attribute__((address_space(3))) v4f *)(wait + (i * 4 + q) * kWave * 16);
+#pragma unroll
+                             for (int r = 0; r < 4; ++r)
+                                 v[4 * q + r] = d[r];
+                         }
+                     },
+                     m, nw, to + p.I, scale + p.I / 128);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 template <class T, Fp8Result kKind>
@@ -506,27 +515,48 @@ int launch_tile(const Fp8Product &p, void *stream)
     return (int)hipGetLastError();
 }
 
-using Large = Tile<2, 4, 4, 2>;   // 256 weight rows x 256 activation rows
-using Middle = Tile<4, 2, 2, 2>;  // 256 x 128
-using Small = Tile<2, 4, 2, 1>;   // 128 x 128
+template <Fp8Result kKind>
+int launch_kind(const Fp8Product &p, void *stream)
+{
+    constexpr bool kGated = kKind == Fp8Result::kGated;
+    switch (fp8_plan(kKind, p.M, kKind == Fp8Result::kBf16 ? p.N : p.I).tile) {
+    case Fp8Tile::k256x256:
+        return launch_tile<Tile<2, 4, 4, 2>, kKind>(p, stream);
+    case Fp8Tile::k256x192:
+        return launch_tile<Tile<4, 2, 2, 3>, kKind>(p, stream);
+    case Fp8Tile::k256x128:
+        return launch_tile<Tile<4, 2, 2, 2>, kKind>(p, stream);
+    case Fp8Tile::k256x64:
+        if constexpr (kGated)
+            return launch_tile<Tile<4, 2, 2, 1>, kKind>(p, stream);
+        break;
+    case Fp8Tile::k128x128:
+        if constexpr (!kGated)
+            return launch_tile<Tile<2, 4, 2, 1, 4>, kKind>(p, stream);
+        break;
+    case Fp8Tile::k128x64:
+        if constexpr (!kGated)
+            return launch_tile<Tile<4, 2, 1, 1, 4>, kKind>(p, stream);
+        break;
+    case Fp8Tile::k64x64:
+        if constexpr (kKind == Fp8Result::kBf16)
+            return launch_tile<Tile<2, 2, 1, 1, 4>, kKind>(p, stream);
+        break;
+    }
+    return (int)hipErrorInvalidValue;
+}
 
 }  // namespace
 
 int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream)
 {
-    const Fp8Tile tile = fp8_tile(kind, p.M, kind == Fp8Result::kBf16 ? p.N : p.I);
     switch (kind) {
     case Fp8Result::kBf16:
-        return tile == Fp8Tile::kLarge    ? launch_tile<Large, Fp8Result::kBf16>(p, stream)
-               : tile == Fp8Tile::kMiddle ? launch_tile<Middle, Fp8Result::kBf16>(p, stream)
-                                          : launch_tile<Small, Fp8Result::kBf16>(p, stream);
+        return launch_kind<Fp8Result::kBf16>(p, stream);
     case Fp8Result::kGated:
-        return tile == Fp8Tile::kLarge ? launch_tile<Large, Fp8Result::kGated>(p, stream)
-                                       : launch_tile<Middle, Fp8Result::kGated>(p, stream);
+        return launch_kind<Fp8Result::kGated>(p, stream);
     default:
-        return tile == Fp8Tile::kLarge    ? launch_tile<Large, Fp8Result::kGrad>(p, stream)
-               : tile == Fp8Tile::kMiddle ? launch_tile<Middle, Fp8Result::kGrad>(p, stream)
-                                          : launch_tile<Small, Fp8Result::kGrad>(p, stream);
+        return launch_kind<Fp8Result::kGrad>(p, stream);
     }
 }
 

@@ -142,7 +142,8 @@ int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *)
 
 int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums, void *)
 {
-    EXPECT(fp8_few(p.M, p.K));
+    EXPECT(x || fp8_few(kind, p.M, p.K, kind == Fp8Result::kBf16 ? p.N : p.I));
+    EXPECT(p.M <= kFp8FewRows && p.M * fp8_scale_stride(p.K) <= 16 * 1024);
     touch_product(kind, p);
     if (x) {
         EXPECT(fp8_few_raw(p.M, p.K));
@@ -247,16 +248,38 @@ void blocks()
         }
 }
 
-// Every size gets a tile, and no tile's launch is refused that the checks let pass.
+// Every size gets a tile that its kind has, in a grid that one launch takes.
 void tiles()
 {
-    for (int64_t M = 1; M < (int64_t(1) << 22); M = M * 3 + 1)
-        for (int64_t N = 128; N < (int64_t(1) << 22); N = N * 3 + 128)
-            for (auto kind : {ck::Fp8Result::kBf16, ck::Fp8Result::kGated, ck::Fp8Result::kGrad}) {
-                const ck::Fp8Tile t = ck::fp8_tile(kind, M, N);
-                EXPECT(t == ck::Fp8Tile::kLarge || t == ck::Fp8Tile::kMiddle || t == ck::Fp8Tile::kSmall);
-                EXPECT(kind != ck::Fp8Result::kGated || t != ck::Fp8Tile::kSmall);
+    const struct {
+        ck::Fp8Tile tile;
+        int64_t n, m;
+    } sizes[] = {{ck::Fp8Tile::k256x256, 256, 256}, {ck::Fp8Tile::k256x192, 256, 192}, {ck::Fp8Tile::k256x128, 256, 128},
+                 {ck::Fp8Tile::k256x64, 256, 64},   {ck::Fp8Tile::k128x128, 128, 128}, {ck::Fp8Tile::k128x64, 128, 64},
+                 {ck::Fp8Tile::k64x64, 64, 64}};
+    bool seen[3][7] = {};
+    for (int64_t M = 1; M < (int64_t(1) << 31); M = M * 5 / 4 + 1)
+        for (int64_t N = 16; N < (int64_t(1) << 31); N = N * 3 / 2 / 16 * 16 + 16)
+            for (int kind = 0; kind < 3; ++kind) {
+                const int64_t columns = kind == 0 ? N : (N + 127) / 128 * 128;
+                if (ck::fp8_tiles(M, columns * (kind == 1 ? 2 : 1)) > ck::kFp8MaxTiles)
+                    continue;
+                const ck::Fp8Plan plan = ck::fp8_plan((ck::Fp8Result)kind, M, columns);
+                bool found = false;
+                for (int i = 0; i < 7; ++i)
+                    if (sizes[i].tile == plan.tile) {
+                        found = seen[kind][i] = true;
+                        const int64_t rows = columns * (kind == 1 ? 2 : 1);
+                        const int64_t grid = (rows + sizes[i].n - 1) / sizes[i].n * ((M + sizes[i].m - 1) / sizes[i].m);
+                        EXPECT(plan.cost > 0 && grid * 512 < (int64_t(1) << 32));
+                        EXPECT(kind != 1 || sizes[i].n == 256);   // whole blocks of gate and up
+                        EXPECT(kind != 2 || sizes[i].n >= 128);
+                    }
+                EXPECT(found);
             }
+    for (int kind = 0; kind < 3; ++kind)
+        for (int i = 0; i < 7; ++i)
+            EXPECT(seen[kind][i] == (kind == 1 ? sizes[i].n == 256 : i != 3 && (kind == 0 || i != 6)));
 }
 
 }  // namespace

@@ -111,8 +111,12 @@ LINEARS = [(1, 16, 16), (1, 3840, 512), (2, 144, 48), (5, 128, 1040), (8, 1024, 
            (17, 272, 528), (32, 3840, 256), (33, 400, 144), (64, 1040, 112), (65, 640, 384), (100, 8192, 144),
            (129, 8320, 272), (130, 8208, 16), (200, 8448, 32), (257, 256, 1040), (300, 2112, 1040), (513, 1168, 784),
            (1000, 384, 272), (3, 32768, 64), (70, 32768, 80),
-           # each tile of the tiled product: 256 x 128, 256 x 256, the latter with two runs of scales
-           (2000, 272, 3824), (4200, 144, 3856), (8191, 400, 2064), (4100, 8336, 3600)]
+           # each tile of the tiled product, with one and with two runs of scales
+           (500, 272, 3824), (1000, 400, 3824), (2000, 272, 3824), (3000, 144, 3856), (8191, 400, 2064), (4200, 144, 3856),
+           (450, 8336, 3600), (900, 8336, 3600), (1800, 8336, 3600), (2800, 8336, 3600), (4100, 8336, 3600),
+           # few rows: each number of 16-row tiles of either operand, and passes
+           (1, 16400, 4304), (2, 16400, 8256), (16, 2112, 4304), (30, 8208, 8256), (33, 4112, 4304), (50, 4112, 4304),
+           (60, 10256, 272), (1, 16, 33040), (3, 144, 50064), (2, 48, 24688)]
 
 
 @pytest.mark.parametrize("M,K,N", LINEARS)
@@ -155,7 +159,11 @@ def test_without_rows():
 BLOCKS = [(1, 16, 128), (1, 3840, 384), (2, 144, 128), (5, 272, 256), (16, 512, 1280), (17, 1040, 384), (37, 2112, 1280),
           (64, 128, 256), (65, 400, 128), (77, 2112, 640), (130, 256, 384), (257, 1040, 256), (300, 144, 896),
           (40, 64, 8320), (90, 8320, 128), (600, 640, 512),
-          (700, 144, 2688), (2000, 144, 2688), (2000, 144, 3840), (4200, 144, 3840)]   # larger tiles
+          (700, 144, 2688), (2000, 144, 2688), (2000, 144, 3840), (4200, 144, 3840),   # larger tiles
+          (700, 144, 3840), (3000, 144, 3840), (600, 8336, 3840), (1000, 8336, 5120), (2000, 8336, 3840),
+          # few rows: each number of 16-row tiles of either operand, and passes
+          (17, 1520, 128), (20, 2512, 4224), (49, 2512, 128), (40, 3008, 4224), (50, 4112, 4224), (17, 4496, 8320),
+          (33, 6976, 8320), (49, 12432, 8320), (1, 16400, 8320), (2, 64, 16640), (1, 16, 24704), (1, 32, 32768)]
 
 
 def block(M, H, I):
