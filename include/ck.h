@@ -447,8 +447,12 @@ ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, cons
  * with a <= 448 s (1 for a block of zeros), and a code is e4m3(x / s), nearest even,
  * ties to even: x / s is exact, so this is the only rounding.  A block that holds a
  * NaN or an infinity gives NaN in every result of its row (of its columns, in a weight).
- * Sums are fp32, rounded once to the result's type.  Range: products whose scales add up
- * beyond fp32's exponents overflow or vanish as fp32 does.
+ * Sums are fp32, rounded once to the result's type; the e4m3 matrix core, which serves all
+ * but a few rows, adds eight neighbouring products at a time and drops what lies 2^-13
+ * below the largest.  How many rows a call has decides which kernel adds them and in what
+ * order, so that a row's last bits may differ from one M to another; the same call gives
+ * the same bits.  Range: products whose scales add up beyond fp32's exponents overflow or
+ * vanish as fp32 does.
  */
 
 /* ck_fp8_quant: codes and scales of bf16 x [M, ldx], K columns. */
@@ -475,11 +479,13 @@ ck_status ck_fp8_gemm(const uint8_t *codes, int64_t ldq, const uint8_t *scales, 
                       const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t N, const uint16_t *bias,
                       uint16_t *out, int64_t ldo, void *stream);
 
-/* Bytes of workspace ck_fp8_linear needs: codes and scales of M rows of K columns.  A
- * workspace of some M, K and N serves every call with no more of each.  0 for sizes it refuses. */
+/* Bytes of workspace ck_fp8_linear needs: codes and scales of M rows of K columns and up to 8 MB
+ * for the sums of a product that is split over K.  A workspace of some M, K and N serves every
+ * call with no more of each.  0 for sizes it refuses. */
 size_t ck_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
-/* ck_fp8_linear: ck_fp8_quant into the workspace, then ck_fp8_gemm (x bf16 [M, ldx]). */
+/* ck_fp8_linear: ck_fp8_quant into the workspace, then ck_fp8_gemm (x bf16 [M, ldx]), whose sums
+ * it may add in another order. */
 ck_status ck_fp8_linear(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint8_t *w, int64_t ldw,
                         const uint8_t *w_scales, int64_t N, const uint16_t *bias, uint16_t *out, int64_t ldo,
                         void *ws, size_t ws_bytes, void *stream);

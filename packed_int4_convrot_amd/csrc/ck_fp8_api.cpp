@@ -132,17 +132,21 @@ bool serves(int64_t M, int64_t K, int64_t of) { return M > 0 && M <= kMaxRows &&
 
 size_t linear_bytes(int64_t M, int64_t K, int64_t N)
 {
-    return serves(M, K, 16) && N > 0 && N % 16 == 0 && N <= kMaxRows ? quantised_bytes(M, K) : 0;
+    return serves(M, K, 16) && N > 0 && N % 16 == 0 && N <= kMaxRows
+               ? quantised_bytes(M, K) + round_up((size_t)ck::fp8_split_floats(M, K, N) * sizeof(float), kWsAlign)
+               : 0;
 }
-// fp32 results of the few-row products, between a block's two.
-size_t sums_bytes(int64_t M, int64_t I)
+// fp32 results of the few-row products, between a block's two; then the sums of the second, where
+// it is split.
+size_t sums_bytes(int64_t M, int64_t H, int64_t I)
 {
-    return round_up((size_t)((M < ck::kFp8FewRows ? M : ck::kFp8FewRows) * I) * sizeof(float), kWsAlign);
+    const int64_t few = (M < ck::kFp8FewRows ? M : ck::kFp8FewRows) * I, split = ck::fp8_split_floats(M, I, H);
+    return round_up((size_t)(few > split ? few : split) * sizeof(float), kWsAlign);
 }
 // x, what lies between the two products, and its fp32 form.
 size_t pair_bytes(int64_t M, int64_t H, int64_t inner)
 {
-    return quantised_bytes(M, H) + quantised_bytes(M, inner) + sums_bytes(M, inner);
+    return quantised_bytes(M, H) + quantised_bytes(M, inner) + sums_bytes(M, H, inner);
 }
 size_t ffn_bytes(int64_t M, int64_t H, int64_t I)
 {
@@ -153,14 +157,23 @@ size_t backward_bytes(int64_t M, int64_t H, int64_t I)
     return serves(M, H, 16) && serves(M, I, 128) ? pair_bytes(M, H, 2 * I) : 0;
 }
 
-bool few(ck::Fp8Result kind, const ck::Fp8Product &p)
+// A product on the kernel that takes the least time.  sums: room for the few-row product's fp32
+// results and for a split product's, or null.
+struct Choice {
+    ck::Fp8Plan plan;
+    bool few;
+};
+Choice choose(ck::Fp8Result kind, const ck::Fp8Product &p, bool room)
 {
-    return ck::fp8_few(kind, p.M, p.K, kind == ck::Fp8Result::kBf16 ? p.N : p.I);
+    const int64_t cols = kind == ck::Fp8Result::kBf16 ? p.N : p.I;
+    const ck::Fp8Plan plan = ck::fp8_plan(kind, p.M, p.K, cols, room);
+    return {plan, ck::fp8_few(kind, p.M, p.K, cols, plan)};
 }
 int from_codes(ck::Fp8Result kind, const ck::Fp8Product &p, float *sums, void *stream)
 {
-    return few(kind, p) ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
-                        : ck::launch_fp8_tiled(kind, p, stream);
+    const Choice c = choose(kind, p, sums != nullptr);
+    return c.few ? ck::launch_fp8_few(kind, p, nullptr, false, 0, sums, stream)
+                 : ck::launch_fp8_tiled(kind, p, c.plan, sums, stream);
 }
 
 // A product of bf16 (or fp32) rows: quantised on the way where that pays, through q otherwise.
@@ -187,10 +200,10 @@ int two_products(ck::Fp8Result kind, ck::Fp8Product &first, ck::Fp8Product &seco
     const int e = from_rows(kind, first, x, false, ldx, q, sums, stream);
     if (e != 0)
         return e;
-    if (ck::fp8_few_raw(first.M, first.K) || few(kind, first))
-        return from_rows(ck::Fp8Result::kBf16, second, sums, true, second.K, h, nullptr, stream);
+    if (ck::fp8_few_raw(first.M, first.K) || choose(kind, first, true).few)
+        return from_rows(ck::Fp8Result::kBf16, second, sums, true, second.K, h, sums, stream);
     second.a = h.codes, second.lda = second.K, second.sa = h.scales, second.ldsa = h.stride;
-    return from_codes(ck::Fp8Result::kBf16, second, nullptr, stream);
+    return from_codes(ck::Fp8Result::kBf16, second, sums, stream);
 }
 
 int quant_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, uint8_t *codes, int64_t ldq, uint8_t *scales,
@@ -305,7 +318,7 @@ int linear_impl(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, const uint
     const Quantised q = take(at, M, K);
     ck::Fp8Product p = product(M, K, w, ldw, w_scales, N);
     p.bias = bias, p.out = out, p.ldo = ldo;
-    return hip_status(from_rows(ck::Fp8Result::kBf16, p, x, false, ldx, q, nullptr, stream), fn);
+    return hip_status(from_rows(ck::Fp8Result::kBf16, p, x, false, ldx, q, reinterpret_cast<float *>(at), stream), fn);
 }
 
 int check_ffn(const char *fn, int64_t M, int64_t H, int64_t I, const uint8_t *w1, const uint8_t *s1, const uint8_t *w2,

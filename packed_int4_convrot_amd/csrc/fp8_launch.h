@@ -30,6 +30,7 @@ enum class Fp8Result {
     kBf16,   // bf16 (sums + bias)
     kGated,  // of 2 I weight rows, gate then up: silu(g) u, quantised; g and u in bf16 where gate_up is given
     kGrad,   // d(gate) and d(up) of silu(g) u from sums dh and given g and u, quantised
+    kSums,   // fp32, a tile's as the matrix core leaves them: part of a split kBf16
 };
 struct Fp8Product {
     const uint8_t *a, *sa;   // activations
@@ -49,29 +50,50 @@ struct Fp8Product {
     int64_t ldg;
     uint8_t *q, *sq;         // the quantised result [M, I] or [M, 2 I]
     int64_t ldsq;
+    // kSums: steps of a split, and the splits' sums
+    int each;
+    float *sums;
 };
-// Tiles of the tiled product, weight rows x activation rows: 256 x 256, 256 x 128, 128 x 128
-// (two workgroups a CU; not for kGated, whose tiles cover 128 columns of gate and of up).
+// Tiles of the tiled product, weight rows x activation rows.  kGated's cover 128 columns of gate and of
+// up, so it has those of 256 weight rows, 256 x 64 by itself; kGrad has no 64 x 64, half a block of 128.
 enum class Fp8Tile { k256x256, k256x192, k256x128, k256x64, k128x128, k128x64, k64x64 };
 constexpr int kFp8Cus = 256;
 // Workgroups of 512 threads that one launch takes, and those of a product on 128 x 128 tiles, which
 // the entry points hold against it.
 constexpr int64_t kFp8MaxTiles = (int64_t(1) << 32) / 512 - 1;
 inline int64_t fp8_tiles(int64_t M, int64_t N) { return fp8_blocks(M) * fp8_blocks(N); }
-// The tile with the least rounds times time of a step: those of the table, in hundredths of a
-// microsecond, with a workgroup on every CU.  Measured, the quantiser included, in the table's
-// order (256 x 64 only for kGated, which has none below): 128 x 3840 x 10240 (rows, K, N)
-// 39.0 / 34.0 / 26.3 / - / 18.9 / 16.0 / 18.5 us, 256 x 3840 x 3840 39.6 / 34.6 / 26.5 / - / 19.0 /
-// 16.0 / 14.3, 512 x 10240 x 3840 91.0 / 77.6 / 59.3 / - / 40.9 / 36.4 / 42.2, 700 x 3840 x 3840
-// 40.6 / 35.3 / 27.6 / - / 21.7 / 28.2 / 27.6, 2048 x 3840 x 3840 45.7 / 41.5 / 36.8 / - / 43.2 /
-// 56.2 / 60.3, 2000 x 3840 x 10240 92 / 83 / 92 / - / 99 / 131 / 140, 8192 x 10240 x 3840 286 / 326 /
-// 346 / - / 416 / 528 / 576.  Feed-forward block of 77 rows, H 2112, I 1280: 31.4 / 28.7 / 23.5 /
-// 20.1; of 2000, H 2048, I 5120: 81.6 / 78.1 / 81.8 / 90.9.
+// The plan that takes the least time: 3200 ns (1000 more with the activation), and for each round
+// of tiles over the CUs and each step of 128 columns 7 ns times the cost in the table below.
+// Measured in us, the quantiser included, on 256 x 256 / 256 x 192 / 256 x 128 / 128 x 128 / 128 x 64 /
+// 64 x 64 tiles, whole (rows x K x N):
+//    128 x  3840 x 10240   39.0 / 34.0 / 26.3 / 18.9 / 16.0 / 18.5
+//    256 x  3840 x  3840   39.6 / 34.6 / 26.5 / 19.0 / 16.0 / 14.3
+//    700 x  3840 x  3840   40.6 / 35.3 / 27.6 / 21.7 / 28.2 / 27.6
+//   2048 x  3840 x  3840   45.7 / 41.5 / 36.8 / 43.2 / 56.2 / 60.3
+//   2000 x  3840 x 10240   92 / 83 / 92 / 99 / 131 / 140
+//   8192 x 10240 x  3840   286 / 326 / 346 / 416 / 528 / 576
+// and with 256 x 256 / 256 x 192 / 256 x 128 / 256 x 64 under the activation, feed-forward blocks (rows,
+// H, I): 77, 2112, 1280 31.4 / 28.7 / 23.5 / 20.1; 2000, 2048, 5120 81.6 / 78.1 / 81.8 / 90.9.
+//
+// kBf16 on the two smallest tiles may split K over `splits` workgroups, each of `each` steps (a
+// multiple of four), whose fp32 sums go through the workspace and a launch that adds them: 1900 ns,
+// and 2.5 for a thousand sums.  Whole / split: 100 x 10240 x 3840 26.4 / 18.2, 100 x 20480 x 3840
+// 47.2 / 25.7, 128 x 8192 x 1024 22.9 / 13.1, 2000 x 20480 x 256 64 / 43, 100 x 3840 x 1040 13.2 / 11.2;
+// 100 x 2112 x 1040 stays whole, 10.0 / 10.6.  Backward pass of 100 rows, H 3840, I 10240: 68.6 / 49.4.
 struct Fp8Plan {
     Fp8Tile tile;
-    int64_t cost;   // of a step
+    int64_t splits, each;
+    int64_t time;
 };
-inline Fp8Plan fp8_plan(Fp8Result kind, int64_t M, int64_t columns)
+constexpr int64_t kFp8MostSplits = 8, kFp8SplitArea = int64_t(kFp8Cus) * 128 * 64;   // elements of all sums
+// Floats that a split product's sums need at most.  Fewer rows need no more.
+inline int64_t fp8_split_floats(int64_t M, int64_t K, int64_t N)
+{
+    const int64_t m = M < (1 << 14) ? (M + 63) / 64 * 64 : 1 << 14, n = N < (1 << 15) ? fp8_blocks(N) * 128 : 1 << 15;
+    const int64_t most = kFp8MostSplits * m * n;
+    return K < 16 * kFp8Block ? 0 : most < kFp8SplitArea ? most : kFp8SplitArea;
+}
+inline Fp8Plan fp8_plan(Fp8Result kind, int64_t M, int64_t K, int64_t columns, bool may_split)
 {
     struct Shape {
         Fp8Tile tile;
@@ -83,20 +105,29 @@ inline Fp8Plan fp8_plan(Fp8Result kind, int64_t M, int64_t columns)
         {Fp8Tile::k64x64, 64, 64, 33},
     };
     const bool gated = kind == Fp8Result::kGated;
-    Fp8Plan best{Fp8Tile::k256x256, INT64_MAX};
+    const int64_t steps = fp8_blocks(K);
+    Fp8Plan best{Fp8Tile::k256x256, 1, steps, INT64_MAX};
     for (const Shape &s : shapes) {
         if (gated ? s.n < 256 : s.n == 256 && s.m == 64)
             continue;
         if (kind == Fp8Result::kGrad && s.n < 128)
             continue;
         const int64_t tiles = (columns * (gated ? 2 : 1) + s.n - 1) / s.n * ((M + s.m - 1) / s.m);
-        const int64_t cost = s.cost * ((tiles + kFp8Cus - 1) / kFp8Cus);
-        if (cost < best.cost && tiles <= kFp8MaxTiles)
-            best = Fp8Plan{s.tile, cost};
+        if (tiles > kFp8MaxTiles)
+            continue;
+        const bool splits = may_split && kind == Fp8Result::kBf16 && s.m == 64 && K >= 16 * kFp8Block;
+        for (int64_t n = 1; n <= (splits ? kFp8MostSplits : 1) && (n == 1 || n * tiles <= kFp8Cus); ++n) {
+            const int64_t each = n == 1 ? steps : ((steps + n - 1) / n + 3) / 4 * 4;
+            const int64_t rounds = (tiles + kFp8Cus - 1) / kFp8Cus;
+            const int64_t join = n == 1 ? 0 : 1900 + n * tiles * s.m * s.n / 400;
+            const int64_t time = (gated ? 4200 : 3200) + 7 * s.cost * each * rounds + join;
+            if (time < best.time)
+                best = Fp8Plan{s.tile, (steps + each - 1) / each, each, time};
+        }
     }
     return best;
 }
-int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream);
+int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream);
 
 // The few-row product.  x given: bf16 or fp32 rows, quantised on the way (fp8_few_raw), a and sa
 // unused; null: the codes and scales.  kGated and kGrad write fp32 [M, I] or [M, 2 I] to sums.
@@ -106,22 +137,26 @@ inline bool fp8_few_raw(int64_t M, int64_t K) { return M <= kFp8RawRows && M * (
 // Columns that rows of codes, in tiles of 16, take at most: wider ones the tiles do faster.
 constexpr int64_t fp8_few_columns(Fp8Result kind, int64_t rows16)
 {
-    return kFp8Cus * 16 * (kind == Fp8Result::kGated || (kind == Fp8Result::kBf16 && rows16 > 2) ? 2 : 3);
+    const int most = rows16 == 1 ? 3 : rows16 == 2 ? 2 : 1;
+    return kFp8Cus * 16 * (kind == Fp8Result::kBf16 ? most : most < 3 ? most + 1 : 3);
 }
-// Whether it serves rows of codes: where the rows' scales fit LDS beside 128 KB of rings, and where it takes
-// less time than the tiles, whose time is that of a step after a step.  Nanoseconds, lines through
-// times that were measured; few rows / tiles in microseconds, both with the quantiser, (rows, K,
-// N): 16 x 3840 x 3840 9.6 / 13.1, 64 x 3840 x 3840 13.0 / 13.3, 16 x 3840 x 10240 13.7 / 13.5,
-// 48 x 10240 x 3840 17.2 / 25.5, 16 x 2112 x 1040 8.1 / 9.7, 32 x 2048 x 20480 18.9 / 12.7.
-inline bool fp8_few(Fp8Result kind, int64_t M, int64_t K, int64_t columns)
+// Whether it serves rows of codes: where the rows' scales fit LDS beside 128 KB of rings, and where
+// it takes less time than the tiles.  Both in nanoseconds, lines through measured times: the weights'
+// way from memory, every workgroup's way through all rows, the quantiser of fp32 results.
+// Measured in us, few rows / tiles, both with the quantiser (rows x K x N), weights in a cache:
+// 16 x 3840 x 3840 9.0 / 11.9, 64 x 3840 x 3840 13.3 / 12.2, 16 x 3840 x 10240 13.4 / 13.6, 64 x 10240 x 3840
+// 19.1 / 16.0; weights from memory: 16 x 3840 x 3840 10.4 / 12.8, 16 x 3840 x 10240 14.9 / 16.1, 64 x 10240 x
+// 3840 23.7 / 20.0; feed-forward block of 16 rows, H 3840, I 10240: 40.8 / 48.2, of 64 rows 55.7 / 51.7.
+inline bool fp8_few(Fp8Result kind, int64_t M, int64_t K, int64_t columns, const Fp8Plan &plan)
 {
     const int64_t rows16 = (M + 15) / 16;
     if (M > kFp8FewRows || M * fp8_scale_stride(K) > 16 * 1024 || columns > fp8_few_columns(kind, rows16))
         return false;
-    const int64_t weights = K * columns * (kind == Fp8Result::kGated ? 2 : 1) / 1000;
-    const int64_t quantiser = kind == Fp8Result::kBf16 ? 0 : 2500;   // of its fp32 results
-    const int64_t few = 3600 + 600 * rows16 + weights * (140 + 28 * rows16) / 1000 + quantiser;
-    return few < 3200 + 7 * fp8_blocks(K) * fp8_plan(kind, M, columns).cost;
+    const int64_t weights = columns * (kind == Fp8Result::kGated ? 2 : 1), tiles = (weights + 4095) / 4096;
+    const int64_t quantiser = kind == Fp8Result::kBf16 ? 0 : 1500;   // of its fp32 results
+    const int64_t few = 3800 + K * weights / 4600 + rows16 * (300 + 24 * fp8_blocks(K)) * (tiles + 3) / 4 + quantiser;
+    const int64_t from_memory = 3200 + K * weights / 3300;
+    return few < (plan.time > from_memory ? plan.time : from_memory);
 }
 int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums,
                    void *stream);

@@ -12,8 +12,16 @@
 //
 // A workgroup has kWn x kWm waves, a wave kTn x kTm tiles of 32 x 32.  A stage is one
 // block of 128 columns of every row of both operands, 128 bytes a row, moved from
-// global memory to LDS directly into two buffers; the 16-byte slots of a row are
-// XORed with bits of the row so that the lanes of a fragment's read meet in no bank.
+// global memory to LDS directly into two buffers, four for the small tiles; the 16-byte
+// slots of a row are XORed with bits of the row so that the lanes of a fragment's read
+// meet in no bank.
+//
+// What bounds it: on the 256-wide tiles the matrix core under the chip's power, at about 1.6 GHz a
+// step of 256 x 256 takes 1.45 us, 1.2 with its loads left out; 8192 x 3840 x 10240 takes LARGE_US us,
+// LARGE_PF PFLOP/s, and 256 x 256 tiles of four waves, which read a third less LDS, 2 % more.  On the
+// small tiles a step's way through barrier, LDS and two products, 0.24 us for 64 x 64: eight buffers
+// and steps shared out to two or four teams of a workgroup's waves took as long; splitting K over
+// workgroups is what helps.
 //
 // kGated: a wave's tiles are half gate rows and half up rows of the same columns, so that
 // the activation and the product happen in registers; a workgroup covers the 128
@@ -38,6 +46,17 @@ __device__ __forceinline__ void wait_reads_and_loads()
 {
     static_assert(N < 64, "vmcnt");
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+
+// Registers 8 g .. 8 g + 7 of a lane's row of a 32 x 32 result in bf16: the two lanes of a row exchange
+// halves, and this one has columns 16 g + 8 half on.
+__device__ __forceinline__ u32x4 bf16x8(const float *v)
+{
+    uint32_t x0 = pack_bf16x2(v[0], v[1]), x1 = pack_bf16x2(v[2], v[3]);
+    uint32_t y0 = pack_bf16x2(v[4], v[5]), y1 = pack_bf16x2(v[6], v[7]);
+    swap_halves(x0, y0);
+    swap_halves(x1, y1);
+    return u32x4{x0, x1, y0, y1};
 }
 
 template <int kWn_, int kWm_, int kTn_, int kTm_, int kStages_ = 2>
@@ -69,7 +88,10 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / kWave), lane = t % kWave;
     const int wn = wave / T::kWm, wm = wave % T::kWm;
     const int l32 = lane % 32, half = lane / 32;
-    const int K = p.K, steps = (K + 127) / 128;
+    // Of a split product a workgroup takes blockIdx.y's steps.
+    constexpr bool kSplit = kKind == Fp8Result::kSums;
+    const int all_steps = (p.K + 127) / 128, step0 = kSplit ? blockIdx.y * p.each : 0;
+    const int K = kSplit ? min(p.K - step0 * 128, p.each * 128) : p.K, steps = (K + 127) / 128;
 
     // Runs of kGroupM tile rows are walked column by column, a contiguous run on each XCD.
     constexpr int kGroupM = 4;
@@ -83,12 +105,13 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     const int rows = (int)min((int64_t)kBm, p.M - m0);
     // Operand rows past the end and columns past K read as zero (out of the buffer's range).
     const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(p.a + m0 * p.lda), (short)0, (int)((rows - 1) * p.lda + K), 0x00020000);
+        (void *)(p.a + m0 * p.lda + step0 * 128), (short)0, (int)((rows - 1) * p.lda + K), 0x00020000);
     const int w_rows = kGated ? p.I + kBn / 2 : min(kBn, p.N - n0);
     const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(p.w + n0 * p.ldw), (short)0, (int)((w_rows - 1) * p.ldw + K), 0x00020000);
+        (void *)(p.w + n0 * p.ldw + step0 * 128), (short)0, (int)((w_rows - 1) * p.ldw + K), 0x00020000);
     const __amdgpu_buffer_rsrc_t sa_rsrc =
-        __builtin_amdgcn_make_buffer_rsrc((void *)(p.sa + m0 * p.ldsa), (short)0, (int)(rows * p.ldsa), 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.sa + m0 * p.ldsa + step0), (short)0, (int)(rows * p.ldsa - step0),
+                                          0x00020000);
     constexpr int kPast = 0x7fffffff;
     constexpr int kALoads = kBm * 128 / (kWaves * 1024), kWLoads = kBn * 128 / (kWaves * 1024);
     static_assert(kALoads * kWaves * 1024 == kBm * 128 && kWLoads * kWaves * 1024 == kBn * 128, "whole loads");
@@ -133,7 +156,7 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
         constexpr int kParts = kBm / kWave, kEach = 16 * kParts / kWaves;
         static_assert(kEach * kWaves == 16 * kParts, "whole loads");
         const int sw_row = min(n0 / 128 + t / 64 % 2 * far, block_rows - 1);
-        sw_in = p.sw[(int64_t)sw_row * steps + min(first + t % 64, steps - 1)];
+        sw_in = p.sw[(int64_t)sw_row * all_steps + step0 + min(first + t % 64, steps - 1)];
 #pragma unroll
         for (int n = 0; n < kEach; ++n) {
             const int e = n * kWaves + wave, part = e % kParts, four = e / kParts;
@@ -262,15 +285,7 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
         swap_halves(c[1], c[3]);
         return u32x4{c[0], c[2], c[1], c[3]};
     };
-    // Columns 32 i + 16 g + 8 half .. of a tile in bf16, g = 0 and 1.
-    auto bf16x8 = [&](const float *v) {   // registers 8 g .. 8 g + 7
-        uint32_t x0 = pack_bf16x2(v[0], v[1]), x1 = pack_bf16x2(v[2], v[3]);
-        uint32_t y0 = pack_bf16x2(v[4], v[5]), y1 = pack_bf16x2(v[6], v[7]);
-        swap_halves(x0, y0);
-        swap_halves(x1, y1);
-        return u32x4{x0, x1, y0, y1};
-    };
-    // The reverse, to fp32.
+    // The reverse of bf16x8, to fp32.
     auto floats8 = [&](u32x4 x, float *v) {
         uint32_t d[4] = {x[0], x[1], x[2], x[3]};
         swap_halves(d[0], d[2]);
@@ -393,6 +408,15 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     wait_vmcnt0();   // loads past the last step
     lds_barrier();
 
+    if constexpr (kSplit) {
+        static_assert(kTn == 1 && kTm == 1, "one tile a wave");
+        v4f *to = reinterpret_cast<v4f *>(p.sums) +
+                  ((((int64_t)blockIdx.y * tiles + m0 / kBm * tiles_n + n0 / kBn) * kWaves + wave) * 4) * kWave + lane;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            to[q * kWave] = v4f{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+        return;
+    }
     const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
     if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
 #pragma unroll
@@ -497,8 +521,43 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     }
 }
 
+// Adds a split product's sums in the order of its splits.  A wave has a 32 x 32 tile of the result.
+template <class T>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Product p, int splits, int tiles, int tiles_n)
+{
+    const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
+    const int w = blockIdx.x * 4 + threadIdx.x / kWave, tile = w / T::kWaves, wave = w % T::kWaves;
+    const int64_t m = (int64_t)(tile / tiles_n) * T::kBm + wave % T::kWm * 32 + l32;
+    const int n = tile % tiles_n * T::kBn + wave / T::kWm * 32;
+    const v4f *from = reinterpret_cast<const v4f *>(p.sums) + (int64_t)w * 4 * kWave + lane;
+    float s[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        s[r] = 0.f;
+#pragma unroll 2
+    for (int z = 0; z < splits; ++z)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const v4f x = from[((int64_t)z * tiles * T::kWaves * 4 + q) * kWave];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                s[4 * q + r] += x[r];
+        }
+    if (p.bias)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            s[r] += bf16_to_f32(p.bias[min(n + r / 4 * 8 + 4 * half + r % 4, p.N - 1)]);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const u32x4 x = bf16x8(s + 8 * g);
+        const int c = n + 16 * g + 8 * half;
+        if (m < p.M && c < p.N)
+            *reinterpret_cast<u32x4 *>(p.out + m * p.ldo + c) = x;
+    }
+}
+
 template <class T, Fp8Result kKind>
-int launch_tile(const Fp8Product &p, void *stream)
+int launch_tile(const Fp8Product &p, int64_t splits, void *stream)
 {
     auto kern = fp8_tiled_kernel<T, kKind>;
     static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
@@ -507,40 +566,62 @@ int launch_tile(const Fp8Product &p, void *stream)
     if (attr != hipSuccess)
         return (int)attr;
     const int64_t tiles_m = (p.M + T::kBm - 1) / T::kBm;
-    const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
+    const int cols = kKind == Fp8Result::kGated || kKind == Fp8Result::kGrad ? p.I : p.N;
     const int width = kKind == Fp8Result::kGated ? T::kBn / 2 : T::kBn;
     const int64_t tiles = tiles_m * ((cols + width - 1) / width);
-    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(T::kWaves * kWave), T::kLds,
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles, (unsigned)splits), dim3(T::kWaves * kWave), T::kLds,
                        reinterpret_cast<hipStream_t>(stream), p, (int)tiles_m, (int)tiles);
-    return (int)hipGetLastError();
+    const int e = (int)hipGetLastError();
+    if constexpr (kKind == Fp8Result::kSums) {
+        if (e != 0)
+            return e;
+        hipLaunchKernelGGL(fp8_join_kernel<T>, dim3((unsigned)(tiles * T::kWaves / 4)), dim3(256), 0,
+                           reinterpret_cast<hipStream_t>(stream), p, (int)splits, (int)tiles, (int)(tiles / tiles_m));
+        return (int)hipGetLastError();
+    }
+    return e;
+}
+
+// The two smallest tiles, split or not.
+template <class T>
+int launch_small(const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream)
+{
+    if (plan.splits == 1)
+        return launch_tile<T, Fp8Result::kBf16>(p, 1, stream);
+    Fp8Product part = p;
+    part.each = (int)plan.each, part.sums = sums;
+    return launch_tile<T, Fp8Result::kSums>(part, plan.splits, stream);
 }
 
 template <Fp8Result kKind>
-int launch_kind(const Fp8Product &p, void *stream)
+int launch_kind(const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream)
 {
-    constexpr bool kGated = kKind == Fp8Result::kGated;
-    switch (fp8_plan(kKind, p.M, kKind == Fp8Result::kBf16 ? p.N : p.I).tile) {
+    constexpr bool kGated = kKind == Fp8Result::kGated, kGrad = kKind == Fp8Result::kGrad;
+    using Narrow = Tile<4, 2, 1, 1, 4>;
+    switch (plan.tile) {
     case Fp8Tile::k256x256:
-        return launch_tile<Tile<2, 4, 4, 2>, kKind>(p, stream);
+        return launch_tile<Tile<2, 4, 4, 2>, kKind>(p, 1, stream);
     case Fp8Tile::k256x192:
-        return launch_tile<Tile<4, 2, 2, 3>, kKind>(p, stream);
+        return launch_tile<Tile<4, 2, 2, 3>, kKind>(p, 1, stream);
     case Fp8Tile::k256x128:
-        return launch_tile<Tile<4, 2, 2, 2>, kKind>(p, stream);
+        return launch_tile<Tile<4, 2, 2, 2>, kKind>(p, 1, stream);
     case Fp8Tile::k256x64:
         if constexpr (kGated)
-            return launch_tile<Tile<4, 2, 2, 1>, kKind>(p, stream);
+            return launch_tile<Tile<4, 2, 2, 1>, kKind>(p, 1, stream);
         break;
     case Fp8Tile::k128x128:
         if constexpr (!kGated)
-            return launch_tile<Tile<2, 4, 2, 1, 4>, kKind>(p, stream);
+            return launch_tile<Tile<2, 4, 2, 1, 4>, kKind>(p, 1, stream);
         break;
     case Fp8Tile::k128x64:
-        if constexpr (!kGated)
-            return launch_tile<Tile<4, 2, 1, 1, 4>, kKind>(p, stream);
+        if constexpr (kGrad)
+            return launch_tile<Narrow, kKind>(p, 1, stream);
+        else if constexpr (!kGated)
+            return launch_small<Narrow>(p, plan, sums, stream);
         break;
     case Fp8Tile::k64x64:
         if constexpr (kKind == Fp8Result::kBf16)
-            return launch_tile<Tile<2, 2, 1, 1, 4>, kKind>(p, stream);
+            return launch_small<Tile<2, 2, 1, 1, 4>>(p, plan, sums, stream);
         break;
     }
     return (int)hipErrorInvalidValue;
@@ -548,15 +629,17 @@ int launch_kind(const Fp8Product &p, void *stream)
 
 }  // namespace
 
-int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *stream)
+int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream)
 {
     switch (kind) {
     case Fp8Result::kBf16:
-        return launch_kind<Fp8Result::kBf16>(p, stream);
+        return launch_kind<Fp8Result::kBf16>(p, plan, sums, stream);
     case Fp8Result::kGated:
-        return launch_kind<Fp8Result::kGated>(p, stream);
+        return launch_kind<Fp8Result::kGated>(p, plan, sums, stream);
+    case Fp8Result::kGrad:
+        return launch_kind<Fp8Result::kGrad>(p, plan, sums, stream);
     default:
-        return launch_kind<Fp8Result::kGrad>(p, stream);
+        return (int)hipErrorInvalidValue;
     }
 }
 

@@ -129,8 +129,17 @@ int launch_fp8_transpose(const uint8_t *codes, int64_t ldw, const uint8_t *scale
     return finish();
 }
 
-int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *)
+int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, const Fp8Plan &plan, float *sums, void *)
 {
+    if (plan.splits > 1) {   // a tile's sums are written whole
+        EXPECT(kind == Fp8Result::kBf16 && sums != nullptr && plan.splits <= kFp8MostSplits && plan.each % 4 == 0);
+        EXPECT((plan.splits - 1) * plan.each < fp8_blocks(p.K) && plan.splits * plan.each >= fp8_blocks(p.K));
+        EXPECT(plan.tile == Fp8Tile::k128x64 || plan.tile == Fp8Tile::k64x64);
+        const int64_t n = plan.tile == Fp8Tile::k128x64 ? 128 : 64;
+        const int64_t floats = plan.splits * ((p.N + n - 1) / n * n) * ((p.M + 63) / 64 * 64);
+        EXPECT(floats <= fp8_split_floats(p.M, p.K, p.N));
+        write_span(sums, 1, floats, floats, 4);
+    }
     touch_product(kind, p);
     touch_rows(p);
     if (kind != Fp8Result::kBf16) {
@@ -142,7 +151,8 @@ int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, void *)
 
 int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums, void *)
 {
-    EXPECT(x || fp8_few(kind, p.M, p.K, kind == Fp8Result::kBf16 ? p.N : p.I));
+    const int64_t columns = kind == Fp8Result::kBf16 ? p.N : p.I;
+    EXPECT(x || columns <= fp8_few_columns(kind, (p.M + 15) / 16));
     EXPECT(p.M <= kFp8FewRows && p.M * fp8_scale_stride(p.K) <= 16 * 1024);
     touch_product(kind, p);
     if (x) {
@@ -264,19 +274,34 @@ void tiles()
                 const int64_t columns = kind == 0 ? N : (N + 127) / 128 * 128;
                 if (ck::fp8_tiles(M, columns * (kind == 1 ? 2 : 1)) > ck::kFp8MaxTiles)
                     continue;
-                const ck::Fp8Plan plan = ck::fp8_plan((ck::Fp8Result)kind, M, columns);
+                const ck::Fp8Plan plan = ck::fp8_plan((ck::Fp8Result)kind, M, 2048, columns, false);
+                EXPECT(plan.splits == 1 && plan.each == 16);
                 bool found = false;
                 for (int i = 0; i < 7; ++i)
                     if (sizes[i].tile == plan.tile) {
                         found = seen[kind][i] = true;
                         const int64_t rows = columns * (kind == 1 ? 2 : 1);
                         const int64_t grid = (rows + sizes[i].n - 1) / sizes[i].n * ((M + sizes[i].m - 1) / sizes[i].m);
-                        EXPECT(plan.cost > 0 && grid * 512 < (int64_t(1) << 32));
+                        EXPECT(plan.time > 0 && grid * 512 < (int64_t(1) << 32));
                         EXPECT(kind != 1 || sizes[i].n == 256);   // whole blocks of gate and up
                         EXPECT(kind != 2 || sizes[i].n >= 128);
                     }
                 EXPECT(found);
             }
+    EXPECT(ck::fp8_split_floats(INT32_MAX, 32768, INT32_MAX) == ck::kFp8SplitArea);
+    EXPECT(ck::fp8_split_floats(1, 32768, INT32_MAX) == ck::kFp8SplitArea && ck::fp8_split_floats(1, 1024, 4096) == 0);
+    // Room for a smaller call's sums is in a larger call's.
+    for (int64_t K = 16; K <= 32768; K += 2032)
+        for (int64_t N = 16; N < 40000; N = N * 3 / 16 * 8 + 16) {
+            int64_t room = 0;
+            for (int64_t M = 1; M < 5000; ++M) {
+                EXPECT(ck::fp8_split_floats(M, K, N) >= room);
+                room = ck::fp8_split_floats(M, K, N);
+                const ck::Fp8Plan plan = ck::fp8_plan(ck::Fp8Result::kBf16, M, K, N, true);
+                const int64_t n = plan.tile == ck::Fp8Tile::k128x64 ? 128 : 64;
+                EXPECT(plan.splits == 1 || plan.splits * ((N + n - 1) / n * n) * ((M + 63) / 64 * 64) <= room);
+            }
+        }
     for (int kind = 0; kind < 3; ++kind)
         for (int i = 0; i < 7; ++i)
             EXPECT(seen[kind][i] == (kind == 1 ? sizes[i].n == 256 : i != 3 && (kind == 0 || i != 6)));

@@ -115,8 +115,11 @@ LINEARS = [(1, 16, 16), (1, 3840, 512), (2, 144, 48), (5, 128, 1040), (8, 1024, 
            (500, 272, 3824), (1000, 400, 3824), (2000, 272, 3824), (3000, 144, 3856), (8191, 400, 2064), (4200, 144, 3856),
            (450, 8336, 3600), (900, 8336, 3600), (1800, 8336, 3600), (2800, 8336, 3600), (4100, 8336, 3600),
            # few rows: each number of 16-row tiles of either operand, and passes
-           (1, 16400, 4304), (2, 16400, 8256), (16, 2112, 4304), (30, 8208, 8256), (33, 4112, 4304), (50, 4112, 4304),
-           (60, 10256, 272), (1, 16, 33040), (3, 144, 50064), (2, 48, 24688)]
+           (1, 16400, 4304), (2, 16400, 8256), (16, 3840, 4304), (16, 3840, 11584), (30, 8208, 3600), (20, 4112, 4304), (40, 4112, 3600),
+           (33, 4112, 4304), (50, 4112, 3600), (1, 16, 33040), (3, 144, 50064), (2, 48, 24688),
+           # K split: 64 and 128 weight rows a tile, two to eight splits, the last ones short, more than a run of scales
+           (100, 3856, 1040), (65, 2064, 144), (64, 10240, 272), (130, 5120, 528), (500, 10256, 512), (2000, 20496, 272),
+           (9, 18880, 3664), (20, 10944, 11584), (200, 20480, 3600), (60, 32752, 272), (50, 32768, 10752)]
 
 
 @pytest.mark.parametrize("M,K,N", LINEARS)
@@ -162,8 +165,9 @@ BLOCKS = [(1, 16, 128), (1, 3840, 384), (2, 144, 128), (5, 272, 256), (16, 512, 
           (700, 144, 2688), (2000, 144, 2688), (2000, 144, 3840), (4200, 144, 3840),   # larger tiles
           (700, 144, 3840), (3000, 144, 3840), (600, 8336, 3840), (1000, 8336, 5120), (2000, 8336, 3840),
           # few rows: each number of 16-row tiles of either operand, and passes
-          (17, 1520, 128), (20, 2512, 4224), (49, 2512, 128), (40, 3008, 4224), (50, 4112, 4224), (17, 4496, 8320),
-          (33, 6976, 8320), (49, 12432, 8320), (1, 16400, 8320), (2, 64, 16640), (1, 16, 24704), (1, 32, 32768)]
+          (17, 1520, 128), (20, 3840, 4224), (49, 2512, 128), (40, 5008, 4224), (50, 6992, 4224), (16, 5008, 11648),
+          (20, 8464, 12288), (1, 16400, 8320), (2, 64, 16640), (1, 16, 24704), (1, 32, 32768),
+          (100, 272, 10240), (300, 512, 5120)]   # the second product's K split
 
 
 def block(M, H, I):
@@ -340,9 +344,9 @@ class Step:
         return [t.clone() for t in (self.y, self.out, self.kept, self.dx, self.dp)]
 
 
-@pytest.mark.parametrize("M", [1, 20, 64, 130, 1030])
-def test_a_run_together_captured_and_replayed(M):
-    H, I = 448, 384
+@pytest.mark.parametrize("M,H,I", [(1, 448, 384), (20, 448, 384), (64, 448, 384), (130, 448, 384), (1030, 448, 384),
+                                   (100, 2112, 4224)])
+def test_a_run_together_captured_and_replayed(M, H, I):
     step = Step(M, H, I, M)
     eager = step.run()
     y, out, kept, dx, dp = (t.double() for t in eager)
@@ -397,13 +401,14 @@ def test_two_graphs_and_two_streams():
         assert all(same(a, b) for a, b in zip(steps[i].results(), want[i]))
 
 
-@pytest.mark.parametrize("M", [1, 8, 33, 65, 300])
-def test_a_workspace_full_of_nan_changes_nothing(M):
+@pytest.mark.parametrize("M,H,I", [(1, 272, 256), (8, 272, 256), (33, 272, 256), (65, 272, 256), (300, 272, 256),
+                                   (20, 272, 8320), (100, 272, 4352), (130, 4112, 256)])
+def test_a_workspace_full_of_nan_changes_nothing(M, H, I):
     """And what a call leaves in it is not read by the next."""
-    H, I = 272, 256
     x, w1, w2 = block(M, H, I)
     ffn, weights = ck.Fp8Ffn(*w1, *w2), ck.Fp8Weights(*random_weight(144, H, 5, DEV))
-    space = torch.full((ck.fp8_ffn_backward_workspace_bytes(M, H, I),), 0xff, dtype=torch.uint8, device=DEV)
+    need = max(ck.fp8_ffn_backward_workspace_bytes(M, H, I), ck.fp8_linear_workspace_bytes(M, H, 144))
+    space = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
     want = ck.fp8_ffn(x, ffn), ck.fp8_linear(x, weights)
     for _ in range(2):
         assert same(ck.fp8_ffn(x, ffn, workspace=space), want[0])
