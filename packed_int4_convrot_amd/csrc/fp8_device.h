@@ -43,19 +43,18 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax)
     const int e = (int)((u + 0x1fffffu) >> 23) - 8;
     return u == 0 ? 127u : u >= 0x7f800000u ? 255u : (uint32_t)(e < 0 ? 0 : e);
 }
-// 1 / s of an e8m0 byte below 254 (0 for 255: codes of such a block are NaN or 0).
-__device__ __forceinline__ float e8m0_inverse(uint32_t byte)
-{
-    return byte >= 254 ? 0.f : __uint_as_float((254u - byte) << 23);
-}
+// The scale of an e8m0 byte as the conversions take it, which read its exponent bits (0: 2^-127,
+// 255: NaN).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Four fp32 to four e4m3, nearest even; |v| <= 448 or NaN.
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+// Four fp32 over a scale to four e4m3, nearest even; results of at most 448, or NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d, float scale)
 {
-    int r = 0;
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-    return (uint32_t)r;
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    v2s r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, r);
 }
 
 // The upper half of a and the lower half of b change places: lanes 0 .. 31 hold their own a and
@@ -86,8 +85,8 @@ __device__ __forceinline__ float logistic(float g)
 __device__ __forceinline__ float gated(float g, float u) { return g * logistic(g) * u; }
 __device__ __forceinline__ float2 gated_gradient(float d, float g, float u)
 {
-    const float s = logistic(g);
-    return float2{d * u * s * (1.f + g * (1.f - s)), d * g * s};  // dg, du
+    const float s = logistic(g), q = g * s;   // s (1 + g (1 - s)) = s + q (1 - s)
+    return float2{d * u * __builtin_fmaf(q, 1.f - s, s), d * q};  // dg, du
 }
 
 }  // namespace ck

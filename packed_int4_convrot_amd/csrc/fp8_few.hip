@@ -53,7 +53,6 @@ __device__ __forceinline__ v8bf values8(uint32_t lo, uint32_t hi, float s)
     const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
     return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // Division of 0 <= n < 2^16 by 1 <= d < 2^16: n ceil(2^32 / d) / 2^32 is less than 1 / d off.
 struct Divide {
@@ -68,7 +67,7 @@ struct Values {
 };
 __device__ __forceinline__ Values values32(u32x4 x, u32x4 y, uint32_t scale)
 {
-    const float s = scale_value(scale);
+    const float s = e8m0_value(scale);
     return Values{{values8(x[0], x[1], s), values8(x[2], x[3], s), values8(y[0], y[1], s), values8(y[2], y[3], s)}};
 }
 
@@ -229,10 +228,10 @@ __global__ __launch_bounds__(kThreads) void fp8_few_kernel(Fp8Product p, const v
                 for (int d = 1; d < 16; d *= 2)
                     a = fmaxf(a, __shfl_xor(a, d));
                 const uint32_t s = e8m0_of(a);
-                const float inv = e8m0_inverse(s);
+                const float by = e8m0_value(s);
                 if (i < chunks) {
-                    const u32x2 q = {pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                                     pack_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+                    const u32x2 q = {pack_e4m3x4(v[0], v[1], v[2], v[3], by),
+                                     pack_e4m3x4(v[4], v[5], v[6], v[7], by)};
                     *(__attribute__((address_space(3))) u32x2 *)(codes + c.x * pitch + c.y) = q;
                     if (i % 16 == 0)
                         sa[c.x * sa_pitch + c.y / 128] = (uint8_t)s;

@@ -23,12 +23,12 @@ __device__ __forceinline__ float abs_max16(const float (&v)[16])
     return a;
 }
 
-__device__ __forceinline__ u32x4 codes16(const float (&v)[16], float inv)
+__device__ __forceinline__ u32x4 codes16(const float (&v)[16], float scale)
 {
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        r[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        r[i] = pack_e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
     return r;
 }
 
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(kThreads) void fp8_quant_kernel(const void *__restr
         a = fmaxf(a, __shfl_xor(a, 4));
         const uint32_t s = e8m0_of(a);
         if (k < K) {
-            *reinterpret_cast<u32x4 *>(codes + m * lda + k) = codes16(v, e8m0_inverse(s));
+            *reinterpret_cast<u32x4 *>(codes + m * lda + k) = codes16(v, e8m0_value(s));
             if (lane % 8 == 0)
                 scales[m * ldsa + k / kFp8Block] = (uint8_t)s;
         }
@@ -119,12 +119,12 @@ __global__ __launch_bounds__(kThreads) void fp8_weight_kernel(const uint16_t *__
     __syncthreads();
     a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
     const uint32_t s = e8m0_of(a);
-    const float inv = e8m0_inverse(s);
+    const float by = e8m0_value(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = bn * kFp8Block + i * 32 + threadIdx.x / 8;
         if (n < N && k < K)
-            *reinterpret_cast<u32x4 *>(codes + n * ldw + k) = codes16(v[i], inv);
+            *reinterpret_cast<u32x4 *>(codes + n * ldw + k) = codes16(v[i], by);
     }
     if (threadIdx.x == 0)
         scales[(int64_t)bn * gridDim.x + bk] = (uint8_t)s;

@@ -276,11 +276,11 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     // its columns from 32 i + 8 q + 4 half on.  The two lanes of a row exchange halves, so that
     // each has 16 bytes that lie together.
     // Columns 32 i + 16 h .. of a tile's codes, h = half.
-    auto codes16 = [&](const float(&v)[16], float inv) {
+    auto codes16 = [&](const float(&v)[16], float scale) {
         uint32_t c[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            c[q] = pack_e4m3x4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv, v[4 * q + 3] * inv);
+            c[q] = pack_e4m3x4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], scale);
         swap_halves(c[0], c[2]);
         swap_halves(c[1], c[3]);
         return u32x4{c[0], c[2], c[1], c[3]};
@@ -312,13 +312,13 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
             lds_barrier();   // read before the next row's is written
         }
         const uint32_t s = e8m0_of(a);
-        const float inv = e8m0_inverse(s);
+        const float by = e8m0_value(s);
         const bool inside = m < rows && n < p.I;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
             float v[16];
             tile(i, v);
-            const u32x4 c = codes16(v, inv);
+            const u32x4 c = codes16(v, by);
             if (inside)
                 *reinterpret_cast<u32x4 *>(dst + 32 * i + 16 * half) = c;
         }
@@ -345,6 +345,21 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
         }
     };
     static_assert(kKind != Fp8Result::kGrad || kWaves * kTn * 4 * kWave * 16 <= kStages * T::kStage, "du fits the stages");
+
+    const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
+    // kGrad reads a tile's g and u while the one before is worked on, the first under the last step
+    // of large tiles (2000 rows, H 1024, I 4096: 50.9 us, each at its time 54.0; 1024 rows, H 2048, I
+    // 5120: 56.4, 58.8; 77 rows, H 2112, I 1280: 21.9 also under a small tile's, 21.5 after).
+    constexpr int kAhead = kKind == Fp8Result::kGrad ? 1 : 0;
+    u32x4 kept[kAhead + 1][4];
+    auto load_piece = [&](int piece) {
+        const int m = wm * kTm * 32 + piece / kTn * 32 + l32;
+        const uint16_t *g = p.gate_up + (m0 + min(m, rows - 1)) * p.ldg + (nw < p.I ? nw : p.I - kTn * 32) +
+                            piece % kTn * 32 + 8 * half;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            kept[piece % (kAhead + 1)][x] = *reinterpret_cast<const u32x4 *>(g + x / 2 * p.I + x % 2 * 16);
+    };
 
     first_loads();
 #pragma unroll
@@ -394,6 +409,8 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
         wait_vmcnt0();
         lds_barrier();
     }
+    if constexpr (kKind == Fp8Result::kGrad && kStages == 2)
+        load_piece(0);
     all_but_last(steps - 1);
 #pragma unroll
     for (int j = 0; j < kTm; ++j)
@@ -417,7 +434,6 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
             to[q * kWave] = v4f{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
         return;
     }
-    const int nw = n0 + wn * (kGated ? kTn / 2 : kTn) * 32;   // the wave's first column
     if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
 #pragma unroll
         for (int i = 0; i < kTn; ++i)
@@ -449,6 +465,8 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
             write_bf16(p.gate_up + p.I, p.ldg, nw, p.I, width, kSlots / 2);
         }
     }
+    if constexpr (kKind == Fp8Result::kGrad && kStages > 2)
+        load_piece(0);
 #pragma unroll
     for (int j = 0; j < (kKind == Fp8Result::kBf16 ? 0 : kTm); ++j) {
         const int m = wm * kTm * 32 + j * 32 + l32;
@@ -472,18 +490,19 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
                      m, nw, p.q + row * p.I + nw, p.sq + row * p.ldsq + nw / 128);
         } else if constexpr (kKind == Fp8Result::kGrad) {
             // dg stays in registers, du waits in the wave's part of the stages.
-            const uint16_t *gu = p.gate_up + (m0 + min(m, rows - 1)) * p.ldg +
-                                 (nw < p.I ? nw : p.I - kTn * 32) + 8 * half;
             lds_u8 *wait = smem + (wave * kTn * 4 * kWave + lane) * 16;
             float dg[kTn][16], largest_g = 0.f, largest_u = 0.f;
 #pragma unroll
             for (int i = 0; i < kTn; ++i) {
+                const int piece = j * kTn + i;
+                if (piece + kAhead < kTm * kTn)
+                    load_piece(piece + kAhead);
 #pragma unroll
                 for (int g2 = 0; g2 < 2; ++g2) {
                     __builtin_amdgcn_sched_barrier(0);
                     float g[8], u[8];
-                    floats8(*reinterpret_cast<const u32x4 *>(gu + i * 32 + 16 * g2), g);
-                    floats8(*reinterpret_cast<const u32x4 *>(gu + p.I + i * 32 + 16 * g2), u);
+                    floats8(kept[piece % (kAhead + 1)][g2], g);
+                    floats8(kept[piece % (kAhead + 1)][2 + g2], u);
                     v4f du[2];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
