@@ -16,6 +16,12 @@
 // kRaw and kRawF32: the rows come as bf16 or fp32 and every workgroup quantises them itself,
 // into LDS, while its first weights are under way, which saves the quantiser's launch.
 // kCodes: the rows' codes come through the ring, before the weights of their block.
+//
+// Bound by the weights' stream and, before it, the launch and the first bytes' way: one row, K 3840,
+// N 10240 10.0 us (39 MB, 3.9 TB/s; a launch that reads 4 KB takes 2.6), the gated product of I 10240
+// 17.3 (79 MB, 4.6 TB/s), the block's second one, of K 10240 and fp32 rows, 11.6 (39 MB, 3.4 TB/s).  32
+// rows, K and N 3840: 7.9 us.  Workgroups that start at columns of their own, to spread over the
+// memory, took 2 % longer.
 #include <type_traits>
 
 #include "fp8_device.h"

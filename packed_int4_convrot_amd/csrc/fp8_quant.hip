@@ -3,6 +3,11 @@
 //
 // A block's scale is the smallest power of two that keeps its values within 448, so x / s
 // is exact and the code is x's own nearest e4m3 value: one rounding.
+//
+// All are bound by memory: one pass, 16 columns a lane, whole lines either way.  8192 rows of 10240
+// columns take 44 us (252 MB, 5.7 TB/s), 2000 of 2048 5.3, five of 3840 2.6 (a launch); a weight of
+// 20480 x 3840 40 us (236 MB, 5.8 TB/s), its transpose 29 to 35 (157 MB, 4.5 to 5.3 TB/s; LDS bytes
+// are gathered across rows, whose conflicts hide under the loads).
 #include "fp8_device.h"
 #include "fp8_launch.h"
 

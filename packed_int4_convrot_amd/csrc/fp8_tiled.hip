@@ -16,12 +16,15 @@
 // slots of a row are XORed with bits of the row so that the lanes of a fragment's read
 // meet in no bank.
 //
-// What bounds it: on the 256-wide tiles the matrix core under the chip's power, at about 1.6 GHz a
-// step of 256 x 256 takes 1.45 us, 1.2 with its loads left out; 8192 x 3840 x 10240 takes LARGE_US us,
-// LARGE_PF PFLOP/s, and 256 x 256 tiles of four waves, which read a third less LDS, 2 % more.  On the
-// small tiles a step's way through barrier, LDS and two products, 0.24 us for 64 x 64: eight buffers
-// and steps shared out to two or four teams of a workgroup's waves took as long; splitting K over
-// workgroups is what helps.
+// What bounds it.  256 x 256 tiles: the matrix cores, 70 % busy over the whole launch at the 1.8 GHz
+// that power leaves, and the loads beside them (a step of 1.45 us takes 1.2 with its loads left out):
+// 8192 x 10240 x 3840 (rows, K, N) 245 us, 2.6 PFLOP/s, as a large library product here.  Read less
+// LDS (four waves of 128 x 128) it takes 2 % more; a burst of loads ahead, prefetches into the L2,
+// workgroups that go on to a next tile: none gained.  Small tiles: a step's way through barrier, LDS
+// and two products, 0.24 us for 64 x 64.  Eight buffers take as long, and so do steps shared out to
+// teams of a workgroup's waves; splitting K over workgroups is what helps.  kGrad's writing of
+// results: 4096 rows, H 3840, I 10240 take 23 us less without the reads of g and u, 35 without the
+// codes' stores, whatever their order; its tiles fill two and a half rounds of the chip.
 //
 // kGated: a wave's tiles are half gate rows and half up rows of the same columns, so that
 // the activation and the product happen in registers; a workgroup covers the 128
