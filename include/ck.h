@@ -452,7 +452,7 @@ ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, cons
  * below the largest.  How many rows a call has decides which kernel adds them and in what
  * order, so that a row's last bits may differ from one M to another; the same call gives
  * the same bits.  Range: products whose scales add up beyond fp32's exponents overflow or
- * vanish as fp32 does.
+ * vanish as fp32 does, and of a block below 2^-100 small values may count as zeros.
  */
 
 /* ck_fp8_quant: codes and scales of bf16 x [M, ldx], K columns. */

@@ -13,7 +13,6 @@ using namespace ck::api;
 
 // Row strides in bytes: a tile's 256 rows are addressed with 32-bit buffer offsets.
 constexpr int64_t kMaxLd = int64_t(1) << 23;
-// Workgroups of up to 512 threads of one launch.
 
 int check_columns(const char *fn, const char *name, int64_t K, int64_t of = 16)
 {

@@ -74,7 +74,6 @@ struct Tile {
     static constexpr int kScaleSteps = 64, kRowScales = kScaleSteps * kBm;
     static constexpr int kScales = kRowScales + 2 * kScaleSteps;
     static constexpr int kLds = kStages * kStage + kScales + kWaves * 32 * 4;
-    static constexpr int kPerCu = 160 * 1024 / kLds;
 };
 
 template <class T, Fp8Result kKind>

@@ -167,7 +167,8 @@ BLOCKS = [(1, 16, 128), (1, 3840, 384), (2, 144, 128), (5, 272, 256), (16, 512, 
           # few rows: each number of 16-row tiles of either operand, and passes
           (17, 1520, 128), (20, 3840, 4224), (49, 2512, 128), (40, 5008, 4224), (50, 6992, 4224), (16, 5008, 11648),
           (20, 8464, 12288), (1, 16400, 8320), (2, 64, 16640), (1, 16, 24704), (1, 32, 32768),
-          (100, 272, 10240), (300, 512, 5120)]   # the second product's K split
+          (100, 272, 10240), (300, 512, 5120),   # the second product's K split
+          (100, 48, 32768)]                      # the widest
 
 
 def block(M, H, I):
@@ -241,6 +242,15 @@ def test_not_finite_in_a_block_stays_in_its_row(M, bad):
     gate_up[1, 5] = bad                        # one element of the gate
     dx = ck.fp8_ffn_backward(x, gate_up, ffn.transposed())
     assert same(dx[keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 272, 144), (16, 2112, 272), (100, 272, 144), (100, 4112, 144), (1000, 272, 3600)])
+def test_powers_of_two_only_move_the_exponents(M, K, N):
+    x, (wc, ws) = random_rows(M, K, 3, DEV), random_weight(N, K, 4, DEV)
+    want = ck.fp8_linear(x, ck.Fp8Weights(wc, ws))
+    for e in (100, -100):
+        moved = ck.Fp8Weights(wc, (ws.view(torch.uint8).int() - e).to(torch.uint8).view(ck.E8M0))
+        assert same(ck.fp8_linear((x.double() * 2.0 ** e).bfloat16(), moved), want)
 
 
 def test_rows_of_zeros_and_largest_values():
