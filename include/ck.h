@@ -479,7 +479,7 @@ ck_status ck_fp8_gemm(const uint8_t *codes, int64_t ldq, const uint8_t *scales, 
                       const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t N, const uint16_t *bias,
                       uint16_t *out, int64_t ldo, void *stream);
 
-/* Bytes of workspace ck_fp8_linear needs: codes and scales of M rows of K columns and up to 8 MB
+/* Bytes of workspace ck_fp8_linear needs: codes and scales of M rows of K columns and up to 16 MB
  * for the sums of a product that is split over K.  A workspace of some M, K and N serves every
  * call with no more of each.  0 for sizes it refuses. */
 size_t ck_fp8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);

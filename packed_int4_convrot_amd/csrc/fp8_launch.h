@@ -75,21 +75,22 @@ inline int64_t fp8_tiles(int64_t M, int64_t N) { return fp8_blocks(M) * fp8_bloc
 // and with 256 x 256 / 256 x 192 / 256 x 128 / 256 x 64 under the activation, feed-forward blocks (rows,
 // H, I): 77, 2112, 1280 31.4 / 28.7 / 23.5 / 20.1; 2000, 2048, 5120 81.6 / 78.1 / 81.8 / 90.9.
 //
-// kBf16 on the two smallest tiles may split K over `splits` workgroups, each of `each` steps (a
+// kBf16 on the three smallest tiles may split K over `splits` workgroups, each of `each` steps (a
 // multiple of four), whose fp32 sums go through the workspace and a launch that adds them: 1900 ns,
 // and 2.5 for a thousand sums.  Whole / split: 100 x 10240 x 3840 26.4 / 18.2, 100 x 20480 x 3840
-// 47.2 / 25.7, 128 x 8192 x 1024 22.9 / 13.1, 2000 x 20480 x 256 64 / 43, 100 x 3840 x 1040 13.2 / 11.2;
+// 47.2 / 25.7, 128 x 8192 x 1024 22.9 / 13.1, 2000 x 20480 x 256 64 / 43, 100 x 3840 x 1040 13.2 / 11.2,
+// 200 x 20480 x 3840 49.5 / 37.3 on 128 x 64, 34.8 on 128 x 128;
 // 100 x 2112 x 1040 stays whole, 10.0 / 10.6.  Backward pass of 100 rows, H 3840, I 10240: 68.6 / 49.4.
 struct Fp8Plan {
     Fp8Tile tile;
     int64_t splits, each;
     int64_t time;
 };
-constexpr int64_t kFp8MostSplits = 8, kFp8SplitArea = int64_t(kFp8Cus) * 128 * 64;   // elements of all sums
+constexpr int64_t kFp8MostSplits = 8, kFp8SplitArea = int64_t(kFp8Cus) * 128 * 128;   // elements of all sums
 // Floats that a split product's sums need at most.  Fewer rows need no more.
 inline int64_t fp8_split_floats(int64_t M, int64_t K, int64_t N)
 {
-    const int64_t m = M < (1 << 14) ? (M + 63) / 64 * 64 : 1 << 14, n = N < (1 << 15) ? fp8_blocks(N) * 128 : 1 << 15;
+    const int64_t m = M < (1 << 15) ? fp8_blocks(M) * 128 : 1 << 15, n = N < (1 << 15) ? fp8_blocks(N) * 128 : 1 << 15;
     const int64_t most = kFp8MostSplits * m * n;
     return K < 16 * kFp8Block ? 0 : most < kFp8SplitArea ? most : kFp8SplitArea;
 }
@@ -115,7 +116,7 @@ inline Fp8Plan fp8_plan(Fp8Result kind, int64_t M, int64_t K, int64_t columns, b
         const int64_t tiles = (columns * (gated ? 2 : 1) + s.n - 1) / s.n * ((M + s.m - 1) / s.m);
         if (tiles > kFp8MaxTiles)
             continue;
-        const bool splits = may_split && kind == Fp8Result::kBf16 && s.m == 64 && K >= 16 * kFp8Block;
+        const bool splits = may_split && kind == Fp8Result::kBf16 && s.n < 256 && K >= 16 * kFp8Block;
         for (int64_t n = 1; n <= (splits ? kFp8MostSplits : 1) && (n == 1 || n * tiles <= kFp8Cus); ++n) {
             const int64_t each = n == 1 ? steps : ((steps + n - 1) / n + 3) / 4 * 4;
             const int64_t rounds = (tiles + kFp8Cus - 1) / kFp8Cus;

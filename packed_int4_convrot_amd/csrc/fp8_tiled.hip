@@ -428,12 +428,17 @@ __global__ __launch_bounds__(T::kWaves *kWave) void fp8_tiled_kernel(Fp8Product 
     lds_barrier();
 
     if constexpr (kSplit) {
-        static_assert(kTn == 1 && kTm == 1, "one tile a wave");
-        v4f *to = reinterpret_cast<v4f *>(p.sums) +
-                  ((((int64_t)blockIdx.y * tiles + m0 / kBm * tiles_n + n0 / kBn) * kWaves + wave) * 4) * kWave + lane;
+        v4f *to = reinterpret_cast<v4f *>(p.sums) + lane +
+                  (((int64_t)blockIdx.y * tiles + m0 / kBm * tiles_n + n0 / kBn) * kWaves + wave) * kTn * kTm * 4 * kWave;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            to[q * kWave] = v4f{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+        for (int i = 0; i < kTn; ++i)
+#pragma unroll
+            for (int j = 0; j < kTm; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const v16f &x = acc[i][j];
+                    to[((i * kTm + j) * 4 + q) * kWave] = v4f{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                }
         return;
     }
     if (kKind == Fp8Result::kBf16 || (kGated && p.gate_up)) {
@@ -547,9 +552,11 @@ template <class T>
 __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Product p, int splits, int tiles, int tiles_n)
 {
     const int lane = threadIdx.x % kWave, l32 = lane % 32, half = lane / 32;
-    const int w = blockIdx.x * 4 + threadIdx.x / kWave, tile = w / T::kWaves, wave = w % T::kWaves;
-    const int64_t m = (int64_t)(tile / tiles_n) * T::kBm + wave % T::kWm * 32 + l32;
-    const int n = tile % tiles_n * T::kBn + wave / T::kWm * 32;
+    constexpr int kEach = T::kTn * T::kTm;   // of a wave's; kEach * kWaves of a workgroup's
+    const int w = blockIdx.x * 4 + threadIdx.x / kWave, tile = w / (kEach * T::kWaves);
+    const int wave = w / kEach % T::kWaves, i = w % kEach / T::kTm, j = w % T::kTm;
+    const int64_t m = (int64_t)(tile / tiles_n) * T::kBm + (wave % T::kWm * T::kTm + j) * 32 + l32;
+    const int n = tile % tiles_n * T::kBn + (wave / T::kWm * T::kTn + i) * 32;
     const v4f *from = reinterpret_cast<const v4f *>(p.sums) + (int64_t)w * 4 * kWave + lane;
     float s[16];
 #pragma unroll
@@ -559,7 +566,7 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Product p, int splits,
     for (int z = 0; z < splits; ++z)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const v4f x = from[((int64_t)z * tiles * T::kWaves * 4 + q) * kWave];
+            const v4f x = from[((int64_t)z * tiles * T::kWaves * kEach * 4 + q) * kWave];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 s[4 * q + r] += x[r];
@@ -596,14 +603,15 @@ int launch_tile(const Fp8Product &p, int64_t splits, void *stream)
     if constexpr (kKind == Fp8Result::kSums) {
         if (e != 0)
             return e;
-        hipLaunchKernelGGL(fp8_join_kernel<T>, dim3((unsigned)(tiles * T::kWaves / 4)), dim3(256), 0,
+        hipLaunchKernelGGL(fp8_join_kernel<T>, dim3((unsigned)(tiles * T::kWaves * T::kTn * T::kTm / 4)),
+                           dim3(256), 0,
                            reinterpret_cast<hipStream_t>(stream), p, (int)splits, (int)tiles, (int)(tiles / tiles_m));
         return (int)hipGetLastError();
     }
     return e;
 }
 
-// The two smallest tiles, split or not.
+// The three smallest tiles, split or not.
 template <class T>
 int launch_small(const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream)
 {
@@ -631,8 +639,10 @@ int launch_kind(const Fp8Product &p, const Fp8Plan &plan, float *sums, void *str
             return launch_tile<Tile<4, 2, 2, 1>, kKind>(p, 1, stream);
         break;
     case Fp8Tile::k128x128:
-        if constexpr (!kGated)
+        if constexpr (kGrad)
             return launch_tile<Tile<2, 4, 2, 1, 4>, kKind>(p, 1, stream);
+        else if constexpr (!kGated)
+            return launch_small<Tile<2, 4, 2, 1, 4>>(p, plan, sums, stream);
         break;
     case Fp8Tile::k128x64:
         if constexpr (kGrad)

@@ -134,9 +134,9 @@ int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, const Fp8Plan &plan, f
     if (plan.splits > 1) {   // a tile's sums are written whole
         EXPECT(kind == Fp8Result::kBf16 && sums != nullptr && plan.splits <= kFp8MostSplits && plan.each % 4 == 0);
         EXPECT((plan.splits - 1) * plan.each < fp8_blocks(p.K) && plan.splits * plan.each >= fp8_blocks(p.K));
-        EXPECT(plan.tile == Fp8Tile::k128x64 || plan.tile == Fp8Tile::k64x64);
-        const int64_t n = plan.tile == Fp8Tile::k128x64 ? 128 : 64;
-        const int64_t floats = plan.splits * ((p.N + n - 1) / n * n) * ((p.M + 63) / 64 * 64);
+        EXPECT(plan.tile == Fp8Tile::k128x128 || plan.tile == Fp8Tile::k128x64 || plan.tile == Fp8Tile::k64x64);
+        const int64_t n = plan.tile == Fp8Tile::k64x64 ? 64 : 128, m = plan.tile == Fp8Tile::k128x128 ? 128 : 64;
+        const int64_t floats = plan.splits * ((p.N + n - 1) / n * n) * ((p.M + m - 1) / m * m);
         EXPECT(floats <= fp8_split_floats(p.M, p.K, p.N));
         write_span(sums, 1, floats, floats, 4);
     }
@@ -298,8 +298,8 @@ void tiles()
                 EXPECT(ck::fp8_split_floats(M, K, N) >= room);
                 room = ck::fp8_split_floats(M, K, N);
                 const ck::Fp8Plan plan = ck::fp8_plan(ck::Fp8Result::kBf16, M, K, N, true);
-                const int64_t n = plan.tile == ck::Fp8Tile::k128x64 ? 128 : 64;
-                EXPECT(plan.splits == 1 || plan.splits * ((N + n - 1) / n * n) * ((M + 63) / 64 * 64) <= room);
+                const int64_t n = plan.tile == ck::Fp8Tile::k64x64 ? 64 : 128, m = plan.tile == ck::Fp8Tile::k128x128 ? 128 : 64;
+                EXPECT(plan.splits == 1 || plan.splits * ((N + n - 1) / n * n) * ((M + m - 1) / m * m) <= room);
             }
         }
     for (int kind = 0; kind < 3; ++kind)
