@@ -87,10 +87,12 @@ struct Fp8Plan {
     int64_t time;
 };
 constexpr int64_t kFp8MostSplits = 8, kFp8SplitArea = int64_t(kFp8Cus) * 128 * 128;   // elements of all sums
-// Floats that a split product's sums need at most.  Fewer rows need no more.
+// Floats that a split product's sums need at most (up to 64 rows take no 128 x 128 tiles).  Fewer
+// rows need no more.
 inline int64_t fp8_split_floats(int64_t M, int64_t K, int64_t N)
 {
-    const int64_t m = M < (1 << 15) ? fp8_blocks(M) * 128 : 1 << 15, n = N < (1 << 15) ? fp8_blocks(N) * 128 : 1 << 15;
+    const int64_t m = M <= 64 ? 64 : M < (1 << 15) ? fp8_blocks(M) * 128 : 1 << 15;
+    const int64_t n = N < (1 << 15) ? fp8_blocks(N) * 128 : 1 << 15;
     const int64_t most = kFp8MostSplits * m * n;
     return K < 16 * kFp8Block ? 0 : most < kFp8SplitArea ? most : kFp8SplitArea;
 }
