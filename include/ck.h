@@ -445,8 +445,11 @@ ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, cons
  *
  * Quantised, a block of largest absolute value a has the smallest scale s >= 2^-127
  * with a <= 448 s (1 for a block of zeros), and a code is e4m3(x / s), nearest even,
- * ties to even: x / s is exact, so this is the only rounding.  A block that holds a
- * NaN or an infinity gives NaN in every result of its row (of its columns, in a weight).
+ * ties to even: x / s is exact, so this is the only rounding.  A block of activations
+ * that holds a NaN or an infinity gives NaN in every result of its row.  Such a block of a
+ * weight has the scale NaN (byte 255), and so every output that the block has a part in
+ * is NaN, of the transposed weight too; of codes made elsewhere, a NaN code is so for its
+ * own row of the weight alone.
  * Sums are fp32, rounded once to the result's type; the e4m3 matrix core, which serves all
  * but a few rows, adds eight neighbouring products at a time and drops what lies 2^-13
  * below the largest.  How many rows a call has decides which kernel adds them and in what

@@ -35,7 +35,7 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t buffer, __attri
 }
 
 // e8m0 byte of the smallest power of two s >= 2^-127 with amax <= 448 s, 127 (1.0) for
-// amax = 0; 255 (NaN) where amax is infinite.  448 = 1.75 * 2^8: the exponent of
+// amax = 0; 255 (NaN) where amax is not finite.  448 = 1.75 * 2^8: the exponent of
 // amax less 8, one more where its mantissa is above 1.75.
 __device__ __forceinline__ uint32_t e8m0_of(float amax)
 {

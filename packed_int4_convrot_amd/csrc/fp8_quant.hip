@@ -28,6 +28,16 @@ __device__ __forceinline__ float abs_max16(const float (&v)[16])
     return a;
 }
 
+// The same by the values' bits, in which a NaN is above all others (fmaxf leaves it out).
+__device__ __forceinline__ uint32_t abs_max16_bits(const float (&v)[16])
+{
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+    return a;
+}
+
 __device__ __forceinline__ u32x4 codes16(const float (&v)[16], float scale)
 {
     u32x4 r;
@@ -94,16 +104,18 @@ __global__ __launch_bounds__(kThreads) void fp8_quant_kernel(const void *__restr
     }
 }
 
-// One 128 x 128 block a workgroup: a thread holds 16 columns of four rows.
+// One 128 x 128 block a workgroup: a thread holds 16 columns of four rows.  A NaN gives the block the
+// scale NaN, as an infinity does: a row of activations is spoiled by its NaN code alone, but here the
+// block's other outputs would stay finite.
 __global__ __launch_bounds__(kThreads) void fp8_weight_kernel(const uint16_t *__restrict__ w, int N, int K,
                                                               int64_t ldw_in, uint8_t *__restrict__ codes, int64_t ldw,
                                                               uint8_t *__restrict__ scales)
 {
-    __shared__ float part[kThreads / kWave];
+    __shared__ uint32_t part[kThreads / kWave];
     const int bn = blockIdx.y, bk = blockIdx.x;
     const int k = bk * kFp8Block + threadIdx.x % 8 * kLaneColumns;
     float v[4][16];
-    float a = 0.f;
+    uint32_t a = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = bn * kFp8Block + i * 32 + threadIdx.x / 8;
@@ -114,16 +126,16 @@ __global__ __launch_bounds__(kThreads) void fp8_weight_kernel(const uint16_t *__
             for (int j = 0; j < 16; ++j)
                 v[i][j] = 0.f;
         }
-        a = fmaxf(a, abs_max16(v[i]));
+        a = max(a, abs_max16_bits(v[i]));
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1)
-        a = fmaxf(a, __shfl_xor(a, d));
+        a = max(a, (uint32_t)__shfl_xor((int)a, d));
     if (threadIdx.x % kWave == 0)
         part[threadIdx.x / kWave] = a;
     __syncthreads();
-    a = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const uint32_t s = e8m0_of(a);
+    a = max(max(part[0], part[1]), max(part[2], part[3]));
+    const uint32_t s = e8m0_of(__uint_as_float(a));
     const float by = e8m0_value(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
