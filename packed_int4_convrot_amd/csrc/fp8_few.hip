@@ -77,11 +77,8 @@ __device__ __forceinline__ Values values32(u32x4 x, u32x4 y, uint32_t scale)
     return Values{{values8(x[0], x[1], s), values8(x[2], x[3], s), values8(y[0], y[1], s), values8(y[2], y[3], s)}};
 }
 
-// Column tiles that one pass takes at most.  Codes take one pass: wider results are the tiled
-// product's (fp8_few).
 template <Source kSource, Fp8Result kKind, int kMt>
-constexpr int kMostTiles = kSource == Source::kCodes ? (int)(fp8_few_columns(kKind, kMt) / kFp8Cus / 16)
-                                                     : 8 / (kKind == Fp8Result::kGated ? 2 : 1);
+constexpr int kMostTiles = fp8_few_most_tiles(kSource != Source::kCodes, kKind, kMt);
 
 // kMt: 16-row tiles of activations; kT: 16-row tiles of weights a pass (half gate and half
 // up, for kGated).
@@ -378,14 +375,11 @@ template <Source kSource, Fp8Result kKind, int kMt>
 int launch_shape(const Fp8Product &p, const void *x, int64_t ldx, float *sums, void *stream)
 {
     constexpr int kPair = kKind == Fp8Result::kGated ? 2 : 1;
-    constexpr int kMost = kMostTiles<kSource, kKind, kMt>;
-    const int cols = kKind == Fp8Result::kBf16 ? p.N : p.I;
-    const int per = (cols + kFp8Cus - 1) / kFp8Cus, grid = (cols + per - 1) / per;
-    const int tiles = (per + 15) / 16, passes = (tiles + kMost - 1) / kMost, each = (tiles + passes - 1) / passes;
+    const Fp8FewRun run = fp8_few_run(kSource != Source::kCodes, kKind, kMt, kKind == Fp8Result::kBf16 ? p.N : p.I);
 #define CK_FP8_FEW(T)                                                                                  \
-    if constexpr (T <= kMost)                                                                          \
-        if (each <= T)                                                                                 \
-    return launch_one<kSource, kKind, kMt, T * kPair>(p, x, ldx, sums, grid, per, passes, stream)
+    if constexpr (T <= kMostTiles<kSource, kKind, kMt>)                                                \
+        if (run.tiles == T)                                                                            \
+    return launch_one<kSource, kKind, kMt, T * kPair>(p, x, ldx, sums, run.grid, run.per, run.passes, stream)
     CK_FP8_FEW(1);
     CK_FP8_FEW(2);
     CK_FP8_FEW(3);

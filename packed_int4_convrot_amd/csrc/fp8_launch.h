@@ -161,6 +161,23 @@ inline bool fp8_few(Fp8Result kind, int64_t M, int64_t K, int64_t columns, const
     const int64_t from_memory = 3200 + K * weights / 3300;
     return few < (plan.time > from_memory ? plan.time : from_memory);
 }
+// 16-row tiles of weights (of gate, and as many of up) that one of its passes takes at most.  Codes take
+// one pass: wider results are the tiled product's.
+constexpr int fp8_few_most_tiles(bool raw, Fp8Result kind, int64_t rows16)
+{
+    return raw ? 8 / (kind == Fp8Result::kGated ? 2 : 1) : (int)(fp8_few_columns(kind, rows16) / kFp8Cus / 16);
+}
+// An equal run of columns for each workgroup, in equal passes; a kernel of 1, 2, 3, 4, 6 or 8 tiles a pass.
+struct Fp8FewRun {
+    int per, grid, passes, tiles;
+};
+inline Fp8FewRun fp8_few_run(bool raw, Fp8Result kind, int64_t rows16, int64_t columns)
+{
+    const int per = (int)((columns + kFp8Cus - 1) / kFp8Cus), grid = (int)((columns + per - 1) / per);
+    const int tiles = (per + 15) / 16, most = fp8_few_most_tiles(raw, kind, rows16);
+    const int passes = (tiles + most - 1) / most, each = (tiles + passes - 1) / passes;
+    return {per, grid, passes, each + (each == 5 || each == 7)};
+}
 int launch_fp8_few(Fp8Result kind, const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums,
                    void *stream);
 
