@@ -393,9 +393,13 @@ int launch_shape(const Fp8Product &p, const void *x, int64_t ldx, float *sums, v
 template <Fp8Result kKind>
 int launch_kind(const Fp8Product &p, const void *x, bool f32, int64_t ldx, float *sums, void *stream)
 {
+    if (x && f32) {   // what lies between a block's two products
+        if constexpr (kKind == Fp8Result::kBf16)
+            return launch_shape<Source::kRawF32, kKind, 1>(p, x, ldx, sums, stream);
+        return (int)hipErrorInvalidValue;
+    }
     if (x)
-        return f32 ? launch_shape<Source::kRawF32, kKind, 1>(p, x, ldx, sums, stream)
-                   : launch_shape<Source::kRaw, kKind, 1>(p, x, ldx, sums, stream);
+        return launch_shape<Source::kRaw, kKind, 1>(p, x, ldx, sums, stream);
     if (p.M <= 16)
         return launch_shape<Source::kCodes, kKind, 1>(p, x, ldx, sums, stream);
     if (p.M <= 32)

@@ -132,8 +132,8 @@ inline Fp8Plan fp8_plan(Fp8Result kind, int64_t M, int64_t K, int64_t columns, b
 }
 int launch_fp8_tiled(Fp8Result kind, const Fp8Product &p, const Fp8Plan &plan, float *sums, void *stream);
 
-// The few-row product.  x given: bf16 or fp32 rows, quantised on the way (fp8_few_raw), a and sa
-// unused; null: the codes and scales.  kGated and kGrad write fp32 [M, I] or [M, 2 I] to sums.
+// The few-row product.  x given: bf16 rows, or fp32 ones for kBf16, quantised on the way (fp8_few_raw),
+// a and sa unused; null: the codes and scales.  kGated and kGrad write fp32 [M, I] or [M, 2 I] to sums.
 constexpr int64_t kFp8FewRows = 64;
 constexpr int kFp8RawRows = 8, kFp8RawBytes = 16 * 1024;
 inline bool fp8_few_raw(int64_t M, int64_t K) { return M <= kFp8RawRows && M * (fp8_blocks(K) * 128) <= kFp8RawBytes; }

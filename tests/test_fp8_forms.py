@@ -3,6 +3,7 @@ kernels that any call can come to (no GPU): the entry points run against stand-i
 (sanitize/fp8_forms.cpp), once for the lists of shapes and once over all sizes, so that a cost or a
 limit changed in fp8_launch.h cannot leave a form unchecked."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -10,6 +11,7 @@ import pytest
 
 import test_fp8_forms_gpu as more
 import test_fp8_gpu as first
+from test_resource_usage import _report
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SAN = os.path.join(ROOT, "tests", "sanitize")
@@ -51,3 +53,22 @@ def test_the_gpu_tests_check_every_form(forms, reachable):
     missing = {f: call for f, call in reachable.items() if f not in checked}
     assert not missing, missing
     assert len(reachable) > 60
+
+
+def test_no_kernel_is_compiled_that_no_call_reaches(reachable):
+    """The kernels in the build's report, by their template arguments."""
+    kinds, compiled = ("bf16", "gated", "grad", "sums"), set()
+    for k in _report()["kernels"]:
+        few = re.search(r"fp8_few_kernelILNS0_6SourceE(\d)ELNS_9Fp8ResultE(\d)ELi(\d)ELi(\d+)E", k["kernel"])
+        tiled = re.search(r"fp8_tiled_kernelINS0_4TileI(?:Li(\d)E)(?:Li(\d)E)(?:Li(\d)E)(?:Li(\d)E)Li\dEEELNS_9Fp8ResultE(\d)E",
+                          k["kernel"])
+        if few:
+            source, kind, rows16, tiles = map(int, few.groups())
+            compiled.add("few %s %s %d %d" % (("codes", "raw", "fp32")[source], kinds[kind], rows16,
+                                              tiles // (2 if kinds[kind] == "gated" else 1)))
+        elif tiled:
+            wn, wm, tn, tm, kind = map(int, tiled.groups())
+            compiled.add("tiled %dx%d %s" % (32 * wn * tn, 32 * wm * tm, kinds[kind]))
+        else:
+            assert "fp8_few" not in k["kernel"] and "fp8_tiled" not in k["kernel"], k["kernel"]
+    assert compiled == {f.replace(" passes", "").replace(" runs", "") for f in reachable}
