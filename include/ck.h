@@ -455,7 +455,8 @@ ck_status ck_lora_add(const uint16_t *x, int64_t M, int64_t K, int64_t ldx, cons
  * below the largest.  How many rows a call has decides which kernel adds them and in what
  * order, so that a row's last bits may differ from one M to another; the same call gives
  * the same bits.  Range: products whose scales add up beyond fp32's exponents overflow or
- * vanish as fp32 does, and of a block below 2^-100 small values may count as zeros.
+ * vanish as fp32 does; a code that stands for 2^128 or more (as |x| of 1.9375 * 2^127 and
+ * above rounds to) may count as infinite, and of a block below 2^-100 small values as zeros.
  */
 
 /* ck_fp8_quant: codes and scales of bf16 x [M, ldx], K columns. */

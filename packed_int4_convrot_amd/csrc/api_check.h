@@ -1,5 +1,5 @@
-// Argument checks shared by the host files of the C ABI (ck_api.cpp and
-// ck_rows_api.cpp).  Plain host C++ without HIP calls, allocations or exceptions:
+// Argument checks shared by the host files of the C ABI (ck_api.cpp,
+// ck_rows_api.cpp and ck_fp8_api.cpp).  Plain host C++ without HIP calls, allocations or exceptions:
 // a failed check writes the thread's error message and returns a status.
 #pragma once
 

@@ -9,9 +9,9 @@
 // the 16-byte slots of a row are XORed with bits of the row, as in the tiled product.
 //
 // The products run on the 16 x 16 x 32 bf16 MFMA: an e4m3 code times its block's power of
-// two is a bf16 value, so both operands are exact and the sums are fp32's.  (The e4m3
-// MFMA aligns eight products at a time and drops what is 2^-13 below the largest; here it
-// would save nothing, since the weights' bytes are what takes the time.)
+// two is a bf16 value (an infinity from 2^128 on), so both operands are exact and the sums are
+// fp32's.  (The e4m3 MFMA aligns eight products at a time and drops what is 2^-13 below the
+// largest; here it would save nothing, since the weights' bytes are what takes the time.)
 //
 // kRaw and kRawF32: the rows come as bf16 or fp32 and every workgroup quantises them itself,
 // into LDS, while its first weights are under way, which saves the quantiser's launch.

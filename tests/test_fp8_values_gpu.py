@@ -1,8 +1,9 @@
-"""What is not finite in the 8-bit float operators' weights and gates."""
+"""What is not finite, and what is nearly so, in the 8-bit float operators' weights, rows and gates."""
 import pytest
 import torch
 
-from fp8_bounds import random_rows, random_weight
+import fp8_bounds as ref
+from fp8_bounds import random_rows, random_weight, refused
 from test_fp8_gpu import DEV, NAN, bits, block, ck, same
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,15 @@ def test_a_gate_or_up_that_is_not_finite_spoils_its_row(M, bad, column):
     gate_up[0, column] = bad
     dx = ck.fp8_ffn_backward(x, gate_up, back)
     assert clean.isfinite().all() and dx[0].isnan().all() and same(dx[1:], clean[1:])
+
+
+@pytest.mark.parametrize("M,K", ROWS)
+def test_the_largest_rows_whose_codes_stay_below_2_to_128(M, K):
+    """x up to 1.9296875 2^127, whose code stands for 1.875 2^127 (from 1.9375 2^127 on it would be 2^128),
+    against weights whose products are of ordinary size."""
+    x, (codes, scales) = random_rows(M, K, 5, DEV), random_weight(144, K, 6, DEV)
+    x = (x.sign() * torch.full_like(x, 1.9296875) * 2.0 ** 127).bfloat16()
+    small = (scales.view(torch.uint8).int() - 100).to(torch.uint8).view(ck.E8M0)
+    want = ref.linear(x.double(), ref.weight(codes, small))
+    for out in linears(x, codes, small):
+        assert out.isfinite().all() and refused(out, *want) is None
