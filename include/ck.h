@@ -478,6 +478,9 @@ ck_status ck_fp8_transpose_weights(const uint8_t *codes, int64_t ldw, const uint
  *   out[m, n] = sum_b 2^(sa[m, b] + sw[n / 128, b] - 254) sum_{k in b} a[m, k] w[n, k] (+ bias[n])
  * for activations that are already quantised, bias bf16 [N] or NULL, out bf16 [M, ldo].
  * The backward pass of the linear, to its input, is the linear of the transposed weight.
+ * It has no workspace, so it never splits a sum over K: of some 100 to 200 rows and K from
+ * 8192 or so on ck_fp8_linear, which does, is the faster one although it quantises as well
+ * (100 rows, K 20480, N 3840: 25 us against 44; 128 rows, K 8192, N 1024: 13 against 19).
  */
 ck_status ck_fp8_gemm(const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds, int64_t M, int64_t K,
                       const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t N, const uint16_t *bias,

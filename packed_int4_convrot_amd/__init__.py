@@ -787,7 +787,9 @@ def _fp8_result(out, name, M, N, device):
 
 
 def fp8_gemm(codes, scales, weights: Fp8Weights, bias=None, out=None):
-    """bf16 [M, N] of quantised activations (fp8_quant, fp8_empty) and a weight, plus bias bf16 [N]."""
+    """bf16 [M, N] of quantised activations and a weight, plus bias bf16 [N].  Rows of scales lie a
+    multiple of four bytes apart, as fp8_quant and fp8_empty lay them out (.contiguous() undoes it).
+    K is not split over workgroups, as fp8_linear does where rows are some hundred and K is long."""
     M, dev = _row_count(codes, "codes"), weights.device
     ldq = _rows(codes, "codes", E4M3, dev, (M, weights.K))
     lds = _fp8_scales(scales, M, weights.K, dev)

@@ -81,6 +81,11 @@ inline int64_t fp8_tiles(int64_t M, int64_t N) { return fp8_blocks(M) * fp8_bloc
 // 47.2 / 25.7, 128 x 8192 x 1024 22.9 / 13.1, 2000 x 20480 x 256 64 / 43, 100 x 3840 x 1040 13.2 / 11.2,
 // 200 x 20480 x 3840 49.5 / 37.3 on 128 x 64, 34.8 on 128 x 128;
 // 100 x 2112 x 1040 stays whole, 10.0 / 10.6.  Backward pass of 100 rows, H 3840, I 10240: 68.6 / 49.4.
+//
+// The lines are of tiles on a part of the chip, weights in a cache.  With nearly all CUs at work they
+// fall short of the time: 300 x 3840 x 10240 15.8 us where the product takes 18.2 (20.5 with weights from
+// memory), 1000 x 3840 x 3840 15.8 of 19.7 (21.6), 2000 x 5120 x 2048 20.0 of 25.1 (28.3), all on 128 x 128
+// tiles.  The table's times, not these sums, say which tile is the faster one there.
 struct Fp8Plan {
     Fp8Tile tile;
     int64_t splits, each;
